@@ -21,6 +21,12 @@ E4M3 = torch.float8_e4m3fn
 TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
+def _scale(amax):
+    """amax / 448 as the IEEE quotient (a division by a Python number may multiply by its
+    reciprocal instead, which moves values that lie midway between two codes); 1 for zeros."""
+    return torch.where(amax == 0, torch.ones_like(amax), amax / torch.full_like(amax, 448.0))
+
+
 # ---------------------------------------------------------------------------------------------
 # the cases
 # ---------------------------------------------------------------------------------------------
@@ -119,7 +125,7 @@ def _row_codes(x):
     m, c = x.shape
     v = x.float().view(m, c // 128, 128)
     a = v.abs().amax(2)
-    s = torch.where(a == 0, torch.ones_like(a), a / 448.0)
+    s = _scale(a)
     return (v / s[:, :, None]).clamp(-448, 448).to(E4M3).view(m, c), s
 
 
@@ -131,7 +137,7 @@ def _block_codes(w):
     v[:n] = w
     v = v.view(nb, 128, c // 128, 128)
     a = v.abs().amax((1, 3))
-    s = torch.where(a == 0, torch.ones_like(a), a / 448.0)
+    s = _scale(a)
     q = (v / s[:, None, :, None]).clamp(-448, 448).to(E4M3).view(nb * 128, c)
     return q[:n].contiguous(), s
 
@@ -289,7 +295,7 @@ def _quantize_cols(x):
     v[:m] = x
     v = v.t().contiguous().view(c, -1, 128)
     a = v.abs().amax(2)
-    s = torch.where(a == 0, torch.ones_like(a), a / 448.0)
+    s = _scale(a)
     return (v / s[:, :, None]).clamp(-448, 448).to(E4M3).view(c, -1), s
 
 
@@ -409,9 +415,10 @@ def _exact_cols(x):
     v = torch.zeros((c, groups * 128), dtype=torch.float32, device=x.device)
     v[:, :m] = x.float().t()
     v = v.view(c, groups, 128)
-    amax = v.abs().max(2)[0]
-    s = torch.where(amax > 0, amax / 448.0, torch.ones_like(amax))
-    q = _e4m3_nearest((v / s.unsqueeze(2)).double())
+    amax = v.double().abs().max(2)[0]
+    # fp32 quotients: a 64-bit one rounded to fp32 is the same value
+    s = torch.where(amax > 0, amax / torch.full_like(amax, 448.0), torch.ones_like(amax)).float()
+    q = _e4m3_nearest((v.double() / s.double().unsqueeze(2)).float().double())
     return q.view(c, -1), s.double()
 
 
