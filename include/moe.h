@@ -15,6 +15,18 @@
  * plus moe_quantize_rows_e4m3 (the fp8 workload's activation quantisation) and
  * moe_forward, which runs the whole chain in a caller-provided workspace.
  *
+ * Around it, for expert products of the caller's own (other widths, other experts' ranks) and
+ * for training:
+ *   moe_permute            token rows gathered into the padded expert-sorted order
+ *   moe_unpermute          expert-sorted rows back in token order, added with the routing
+ *                          weights; without weights: the gradient of moe_permute
+ *   moe_unpermute_bwd      gradient of moe_unpermute (rows and routing weights)
+ *   moe_route_bwd          gradient of moe_route (routing weights to logits)
+ *   moe_gemm_e4m3          product of e4m3 codes with one scale per 128 values (a shared
+ *                          expert, a dense projection, their gradients)
+ *   moe_grouped_gemm_e4m3  the same over expert-sorted rows
+ *   moe_quantize_cols_e4m3 transposed quantisation, the operands of a weight gradient
+ *
  * Conventions shared by every entry point
  *   - Pointers named as tensors are DEVICE pointers owned by the caller; the
  *     library never allocates, frees or synchronises.  All work is enqueued on
@@ -304,6 +316,144 @@ int64_t moe_gemm_workspace_bytes(const moe_problem* p);
  */
 int moe_combine(const moe_problem* p, const void* slot_out, const int32_t* slot_row, void* out,
                 void* stream);
+
+/*
+ * moe_permute -- token rows in expert-sorted order (the gather that moe_grouped_gemm_up fuses,
+ * as rows in memory).
+ * ("MOE Bmm1 Fused Gather": load_activations, gather index = slot // top_k, masked rows zero.)
+ *   rows[r, :] = x[sorted_slots[r] / top_k, :]   for every row r of a valid tile that holds a slot
+ * Rows of valid tiles that hold no slot are zeros (their scales 1); rows past the last valid tile
+ * are left untouched.
+ * Of the problem only its sizes count (T, H, E, top_k, block_m); row_dtype is the type of the
+ * rows: MOE_F32, MOE_BF16 or MOE_E4M3 (codes, one byte; MOE_ERR_DTYPE otherwise).
+ * In:  x        row_dtype [T,H];  x_scales: MOE_E4M3 only, fp32 [T,H/128] (H a multiple of 128,
+ *               MOE_ERR_SHAPE otherwise), or NULL: the codes have no scales per row
+ *      slot_row, sorted_slots, num_tiles: outputs of moe_align for the same problem
+ * Out: rows     row_dtype [moe_max_padded_slots, H];  row_scales fp32
+ *               [moe_max_padded_slots, H/128], given exactly when x_scales is (MOE_ERR_NULL)
+ */
+int moe_permute(const moe_problem* p, int32_t row_dtype, const void* x, const float* x_scales,
+                const int32_t* slot_row, const int32_t* sorted_slots, const int32_t* num_tiles,
+                void* rows, float* row_scales, void* stream);
+
+/*
+ * moe_unpermute -- expert-sorted rows back in token order, weighted and added.
+ * ("factor_moe_fused_gemm.cu": weighted_scatter_add_kernel / index_add_ of the slow path.)
+ *   out[t, :] = round( sum over j = 0..top_k-1 in ascending order of
+ *                      topk_weights[t, j] * rows[slot_row[t*top_k+j], :] )
+ * with the sum carried in fp32 and rounded once; slots with slot_row[s] < 0 (excluded ids) are
+ * skipped, whatever their weight.  topk_weights NULL: every weight is 1, which is the gradient of
+ * moe_permute with respect to x (rows = d_rows, out = d_x).  Deterministic, no atomics.
+ * row_dtype: MOE_F32 or MOE_BF16 (rows and out).
+ * In:  rows row_dtype [moe_max_padded_slots, H]; slot_row int32 [N]; topk_weights fp32 [T,top_k]
+ * Out: out  row_dtype [T, H]
+ */
+int moe_unpermute(const moe_problem* p, int32_t row_dtype, const void* rows,
+                  const int32_t* slot_row, const float* topk_weights, void* out, void* stream);
+
+/*
+ * moe_unpermute_bwd -- gradient of moe_unpermute.
+ * For every slot s = t*top_k+j with r = slot_row[s] >= 0:
+ *   d_rows[r, :]    = round( topk_weights[s] * d_out[t, :] )
+ *   d_weights[t, j] = d_out[t, :] . rows[r, :]            (fp32, a fixed order of additions)
+ * d_weights of excluded slots is 0.  Rows of d_rows in valid tiles that hold no slot are zeros;
+ * rows past the last valid tile are left untouched.  Either output may be NULL (not both);
+ * rows is read for d_weights only and may be NULL without it.  The outputs must not overlap the
+ * inputs.  topk_weights NULL: every weight is 1.
+ * row_dtype: MOE_F32 or MOE_BF16 (d_out, rows and d_rows).
+ * In:  d_out row_dtype [T,H]; rows row_dtype [moe_max_padded_slots, H]; slot_row, sorted_slots,
+ *      num_tiles: outputs of moe_align for the same problem; topk_weights fp32 [T,top_k]
+ * Out: d_rows row_dtype [moe_max_padded_slots, H]; d_weights fp32 [T,top_k]
+ */
+int moe_unpermute_bwd(const moe_problem* p, int32_t row_dtype, const void* d_out,
+                      const void* rows, const int32_t* slot_row, const int32_t* sorted_slots,
+                      const int32_t* num_tiles, const float* topk_weights, void* d_rows,
+                      float* d_weights, void* stream);
+
+/*
+ * moe_route_bwd -- gradient of moe_route's weights with respect to the logits.
+ * With p = softmax(logits[t, :]), c_j = topk_ids[t, j], w the weights that moe_route gives for
+ * the same `renormalize` and G = sum_j w_j * d_weights[t, j]:
+ *   renormalize == 0:  d_logits[t, e] = sum over j with c_j = e of w_j d_weights[t, j] - p_e G
+ *   renormalize != 0:  d_logits[t, e] = sum over j with c_j = e of w_j (d_weights[t, j] - G)
+ * (0 for experts that were not chosen).  All in fp32.  The choice of the experts itself has no
+ * gradient.  Slots whose id is outside [0,E) add nothing and their d_weights is not used.
+ * In:  logits fp32 [T,E], finite; topk_ids int32 [T,top_k]; d_weights fp32 [T,top_k]
+ * Out: d_logits fp32 [T,E], every element written.
+ * Needs top_k <= 64 (MOE_ERR_SHAPE otherwise).  Deterministic.
+ */
+int moe_route_bwd(const moe_problem* p, const float* logits, int renormalize,
+                  const int32_t* topk_ids, const float* d_weights, float* d_logits, void* stream);
+
+/*
+ * moe_quantize_cols_e4m3 -- transposed quantisation: e4m3 codes with one scale per (column,
+ * group of 128 rows), the operand of a product that sums over the rows (a weight gradient).
+ * For each column c and rows group g of x (bf16 [m, n]), with mp = m rounded up to 128 and rows
+ * m..mp-1 taken as zeros:
+ *   scales[c, g] = amax|x[g-group, c]| / 448 in fp32 (1 if the group is all zero),
+ *   xq[c, i]     = e4m3(x[i, c] / scales[c, i/128]), IEEE fp32 quotient, nearest even.
+ * NaN stays NaN; a group that holds an infinity has an infinite scale (its values come back as
+ * NaN).
+ * Needs m >= 1, n a positive multiple of 8, m and n at most 2^22 and
+ * ceil(m/128) * ceil(n/64) < 2^24 (MOE_ERR_SHAPE otherwise).
+ * Out: xq uint8 [n, mp] (e4m3 codes), scales fp32 [n, mp/128].
+ */
+int moe_quantize_cols_e4m3(int32_t m, int32_t n, const void* x, uint8_t* xq, float* scales,
+                           void* stream);
+
+/*
+ * moe_gemm_e4m3 -- product of e4m3 codes with one scale per 128 values along k.
+ *   c[i, j] = sum over groups g of 128 along k, ascending, of
+ *             a_scales[i, g] * b_scales[., g] * ( a[i, g-group] . b[j, g-group] )
+ * accumulated in fp32 and rounded once to c_dtype (MOE_F32 or MOE_BF16).
+ * b_block says what a scale of b covers: 128: a block of 128 rows (b_scales [ceil(n/128), k/128],
+ * the layout of the layer's e4m3 weights); 1: one row (b_scales [n, k/128], the layout of
+ * moe_quantize_rows_e4m3 and moe_quantize_cols_e4m3).
+ * The three products of a projection y[m, n] = x[m, k] w[n, k]^T:
+ *   y    a = x by rows,              b = w, b_block 128
+ *   d_x  a = d_y by rows,            b = w transposed (codes [k, n], scales [k/128, n/128])
+ *   d_w  a = d_y by columns [n, mp], b = x by columns [k, mp], b_block 1
+ * Needs m, n >= 1; k a positive multiple of 128, at most 2^22; m and n at most 2^24; and
+ * ceil(m/16) * ceil(n/16) <= 2^30 (MOE_ERR_SHAPE otherwise).
+ * In:  a uint8 [m, k] (e4m3 codes), a_scales fp32 [m, k/128]; b uint8 [n, k], b_scales
+ * Out: c c_dtype [m, n]
+ * workspace: NULL, or device memory of at least moe_gemm_e4m3_workspace_bytes(m, n, k) bytes,
+ *      256-byte aligned (MOE_ERR_WORKSPACE / MOE_ERR_ALIGN otherwise): caller-owned scratch,
+ *      contents unspecified afterwards; calls that share one must not overlap.  With it, products
+ *      too small to fill the GPU are cut along k, their fp32 parts added in a fixed order: the
+ *      result is deterministic, but its rounding differs from a call without workspace.
+ */
+int moe_gemm_e4m3(int32_t m, int32_t n, int32_t k, const uint8_t* a, const float* a_scales,
+                  const uint8_t* b, const float* b_scales, int32_t b_block, void* c,
+                  int32_t c_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of the optional workspace of moe_gemm_e4m3 (0: such a product never uses one);
+ * negative moe_status for sizes that moe_gemm_e4m3 refuses. */
+int64_t moe_gemm_e4m3_workspace_bytes(int32_t m, int32_t n, int32_t k);
+
+/*
+ * moe_grouped_gemm_e4m3 -- the same product over expert-sorted rows, each with its expert's w:
+ * for every valid tile (e, row0) and row r in [row0, row0+block_m):
+ *   out[r, j] = sum over groups g of row_scales[r, g] * w_scales[e, j/128, g]
+ *               * ( rows[r, g-group] . w[e, j, g-group] )
+ * Unlike moe_grouped_gemm_up and _down it takes and leaves rows in sorted order, of any widths
+ * n and k and with no epilogue: with moe_permute and moe_unpermute around it, the expert products
+ * of layers that those two do not describe, and the gradient with respect to the rows (w
+ * transposed).
+ * Problem: dtype BF16, w_dtype E4M3 (MOE_ERR_DTYPE otherwise); of its sizes T, E, top_k and
+ * block_m count.  n >= 1 and k a positive multiple of 128, at most 32768 each; n*k < 2^31
+ * (MOE_ERR_SHAPE otherwise).
+ * In:  rows uint8 [moe_max_padded_slots, k] (e4m3 codes), row_scales fp32
+ *      [moe_max_padded_slots, k/128]; w uint8 [E, n, k]; w_scales fp32 [E, ceil(n/128), k/128];
+ *      offsets, tiles, num_tiles: outputs of moe_align for the same problem
+ * Out: out out_dtype (MOE_F32 or MOE_BF16) [moe_max_padded_slots, n]: every row of a valid tile
+ *      is written (what its row of `rows` gives: zeros for the padding that moe_permute writes);
+ *      rows past the last valid tile are left untouched.
+ */
+int moe_grouped_gemm_e4m3(const moe_problem* p, int32_t n, int32_t k, const uint8_t* rows,
+                          const float* row_scales, const uint8_t* w, const float* w_scales,
+                          const int32_t* offsets, const int32_t* tiles, const int32_t* num_tiles,
+                          void* out, int32_t out_dtype, void* stream);
 
 /*
  * moe_forward -- the whole layer: align, [quantise X], up, down, combine.

@@ -7,7 +7,8 @@ and call them.
 """
 from __future__ import annotations
 
-from typing import Optional
+import contextlib
+from typing import Optional, Tuple
 
 import torch
 
@@ -36,16 +37,24 @@ from ._lib import (  # noqa: F401
     moe_gemm_workspace_bytes,
     moe_forward,
     moe_forward_scratch,
+    moe_gemm_e4m3,
+    moe_gemm_e4m3_workspace_bytes,
     moe_grouped_gemm_down,
+    moe_grouped_gemm_e4m3,
     moe_grouped_gemm_up,
     moe_grouped_gemm_up_mxfp4,
     moe_max_padded_slots,
     moe_max_tiles,
+    moe_permute,
     moe_pick_block_m,
+    moe_quantize_cols_e4m3,
     moe_quantize_rows_e4m3,
     moe_route,
     moe_route_align,
+    moe_route_bwd,
     moe_scratch_max_bytes,
+    moe_unpermute,
+    moe_unpermute_bwd,
     moe_validate,
     moe_workspace_bytes,
     status_str,
@@ -109,4 +118,123 @@ def forward(p: Problem, x, topk_ids, topk_weights, w13, w2, w13_scales=None, w2_
         workspace = alloc_workspace(p, x.device)
     moe_forward(p, x, topk_ids, topk_weights, w13, w13_scales, w2, w2_scales, out, workspace,
                 stream)
+    return out
+
+
+# ---------------------------------------------------------------------------------------------
+# rows in expert-sorted order, gradients, products of e4m3 codes.  `a` is the alignment that
+# align() or route_align() returns for the same problem.
+# ---------------------------------------------------------------------------------------------
+def _on(stream):
+    """Allocate on the stream that the call runs on, so that the buffers' memory belongs to it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    if stream.device_index != torch.cuda.current_device():
+        raise ValueError(f"stream: of device {stream.device_index}, the current device is "
+                         f"{torch.cuda.current_device()}")
+    return torch.cuda.stream(stream)
+
+
+def permute(p: Problem, x: torch.Tensor, a: dict, x_scales: Optional[torch.Tensor] = None,
+            rows: Optional[torch.Tensor] = None, row_scales: Optional[torch.Tensor] = None,
+            stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Token rows (fp32, bf16 or e4m3 codes with optional scales per 128 columns) in
+    expert-sorted order through moe_permute; returns (rows, row_scales or None)."""
+    with _on(stream):
+        if rows is None:
+            rows = torch.empty((moe_max_padded_slots(p), p.H), dtype=x.dtype, device=x.device)
+        if row_scales is None and x_scales is not None:
+            row_scales = torch.empty((moe_max_padded_slots(p), p.H // 128), dtype=torch.float32,
+                                     device=x.device)
+    moe_permute(p, x, x_scales, a["slot_row"], a["sorted_slots"], a["num_tiles"], rows,
+                row_scales, stream)
+    return rows, row_scales
+
+
+def unpermute(p: Problem, rows: torch.Tensor, a: dict,
+              topk_weights: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """Expert-sorted rows added per token with the routing weights (1 without them: the gradient
+    of permute) through moe_unpermute."""
+    if out is None:
+        with _on(stream):
+            out = torch.empty((p.T, p.H), dtype=rows.dtype, device=rows.device)
+    moe_unpermute(p, rows, a["slot_row"], topk_weights, out, stream)
+    return out
+
+
+def unpermute_bwd(p: Problem, d_out: torch.Tensor, rows: torch.Tensor, a: dict,
+                  topk_weights: Optional[torch.Tensor] = None,
+                  d_rows: Optional[torch.Tensor] = None,
+                  d_weights: Optional[torch.Tensor] = None,
+                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Gradient of unpermute through moe_unpermute_bwd; returns (d_rows, d_weights)."""
+    with _on(stream):
+        if d_rows is None:
+            d_rows = torch.empty((moe_max_padded_slots(p), p.H), dtype=d_out.dtype,
+                                 device=d_out.device)
+        if d_weights is None:
+            d_weights = torch.empty((p.T, p.top_k), dtype=torch.float32, device=d_out.device)
+    moe_unpermute_bwd(p, d_out, rows, a["slot_row"], a["sorted_slots"], a["num_tiles"],
+                      topk_weights, d_rows, d_weights, stream)
+    return d_rows, d_weights
+
+
+def route_bwd(p: Problem, logits: torch.Tensor, renormalize: bool, topk_ids: torch.Tensor,
+              d_weights: torch.Tensor, d_logits: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """Gradient of route's weights with respect to the logits through moe_route_bwd."""
+    if d_logits is None:
+        with _on(stream):
+            d_logits = torch.empty((p.T, p.E), dtype=torch.float32, device=logits.device)
+    moe_route_bwd(p, logits, renormalize, topk_ids, d_weights, d_logits, stream)
+    return d_logits
+
+
+def quantize_cols_e4m3(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Transposed quantisation of a bf16 matrix [m, n] through moe_quantize_cols_e4m3; returns
+    (codes [n, mp], scales [n, mp/128]), mp = m rounded up to 128."""
+    m, n = x.shape
+    groups = -(-m // 128)
+    with _on(stream):
+        xq = torch.empty((n, groups * 128), dtype=torch.float8_e4m3fn, device=x.device)
+        scales = torch.empty((n, groups), dtype=torch.float32, device=x.device)
+    moe_quantize_cols_e4m3(x, xq, scales, stream)
+    return xq, scales
+
+
+def alloc_gemm_e4m3_workspace(m: int, n: int, k: int, device) -> Optional[torch.Tensor]:
+    """The optional workspace of moe_gemm_e4m3 (None when such a product uses none)."""
+    b = moe_gemm_e4m3_workspace_bytes(m, n, k)
+    return torch.empty(b, dtype=torch.uint8, device=device) if b > 0 else None
+
+
+def gemm_e4m3(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
+              out_dtype: torch.dtype = torch.bfloat16, b_block: int = 128,
+              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """a [m, k] times b [n, k] transposed, both e4m3 codes with one scale per 128 values along k,
+    through moe_gemm_e4m3.  Allocates `out` / `workspace` if not given."""
+    with _on(stream):
+        if out is None:
+            out = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype, device=a.device)
+        if workspace is None:
+            workspace = alloc_gemm_e4m3_workspace(a.shape[0], b.shape[0], a.shape[1], a.device)
+    moe_gemm_e4m3(a, a_scales, b, b_scales, b_block, out, workspace, stream)
+    return out
+
+
+def grouped_gemm_e4m3(p: Problem, rows: torch.Tensor, row_scales: torch.Tensor, w: torch.Tensor,
+                      w_scales: torch.Tensor, a: dict, out_dtype: torch.dtype = torch.bfloat16,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Expert-sorted rows (e4m3 codes) times their experts' w [E, n, k] transposed, through
+    moe_grouped_gemm_e4m3."""
+    if out is None:
+        with _on(stream):
+            out = torch.empty((moe_max_padded_slots(p), w.shape[1]), dtype=out_dtype,
+                              device=rows.device)
+    moe_grouped_gemm_e4m3(p, rows, row_scales, w, w_scales, a["offsets"], a["tiles"],
+                          a["num_tiles"], out, stream)
     return out

@@ -34,7 +34,10 @@ EXPORTS = ["moe_status_str", "moe_validate", "moe_pick_block_m", "moe_block_m_fo
            "moe_max_tiles", "moe_workspace_bytes", "moe_route", "moe_route_align", "moe_align",
            "moe_quantize_rows_e4m3", "moe_grouped_gemm_up", "moe_grouped_gemm_up_mxfp4",
            "moe_grouped_gemm_down", "moe_gemm_workspace_bytes",
-           "moe_combine", "moe_forward", "moe_scratch_max_bytes", "moe_forward_scratch"]
+           "moe_combine", "moe_forward", "moe_scratch_max_bytes", "moe_forward_scratch",
+           "moe_permute", "moe_unpermute", "moe_unpermute_bwd", "moe_route_bwd",
+           "moe_quantize_cols_e4m3", "moe_gemm_e4m3", "moe_gemm_e4m3_workspace_bytes",
+           "moe_grouped_gemm_e4m3"]
 
 
 class MoeError(RuntimeError):
@@ -97,6 +100,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_forward": (ctypes.c_int, [P] + [vp] * 9 + [ctypes.c_size_t, vp]),
         "moe_scratch_max_bytes": (ctypes.c_int64, []),
         "moe_forward_scratch": (ctypes.c_int, [P] + [vp] * 9 + [vp]),
+        "moe_permute": (ctypes.c_int, [P, i32] + [vp] * 7 + [vp]),
+        "moe_unpermute": (ctypes.c_int, [P, i32] + [vp] * 4 + [vp]),
+        "moe_unpermute_bwd": (ctypes.c_int, [P, i32] + [vp] * 8 + [vp]),
+        "moe_route_bwd": (ctypes.c_int, [P, vp, ctypes.c_int] + [vp] * 3 + [vp]),
+        "moe_quantize_cols_e4m3": (ctypes.c_int, [i32] * 2 + [vp] * 3 + [vp]),
+        "moe_gemm_e4m3": (ctypes.c_int, [i32] * 3 + [vp] * 4 + [i32, vp, i32, vp,
+                                                                 ctypes.c_size_t, vp]),
+        "moe_gemm_e4m3_workspace_bytes": (ctypes.c_int64, [i32] * 3),
+        "moe_grouped_gemm_e4m3": (ctypes.c_int, [P, i32, i32] + [vp] * 8 + [i32, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -337,3 +349,140 @@ def moe_forward_scratch(p: Problem, x, topk_ids, topk_weights, w13, w13_scales, 
             _ptr(n_invalid, "n_invalid", torch.int32, 1)]
     _checked(load().moe_forward_scratch(ctypes.byref(p), *args, _stream(stream)),
              "moe_forward_scratch")
+
+
+# ---------------------------------------------------------------------------------------------
+# rows in expert-sorted order, gradients, products of e4m3 codes.  Every tensor of a call must be
+# on the current device: the launch goes to that device's stream.
+# ---------------------------------------------------------------------------------------------
+_ROW_DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_E4M3,
+           torch.uint8: MOE_E4M3}
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _here() -> torch.device:
+    return torch.device("cuda", torch.cuda.current_device())
+
+
+def _row_dtype(t: torch.Tensor, name: str) -> int:
+    dt = _ROW_DT.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if dt is None:
+        raise ValueError(f"{name}: dtype {getattr(t, 'dtype', type(t))} not supported")
+    return dt
+
+
+def _mat(t: Optional[torch.Tensor], name: str, dtype, shape, device):
+    """_ptr with the whole shape checked."""
+    if isinstance(t, torch.Tensor) and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return _ptr(t, name, dtype, device=device)
+
+
+def moe_permute(p: Problem, x, x_scales, slot_row, sorted_slots, num_tiles, rows, row_scales,
+                stream=None) -> None:
+    dt = _row_dtype(x, "x")
+    same = _CODES if dt == MOE_E4M3 else x.dtype
+    rm = moe_max_padded_slots(p)
+    dev = _here()
+    args = [_ptr(x, "x", same, p.T * p.H, dev),
+            _ptr(x_scales, "x_scales", torch.float32, p.T * (p.H // 128), dev),
+            _ptr(slot_row, "slot_row", torch.int32, p.T * p.top_k, dev),
+            _ptr(sorted_slots, "sorted_slots", torch.int32, rm, dev),
+            _ptr(num_tiles, "num_tiles", torch.int32, 1, dev),
+            _ptr(rows, "rows", same, rm * p.H, dev),
+            _ptr(row_scales, "row_scales", torch.float32, rm * (p.H // 128), dev)]
+    _checked(load().moe_permute(ctypes.byref(p), dt, *args, _stream(stream)), "moe_permute")
+
+
+def moe_unpermute(p: Problem, rows, slot_row, topk_weights, out, stream=None) -> None:
+    dt = _row_dtype(rows, "rows")
+    rm = moe_max_padded_slots(p)
+    dev = _here()
+    N = p.T * p.top_k
+    args = [_ptr(rows, "rows", rows.dtype, rm * p.H, dev),
+            _ptr(slot_row, "slot_row", torch.int32, N, dev),
+            _ptr(topk_weights, "topk_weights", torch.float32, N, dev),
+            _ptr(out, "out", rows.dtype, p.T * p.H, dev)]
+    _checked(load().moe_unpermute(ctypes.byref(p), dt, *args, _stream(stream)), "moe_unpermute")
+
+
+def moe_unpermute_bwd(p: Problem, d_out, rows, slot_row, sorted_slots, num_tiles, topk_weights,
+                      d_rows, d_weights, stream=None) -> None:
+    dt = _row_dtype(d_out, "d_out")
+    rm = moe_max_padded_slots(p)
+    dev = _here()
+    N = p.T * p.top_k
+    args = [_ptr(d_out, "d_out", d_out.dtype, p.T * p.H, dev),
+            _ptr(rows, "rows", d_out.dtype, rm * p.H, dev),
+            _ptr(slot_row, "slot_row", torch.int32, N, dev),
+            _ptr(sorted_slots, "sorted_slots", torch.int32, rm, dev),
+            _ptr(num_tiles, "num_tiles", torch.int32, 1, dev),
+            _ptr(topk_weights, "topk_weights", torch.float32, N, dev),
+            _ptr(d_rows, "d_rows", d_out.dtype, rm * p.H, dev),
+            _ptr(d_weights, "d_weights", torch.float32, N, dev)]
+    _checked(load().moe_unpermute_bwd(ctypes.byref(p), dt, *args, _stream(stream)),
+             "moe_unpermute_bwd")
+
+
+def moe_route_bwd(p: Problem, logits, renormalize: bool, topk_ids, d_weights, d_logits,
+                  stream=None) -> None:
+    dev = _here()
+    N = p.T * p.top_k
+    args = [_ptr(logits, "logits", torch.float32, p.T * p.E, dev), 1 if renormalize else 0,
+            _ptr(topk_ids, "topk_ids", torch.int32, N, dev),
+            _ptr(d_weights, "d_weights", torch.float32, N, dev),
+            _ptr(d_logits, "d_logits", torch.float32, p.T * p.E, dev)]
+    _checked(load().moe_route_bwd(ctypes.byref(p), *args, _stream(stream)), "moe_route_bwd")
+
+
+def moe_quantize_cols_e4m3(x, xq, scales, stream=None) -> None:
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x: expected a matrix")
+    m, n = x.shape
+    groups = -(-m // 128)
+    dev = _here()
+    args = [_ptr(x, "x", torch.bfloat16, device=dev),
+            _mat(xq, "xq", _CODES, (n, groups * 128), dev),
+            _mat(scales, "scales", torch.float32, (n, groups), dev)]
+    _checked(load().moe_quantize_cols_e4m3(m, n, *args, _stream(stream)), "moe_quantize_cols_e4m3")
+
+
+def moe_gemm_e4m3_workspace_bytes(m: int, n: int, k: int) -> int:
+    return _checked(load().moe_gemm_e4m3_workspace_bytes(m, n, k), "moe_gemm_e4m3_workspace_bytes")
+
+
+def moe_gemm_e4m3(a, a_scales, b, b_scales, b_block: int, c, workspace=None, stream=None) -> None:
+    for name, t in (("a", a), ("b", b)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{name}: expected a matrix")
+    m, k = a.shape
+    n = b.shape[0]
+    dev = _here()
+    sb = n if b_block == 1 else -(-n // 128)
+    args = [_ptr(a, "a", _CODES, device=dev),
+            _mat(a_scales, "a_scales", torch.float32, (m, k // 128), dev),
+            _mat(b, "b", _CODES, (n, k), dev),
+            _mat(b_scales, "b_scales", torch.float32, (sb, k // 128), dev), int(b_block),
+            _mat(c, "c", (torch.float32, torch.bfloat16), (m, n), dev), _row_dtype(c, "c"),
+            _ptr(workspace, "workspace", torch.uint8, device=dev),
+            0 if workspace is None else workspace.numel()]
+    _checked(load().moe_gemm_e4m3(m, n, k, *args, _stream(stream)), "moe_gemm_e4m3")
+
+
+def moe_grouped_gemm_e4m3(p: Problem, rows, row_scales, w, w_scales, offsets, tiles, num_tiles,
+                          out, stream=None) -> None:
+    if not isinstance(w, torch.Tensor) or w.dim() != 3 or w.shape[0] != p.E:
+        raise ValueError("w: expected [E, n, k]")
+    n, k = w.shape[1:]
+    rm = moe_max_padded_slots(p)
+    dev = _here()
+    args = [_mat(rows, "rows", _CODES, (rm, k), dev),
+            _mat(row_scales, "row_scales", torch.float32, (rm, k // 128), dev),
+            _ptr(w, "w", _CODES, device=dev),
+            _mat(w_scales, "w_scales", torch.float32, (p.E, -(-n // 128), k // 128), dev),
+            _ptr(offsets, "offsets", torch.int32, p.E + 1, dev),
+            _ptr(tiles, "tiles", torch.int32, 2 * moe_max_tiles(p), dev),
+            _ptr(num_tiles, "num_tiles", torch.int32, 1, dev),
+            _mat(out, "out", (torch.float32, torch.bfloat16), (rm, n), dev)]
+    _checked(load().moe_grouped_gemm_e4m3(ctypes.byref(p), n, k, *args, _row_dtype(out, "out"),
+                                          _stream(stream)), "moe_grouped_gemm_e4m3")

@@ -93,6 +93,18 @@ Resolved resolve(const moe_problem* p) {
   return r;
 }
 
+// Sizes of moe_gemm_e4m3.  k below 2^22 keeps a tile's 256 operand rows within the 31-bit offsets
+// of one buffer descriptor; the tile bound keeps every launch's threads within 32 bits.
+constexpr int kGemmMaxK = 1 << 22, kGemmMaxDim = 1 << 24, kQuantMaxDim = 1 << 22;
+constexpr int64_t kMaxGemmTiles = 1LL << 30;   // of 16x16
+
+int validate_gemm(int32_t m, int32_t n, int32_t k) {
+  if (m < 1 || n < 1 || m > kGemmMaxDim || n > kGemmMaxDim) return MOE_ERR_SHAPE;
+  if (k < kGroup || k % kGroup || k > kGemmMaxK) return MOE_ERR_SHAPE;
+  if (((int64_t)m + 15) / 16 * (((int64_t)n + 15) / 16) > kMaxGemmTiles) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
 // Workspace pieces of moe_forward, in order, each 256-byte aligned.
 struct Layout {
   int64_t status, counts, offsets, sorted_slots, slot_row, tiles, num_tiles;
@@ -420,6 +432,127 @@ int moe_combine(const moe_problem* p, const void* slot_out, const int32_t* slot_
   if ((v = check_align({{slot_out, 16}, {slot_row, 4}, {out, 16}}))) return v;
   if ((v = check_device())) return v;
   return status_of(launch_combine(resolve(p), slot_out, slot_row, out, (hipStream_t)stream));
+}
+
+int moe_permute(const moe_problem* p, int32_t row_dtype, const void* x, const float* x_scales,
+                const int32_t* slot_row, const int32_t* sorted_slots, const int32_t* num_tiles,
+                void* rows, float* row_scales, void* stream) {
+  int v = validate(p);
+  if (v) return v;
+  if (row_dtype != MOE_F32 && row_dtype != MOE_BF16 && row_dtype != MOE_E4M3) return MOE_ERR_DTYPE;
+  if ((x_scales || row_scales) && row_dtype != MOE_E4M3) return MOE_ERR_DTYPE;
+  if ((x_scales || row_scales) && p->H % kGroup) return MOE_ERR_SHAPE;
+  if (!x || !slot_row || !sorted_slots || !num_tiles || !rows || !x_scales != !row_scales)
+    return MOE_ERR_NULL;
+  if ((v = check_align({{x, 16}, {x_scales, 4}, {slot_row, 4}, {sorted_slots, 4}, {num_tiles, 4},
+                        {rows, 16}, {row_scales, 4}})))
+    return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_permute(resolve(p), row_dtype, x, x_scales, slot_row, sorted_slots,
+                                  num_tiles, rows, row_scales, (hipStream_t)stream));
+}
+
+int moe_unpermute(const moe_problem* p, int32_t row_dtype, const void* rows,
+                  const int32_t* slot_row, const float* topk_weights, void* out, void* stream) {
+  int v = validate(p);
+  if (v) return v;
+  if (row_dtype != MOE_F32 && row_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (!rows || !slot_row || !out) return MOE_ERR_NULL;
+  if ((v = check_align({{rows, 16}, {slot_row, 4}, {topk_weights, 4}, {out, 16}}))) return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_unpermute(resolve(p), row_dtype, rows, slot_row, topk_weights, out,
+                                    (hipStream_t)stream));
+}
+
+int moe_unpermute_bwd(const moe_problem* p, int32_t row_dtype, const void* d_out,
+                      const void* rows, const int32_t* slot_row, const int32_t* sorted_slots,
+                      const int32_t* num_tiles, const float* topk_weights, void* d_rows,
+                      float* d_weights, void* stream) {
+  int v = validate(p);
+  if (v) return v;
+  if (row_dtype != MOE_F32 && row_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (!d_out || !slot_row || !sorted_slots || !num_tiles || (!d_rows && !d_weights) ||
+      (d_weights && !rows))
+    return MOE_ERR_NULL;
+  if ((v = check_align({{d_out, 16}, {rows, 16}, {slot_row, 4}, {sorted_slots, 4}, {num_tiles, 4},
+                        {topk_weights, 4}, {d_rows, 16}, {d_weights, 4}})))
+    return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_unpermute_bwd(resolve(p), row_dtype, d_out, rows, slot_row, sorted_slots,
+                                        num_tiles, topk_weights, d_rows, d_weights,
+                                        (hipStream_t)stream));
+}
+
+int moe_route_bwd(const moe_problem* p, const float* logits, int renormalize,
+                  const int32_t* topk_ids, const float* d_weights, float* d_logits, void* stream) {
+  int v = validate(p);
+  if (v) return v;
+  if (p->top_k > kRouteMaxK) return MOE_ERR_SHAPE;
+  if (!logits || !topk_ids || !d_weights || !d_logits) return MOE_ERR_NULL;
+  if ((v = check_align({{logits, 4}, {topk_ids, 4}, {d_weights, 4}, {d_logits, 4}}))) return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_route_bwd(resolve(p), logits, renormalize, topk_ids, d_weights, d_logits,
+                                    (hipStream_t)stream));
+}
+
+int moe_quantize_cols_e4m3(int32_t m, int32_t n, const void* x, uint8_t* xq, float* scales,
+                           void* stream) {
+  int v;
+  if (m < 1 || n < 8 || n % 8 || m > kQuantMaxDim || n > kQuantMaxDim ||
+      ((int64_t)m + 127) / 128 * (((int64_t)n + 63) / 64) >= (1 << 24))
+    return MOE_ERR_SHAPE;
+  if (!x || !xq || !scales) return MOE_ERR_NULL;
+  if ((v = check_align({{x, 16}, {xq, 16}, {scales, 4}}))) return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_quant_cols(m, n, x, xq, scales, (hipStream_t)stream));
+}
+
+int64_t moe_gemm_e4m3_workspace_bytes(int32_t m, int32_t n, int32_t k) {
+  const int v = validate_gemm(m, n, k);
+  return v != MOE_OK ? v : gemm_e4m3_split_bytes(m, n, k);
+}
+
+int moe_gemm_e4m3(int32_t m, int32_t n, int32_t k, const uint8_t* a, const float* a_scales,
+                  const uint8_t* b, const float* b_scales, int32_t b_block, void* c,
+                  int32_t c_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  int v = validate_gemm(m, n, k);
+  if (v) return v;
+  if (b_block != 1 && b_block != kGroup) return MOE_ERR_SHAPE;
+  if (c_dtype != MOE_F32 && c_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (!a || !a_scales || !b || !b_scales || !c) return MOE_ERR_NULL;
+  const int64_t split = gemm_e4m3_split_bytes(m, n, k);
+  if (workspace && (int64_t)workspace_bytes < split) return MOE_ERR_WORKSPACE;
+  if ((v = check_align({{a, 16}, {a_scales, 4}, {b, 16}, {b_scales, 4}, {c, 16},
+                        {workspace, 256}})))
+    return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_gemm_e4m3(m, n, k, a, a_scales, b, b_scales, b_block == 1, c,
+                                    c_dtype == MOE_F32, split > 0 ? workspace : nullptr,
+                                    (hipStream_t)stream));
+}
+
+int moe_grouped_gemm_e4m3(const moe_problem* p, int32_t n, int32_t k, const uint8_t* rows,
+                          const float* row_scales, const uint8_t* w, const float* w_scales,
+                          const int32_t* offsets, const int32_t* tiles, const int32_t* num_tiles,
+                          void* out, int32_t out_dtype, void* stream) {
+  int v = validate(p);
+  if (v) return v;
+  if (p->dtype != MOE_BF16 || p->w_dtype != MOE_E4M3) return MOE_ERR_DTYPE;
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (n < 1 || n > kMaxDim || k < kGroup || k % kGroup || k > kMaxDim ||
+      (int64_t)n * k > kI32Max)
+    return MOE_ERR_SHAPE;
+  const Resolved r = resolve(p);
+  if (r.tiles_max * ((n + 15) / 16) > kMaxGemmTiles) return MOE_ERR_SHAPE;   // grid bound
+  if (!rows || !row_scales || !w || !w_scales || !offsets || !tiles || !num_tiles || !out)
+    return MOE_ERR_NULL;
+  if ((v = check_align({{rows, 16}, {row_scales, 4}, {w, 16}, {w_scales, 4}, {offsets, 4},
+                        {tiles, 4}, {num_tiles, 4}, {out, 16}})))
+    return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_grouped_gemm_e4m3(r, n, k, rows, row_scales, w, w_scales, offsets,
+                                            tiles, num_tiles, out, out_dtype == MOE_F32,
+                                            (hipStream_t)stream));
 }
 
 int moe_forward(const moe_problem* p, const void* x, const int32_t* topk_ids,

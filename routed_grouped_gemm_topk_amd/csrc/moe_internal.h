@@ -279,6 +279,32 @@ hipError_t launch_up_mxfp4(const Resolved& r, const uint8_t* x, const float* x_s
                            const int32_t* sorted_slots, const int32_t* offsets,
                            const int32_t* tiles, const int32_t* num_tiles, uint8_t* act,
                            hipStream_t s);
+// Rows in expert-sorted order and back (moe_permute.hip).
+hipError_t launch_permute(const Resolved& r, int row_dtype, const void* x, const float* x_scales,
+                          const int32_t* slot_row, const int32_t* sorted_slots,
+                          const int32_t* num_tiles, void* rows, float* row_scales, hipStream_t s);
+hipError_t launch_unpermute(const Resolved& r, int row_dtype, const void* rows,
+                            const int32_t* slot_row, const float* topk_w, void* out,
+                            hipStream_t s);
+hipError_t launch_unpermute_bwd(const Resolved& r, int row_dtype, const void* d_out,
+                                const void* rows, const int32_t* slot_row,
+                                const int32_t* sorted_slots, const int32_t* num_tiles,
+                                const float* topk_w, void* d_rows, float* d_w, hipStream_t s);
+hipError_t launch_route_bwd(const Resolved& r, const float* logits, int renorm,
+                            const int32_t* topk_ids, const float* d_w, float* d_logits,
+                            hipStream_t s);
+// Products of e4m3 codes with one scale per 128 values (moe_gemm_e4m3.hip).
+hipError_t launch_quant_cols(int M, int C, const void* x, uint8_t* xq, float* scales,
+                             hipStream_t s);
+int64_t gemm_e4m3_split_bytes(int M, int N, int K);
+hipError_t launch_gemm_e4m3(int M, int N, int K, const uint8_t* a, const float* sa,
+                            const uint8_t* b, const float* sb, bool b_rows, void* c, bool c_f32,
+                            void* split_ws, hipStream_t s);
+hipError_t launch_grouped_gemm_e4m3(const Resolved& r, int N, int K, const uint8_t* rows,
+                                    const float* row_scales, const uint8_t* w,
+                                    const float* w_scales, const int32_t* offsets,
+                                    const int32_t* tiles, const int32_t* num_tiles, void* out,
+                                    bool out_f32, hipStream_t s);
 hipError_t launch_combine(const Resolved& r, const void* slot_out, const int32_t* slot_row,
                           void* out, hipStream_t s);
 

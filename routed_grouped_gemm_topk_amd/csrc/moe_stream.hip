@@ -57,6 +57,71 @@ hipError_t launch_quant_rows(const Resolved& r, const void* x, uint8_t* xq, floa
 }
 
 // ---------------------------------------------------------------------------------------------
+// The same quantisation along the rows, transposed: x [M, C] -> codes [C, Mp], scales
+// [C, Mp/128], Mp = M rounded up to 128.  Operand of a weight gradient, whose sum runs over the
+// tokens.  One workgroup takes 128 rows x 64 columns: the tile goes through LDS (pitch 33 words,
+// so that the 4 lanes of a column and the 16 columns of a wave read different banks but for a
+// two-way conflict), 4 lanes per column take 32 rows each and store them as 32 bytes.  Rows past
+// M are zeros.  The quotients are IEEE fp32 and at most 448 up to their rounding (up to 450 where
+// the scale itself is subnormal), below the 464 from which e4m3 would overflow, so the gfx950
+// convert (nearest even, NaN kept) needs no clamp.
+// ---------------------------------------------------------------------------------------------
+constexpr int kQuantCols = 64;
+
+__global__ __launch_bounds__(kQuantThreads) void quant_cols_e4m3_kernel(
+    const uint16_t* __restrict__ x, uint8_t* __restrict__ xq, float* __restrict__ scales, int M,
+    int C, int groups) {
+  constexpr int PITCH = kQuantCols / 2 + 1;              // words
+  __shared__ uint32_t tile[kGroup * PITCH];
+  const int g = blockIdx.x % groups;
+  const int c0 = (blockIdx.x / groups) * kQuantCols;
+  const int64_t m0 = (int64_t)g * kGroup;
+  #pragma unroll
+  for (int i = 0; i < kGroup * kQuantCols / 8 / kQuantThreads; ++i) {
+    const int q = i * kQuantThreads + threadIdx.x;
+    const int r = q / (kQuantCols / 8), c = (q % (kQuantCols / 8)) * 8;
+    i32x4 v{0, 0, 0, 0};
+    if (m0 + r < M && c0 + c < C)                        // C is a multiple of 8
+      v = *reinterpret_cast<const i32x4*>(x + (m0 + r) * C + c0 + c);
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) tile[r * PITCH + c / 2 + k] = (uint32_t)v[k];
+  }
+  __syncthreads();
+  const int c = threadIdx.x >> 2, part = threadIdx.x & 3;
+  float v[32];
+  float m = 0.0f;
+  #pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const uint32_t w = tile[(part * 32 + i) * PITCH + (c >> 1)];
+    v[i] = bf16_bits_to_f32((c & 1) ? w >> 16 : w & 0xFFFFu);
+    m = fmaxf(m, fabsf(v[i]));
+  }
+  m = fmaxf(m, __shfl_xor(m, 1, kWave));
+  m = fmaxf(m, __shfl_xor(m, 2, kWave));
+  if (c0 + c >= C) return;
+  const float s = (m == 0.0f) ? 1.0f : m / kE4M3Max;
+  uint32_t o[8];
+  #pragma unroll
+  for (int i = 0; i < 8; ++i)
+    o[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(
+        v[4 * i + 2] / s, v[4 * i + 3] / s,
+        __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] / s, v[4 * i + 1] / s, 0, false), true);
+  i32x4* dst = reinterpret_cast<i32x4*>(xq + (size_t)(c0 + c) * groups * kGroup + m0 + part * 32);
+  dst[0] = i32x4{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+  dst[1] = i32x4{(int)o[4], (int)o[5], (int)o[6], (int)o[7]};
+  if (part == 0) scales[(size_t)(c0 + c) * groups + g] = s;
+}
+
+hipError_t launch_quant_cols(int M, int C, const void* x, uint8_t* xq, float* scales,
+                             hipStream_t s) {
+  const int groups = (M + kGroup - 1) / kGroup;
+  const int64_t blocks = (int64_t)groups * ((C + kQuantCols - 1) / kQuantCols);
+  hipLaunchKernelGGL(quant_cols_e4m3_kernel, dim3((unsigned)blocks), dim3(kQuantThreads), 0, s,
+                     (const uint16_t*)x, xq, scales, M, C, groups);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------------------------
 // Combine ("factor_moe_fused_gemm.cu": index_add_ in the slow path and
 // weighted_scatter_add_kernel, which there adds with float atomics).  Here each thread
 // owns 16 bytes of one token's output row and adds that token's top_k slot rows in

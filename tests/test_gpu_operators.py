@@ -1,0 +1,568 @@
+"""The operators around the layer on the GPU, against plain computations in 64 bits.
+
+Tolerances count roundings (u = half a step of the type, relative: 2^-24 fp32, 2^-8 bf16):
+  * permute, the codes and scales of quantize_cols: none, bit for bit;
+  * unpermute: top_k fp32 products and sums, then one rounding to the row type;
+  * unpermute_bwd: d_rows one product, one rounding; d_weights a sum of H products, at most
+    H / 64 + 8 of them one after another (a wave's lanes, then a tree);
+  * route_bwd: p carries the rounding of l - max (|l - max| u in the exponent), of exp (2 u) and of
+    the sum and quotient (16 + 6 + 2 additions at most);
+  * products of codes: every product of two e4m3 values is exact in fp32; a group's 128 products
+    are added inside the matrix instruction (at most 2 u each of the sum of magnitudes), then one
+    product of scales, one fma and one addition per group.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import routed_grouped_gemm_topk_amd as moe
+
+pytestmark = pytest.mark.gpu
+
+U32, UBF = 2.0 ** -24, 2.0 ** -8
+TD = {"f32": torch.float32, "bf16": torch.bfloat16}
+UT = {"f32": 0.0, "bf16": UBF}
+E4M3 = torch.float8_e4m3fn
+G, PAT = 4096, 0xA5
+
+
+class Guarded:
+    """A tensor whose surroundings hold a known pattern, body filled with it too."""
+
+    def __init__(self, shape, dtype, device):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        self.n = n
+        self.buf = torch.full((G + n + G,), PAT, dtype=torch.uint8, device=device)
+        self.t = self.buf[G:G + n].view(dtype).view(shape)
+
+    def intact(self, rows_written=None):
+        """No byte outside the body changed, nor any from row `rows_written` on."""
+        ok = bool((self.buf[:G] == PAT).all()) and bool((self.buf[G + self.n:] == PAT).all())
+        if rows_written is not None:
+            per = self.n // self.t.shape[0]
+            ok = ok and bool((self.buf[G + rows_written * per:] == PAT).all())
+        return ok
+
+
+def gen(device, seed):
+    g = torch.Generator(device=device)
+    g.manual_seed(seed)
+    return g
+
+
+def routing(device, T, E, k, mode, seed):
+    """ids int32 [T, k]; mode: 'all' local, 'some' excluded, 'none' local, 'one' expert only,
+    'twice' (each token names the same expert k times)."""
+    g = gen(device, seed)
+    ids = torch.rand((T, E), generator=g, device=device).topk(k, 1)[1].to(torch.int32)
+    if mode == "some":
+        drop = torch.rand((T, k), generator=g, device=device) < 0.6
+        ids = torch.where(drop, torch.where(ids % 2 == 0, E + ids, -1 - ids), ids).to(torch.int32)
+    elif mode == "none":
+        ids = ids + E
+    elif mode == "one":
+        ids = torch.full_like(ids, E - 1)
+    elif mode == "twice":
+        ids = ids[:, :1].expand(T, k)
+    return ids.contiguous()
+
+
+def aligned(device, T, H, E, k, bm, mode, seed, fp8=False):
+    p = moe.make_problem(T, H, 128, E, k, "bf16", "e4m3" if fp8 else None, bm)
+    a = moe.align(p, routing(device, T, E, k, mode, seed))
+    used = int(a["num_tiles"]) * bm
+    ss = a["sorted_slots"].long()
+    held = (ss < T * k) & (torch.arange(ss.numel(), device=device) < used)
+    return p, a, used, ss, held
+
+
+def say(*x):
+    print(*x, flush=True)
+
+
+def close(got, ref, tol, what):
+    """|got - ref| <= tol elementwise (NaN and infinities have to agree)."""
+    got = got.double()
+    fin = torch.isfinite(ref)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), f"{what}: NaN in other places"
+    inf = ~fin & ~torch.isnan(ref)
+    assert torch.equal(got[inf], ref[inf]), f"{what}: infinities differ"
+    d = (got - ref).abs()[fin] - (tol.expand_as(ref)[fin] if isinstance(tol, torch.Tensor) else tol)
+    worst = float(d.max()) if d.numel() else 0.0
+    assert worst <= 0.0, f"{what}: {worst:.3e} beyond the tolerance"
+
+
+# (T, H, E, k, block_m, ids)
+SORTED = [(1, 64, 1, 1, 16, "all"), (1, 7168, 256, 8, 16, "all"), (3, 192, 5, 3, 32, "some"),
+          (65, 2880, 16, 4, 64, "some"), (33, 128, 4, 2, 128, "none"), (40, 256, 8, 5, 16, "twice"),
+          (300, 1024, 64, 6, 256, "all"), (257, 512, 3, 2, 128, "one"), (9, 32768, 2, 2, 16, "all"),
+          (2000, 128, 1024, 8, 16, "all")]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "e4m3", "e4m3_plain"])
+@pytest.mark.parametrize("c", SORTED, ids=str)
+def test_permute(device, c, dtype):
+    T, H, E, k, bm, mode = c
+    say("permute", c, dtype)
+    p, a, used, ss, held = aligned(device, T, H, E, k, bm, mode, 1)
+    g = gen(device, 2)
+    scales = rs = None
+    if dtype.startswith("e4m3"):
+        x = torch.randint(0, 256, (T, H), generator=g, device=device, dtype=torch.uint8)
+        if dtype == "e4m3" and H % 128 == 0:
+            scales = torch.rand((T, H // 128), generator=g, device=device)
+            rs = Guarded((ss.numel(), H // 128), torch.float32, device)
+    else:
+        x = torch.randn((T, H), generator=g, device=device).to(TD[dtype])
+        x[0, 3], x[-1, 0] = float("nan"), float("inf")
+    rows = Guarded((ss.numel(), H), x.dtype, device)
+    moe.permute(p, x, a, scales, rows=rows.t, row_scales=rs.t if rs else None)
+    torch.cuda.synchronize()
+    tok = (ss // k).clamp(max=T - 1)
+    want = torch.where(held[:, None], x[tok], torch.zeros((), dtype=x.dtype, device=device))
+    as_bits = (lambda t: t) if x.dtype == torch.uint8 else (lambda t: t.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32))
+    assert torch.equal(as_bits(rows.t[:used]), as_bits(want[:used]))
+    assert rows.intact(used)
+    if rs:
+        want = torch.where(held[:, None], scales[tok], torch.ones((), device=device))
+        assert torch.equal(rs.t[:used], want[:used]) and rs.intact(used)
+
+
+def sorted_rows(device, ss, held, H, dt, seed):
+    """Rows of the sorted list; what no slot owns holds NaN, which nothing may read."""
+    y = torch.randn((ss.numel(), H), generator=gen(device, seed), device=device)
+    return torch.where(held[:, None], y, float("nan")).to(dt)
+
+
+@pytest.mark.parametrize("weighted", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", SORTED, ids=str)
+def test_unpermute(device, c, dtype, weighted):
+    T, H, E, k, bm, mode = c
+    say("unpermute", c, dtype, weighted)
+    p, a, used, ss, held = aligned(device, T, H, E, k, bm, mode, 3)
+    rows = sorted_rows(device, ss, held, H, TD[dtype], 4)
+    at = a["slot_row"].long()
+    w = torch.randn((T, k), generator=gen(device, 5), device=device)
+    w = torch.where(at.view(T, k) < 0, float("nan"), w) if weighted else None
+    out = Guarded((T, H), TD[dtype], device)
+    moe.unpermute(p, rows, a, w, out=out.t)
+    torch.cuda.synchronize()
+    there = (at >= 0)[:, None]
+    y = torch.where(there, rows.double()[at.clamp(min=0)], 0.0).view(T, k, H)
+    wd = torch.where(at >= 0, w.double().view(-1), 0.0).view(T, k) if weighted else torch.ones((T, k), device=device).double()
+    terms = y * wd[:, :, None]
+    ref, mag = terms.sum(1), terms.abs().sum(1)
+    assert out.intact()
+    close(out.t, ref, (k + 1) * U32 * mag + UT[dtype] * (ref.abs() + (k + 1) * U32 * mag) + 1e-38, "out")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", SORTED, ids=str)
+def test_unpermute_bwd(device, c, dtype):
+    T, H, E, k, bm, mode = c
+    say("unpermute_bwd", c, dtype)
+    p, a, used, ss, held = aligned(device, T, H, E, k, bm, mode, 6)
+    g = gen(device, 7)
+    rows = sorted_rows(device, ss, held, H, TD[dtype], 8)
+    d_out = torch.randn((T, H), generator=g, device=device).to(TD[dtype])
+    w = torch.randn((T, k), generator=g, device=device)
+    d_rows = Guarded((ss.numel(), H), TD[dtype], device)
+    d_w = Guarded((T, k), torch.float32, device)
+    moe.unpermute_bwd(p, d_out, rows, a, w, d_rows=d_rows.t, d_weights=d_w.t)
+    torch.cuda.synchronize()
+    slot = ss.clamp(max=T * k - 1)
+    d = d_out.double()[slot // k]
+    ref = torch.where(held[:, None], d * w.double().view(-1)[slot][:, None], 0.0)[:used]
+    close(d_rows.t[:used], ref, (UT[dtype] + 2 * U32) * ref.abs() + 1e-38, "d_rows")
+    assert d_rows.intact(used) and d_w.intact()
+    at = a["slot_row"].long()
+    y = torch.where((at >= 0)[:, None], rows.double()[at.clamp(min=0)], 0.0).view(T, k, H)
+    terms = y * d_out.double()[:, None, :]
+    close(d_w.t, terms.sum(2), (H / 64 + 8) * U32 * terms.abs().sum(2), "d_weights")
+    # one output alone, and no weights
+    alone = Guarded((ss.numel(), H), TD[dtype], device)
+    moe.moe_unpermute_bwd(p, d_out, None, a["slot_row"], a["sorted_slots"], a["num_tiles"], w,
+                          alone.t, None)
+    only = Guarded((T, k), torch.float32, device)
+    moe.moe_unpermute_bwd(p, d_out, rows, a["slot_row"], a["sorted_slots"], a["num_tiles"], None,
+                          None, only.t)
+    torch.cuda.synchronize()
+    assert torch.equal(alone.buf, d_rows.buf) and torch.equal(only.buf, d_w.buf)
+    plain, _ = moe.unpermute_bwd(p, d_out, rows, a)
+    assert torch.equal(plain[:used][held[:used]], d_out[(ss // k)[held]])
+
+
+def test_permute_and_unpermute_are_adjoint(device):
+    """<permute(x), d> = <x, unpermute(d)>, and unpermute's gradients against differences: the
+    combine is linear in the rows and in the weights, so a step of any length is exact."""
+    T, H, E, k, bm = 130, 256, 16, 3, 32
+    p, a, used, ss, held = aligned(device, T, H, E, k, bm, "some", 9)
+    g = gen(device, 10)
+    x = torch.randn((T, H), generator=g, device=device)
+    d = torch.randn((ss.numel(), H), generator=g, device=device)
+    rows, _ = moe.permute(p, x, a)
+    dx = moe.unpermute(p, d, a)
+    lhs = (rows[:used].double() * d[:used].double()).sum()
+    terms = x.double() * dx.double()
+    assert abs(float(lhs - terms.sum())) <= (k + 1) * U32 * float(terms.abs().sum()) * math.sqrt(k)
+    w = torch.randn((T, k), generator=g, device=device)
+    d_out = torch.randn((T, H), generator=g, device=device)
+    y = torch.where(held[:, None], d, 0.0)
+    d_rows, d_w = moe.unpermute_bwd(p, d_out, y, a, w)
+    base = moe.unpermute(p, y, a, w).double()
+    for rows2, w2, ref in ((y + torch.where(held[:, None], x[(ss // k).clamp(max=T - 1)], 0.0), w,
+                            lambda r, v: (d_rows[:used].double() * (r - y.double())[:used]).sum()),
+                           (y, w + 1.0, lambda r, v: (d_w.double() * (v - w.double())).sum())):
+        got = ((moe.unpermute(p, rows2, a, w2).double() - base) * d_out.double()).sum()
+        mag = moe.unpermute(p, y.abs(), a, w.abs()) + moe.unpermute(p, rows2.abs(), a, w2.abs())
+        mag = float((mag.double() * d_out.double().abs()).sum())
+        assert abs(float(got - ref(rows2.double(), w2.double()))) <= (H / 64 + 8 + 4 * k) * U32 * mag
+
+
+ROUTE = [(1, 1, 1), (1, 2, 1), (5, 8, 2), (4097, 8, 2), (7, 64, 6), (3, 65, 64), (100, 256, 8),
+         (2, 1000, 7), (33, 1024, 64), (6, 200, 1)]
+
+
+def route_reference(lg, renorm, ids, dw):
+    """d_logits in 64 bits by automatic differentiation of the weights' definition; also the sum
+    of the magnitudes that each element is made of."""
+    E = lg.shape[1]
+    l64 = lg.double().clone().requires_grad_(True)
+    ok = (ids >= 0) & (ids < E)
+    p = torch.softmax(l64, 1)
+    w = torch.where(ok, torch.gather(p, 1, ids.clamp(0, E - 1).long()), 0.0)
+    if renorm:
+        s = w.sum(1, keepdim=True)
+        w = w / torch.where(s > 0, s, 1.0)
+    dwd = torch.where(ok, dw, 0.0).double()
+    (w * dwd).sum().backward()
+    wm = (w * dwd).abs().detach()
+    mag = torch.zeros_like(lg, dtype=torch.float64)
+    mag.scatter_add_(1, ids.clamp(0, E - 1).long(), wm + w.detach() * wm.sum(1, keepdim=True))
+    if not renorm:
+        mag += p.detach() * wm.sum(1, keepdim=True)
+    # the reference's own rounding: with renorm the automatic derivative reaches the 0 of an
+    # expert that was not chosen as a difference of terms up to the row's sum, each carrying at
+    # most E + 8 roundings of 2^-53; in units of the fp32 tolerance below (at least 60 * 2^-24)
+    mag += (E + 8) * 2.0 ** -53 / (60 * U32) * 4 * wm.sum(1, keepdim=True)
+    return l64.grad, mag
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("c", ROUTE, ids=str)
+def test_route_bwd(device, c, renorm):
+    T, E, k = c
+    say("route_bwd", c, renorm)
+    g = gen(device, 11)
+    lg = 3 * torch.randn((T, E), generator=g, device=device)
+    p = moe.make_problem(T, 128, 128, E, k, "bf16")
+    ids, _ = moe.route(p, lg, renorm)
+    dw = torch.randn((T, k), generator=g, device=device)
+    span = float((lg.max(1)[0] - lg.min(1)[0]).max())
+    for change in ("as routed", "some outside", "twice"):
+        i2, d2 = ids.clone(), dw.clone()
+        if change == "some outside":
+            i2[::2, 0] = E
+            i2[1::3, -1] = -1
+            d2 = torch.where((i2 < 0) | (i2 >= E), float("nan"), d2)
+        elif change == "twice":
+            i2[:, -1] = i2[:, 0]
+        out = Guarded((T, E), torch.float32, device)
+        moe.moe_route_bwd(p, lg, renorm, i2, d2, out.t)
+        torch.cuda.synchronize()
+        ref, mag = route_reference(lg, renorm, i2, d2)
+        assert out.intact()
+        close(out.t, ref, 2 * (span + 2 + 24 + 4) * U32 * mag + 1e-37, change)
+
+
+def test_route_bwd_against_differences(device):
+    """Central differences of the loss sum(w dw), in 64 bits on the definition: their error is
+    h^2/6 times the third derivative (at most a few times the weights' magnitude)."""
+    T, E, k, h = 4, 12, 3, 1e-4
+    g = gen(device, 12)
+    lg = torch.randn((T, E), generator=g, device=device)
+    dw = torch.randn((T, k), generator=g, device=device)
+    p = moe.make_problem(T, 128, 128, E, k, "bf16")
+    for renorm in (False, True):
+        ids, _ = moe.route(p, lg, renorm)
+        got = moe.route_bwd(p, lg, renorm, ids, dw).double()
+
+        def loss(l):
+            w = torch.gather(torch.softmax(l, 1), 1, ids.long())
+            w = w / w.sum(1, keepdim=True) if renorm else w
+            return (w * dw.double()).sum(1)
+        for e in range(E):
+            step = torch.zeros((T, E), device=device, dtype=torch.float64)
+            step[:, e] = h
+            diff = (loss(lg.double() + step) - loss(lg.double() - step)) / (2 * h)
+            bound = h * h * 8 * float(dw.abs().sum(1).max()) + 200 * U32 * float(dw.abs().sum())
+            assert float((diff - got[:, e]).abs().max()) <= bound
+
+
+def row_codes(x):
+    m, c = x.shape
+    v = x.float().view(m, c // 128, 128)
+    a = v.abs().amax(2)
+    s = torch.where(a == 0, torch.ones_like(a), a / torch.full_like(a, 448.0))   # IEEE quotient
+    return (v / s[:, :, None]).clamp(-448, 448).to(E4M3).view(m, c), s
+
+
+def operands(device, m, n, k, b_block, seed):
+    g = gen(device, seed)
+    a, sa = row_codes(torch.randn((m, k), generator=g, device=device))
+    b, _ = row_codes(torch.randn((n, k), generator=g, device=device))
+    sb = torch.rand((n if b_block == 1 else -(-n // 128), k // 128), generator=g, device=device) + 0.1
+    return a, sa, b, sb
+
+
+def product(a, sa, b, sb, b_block):
+    """(product, sum of magnitudes) in 64 bits."""
+    sbr = sb if b_block == 1 else sb.repeat_interleave(128, 0)[: b.shape[0]]
+    a64 = a.view(E4M3).double() * sa.double().repeat_interleave(128, 1)
+    b64 = b.view(E4M3).double() * sbr.double().repeat_interleave(128, 1)
+    return a64 @ b64.t(), a64.abs() @ b64.abs().t()
+
+
+def gemm_tol(ref, mag, k, dtype):
+    fp32 = (2 * 128 + 3 + k // 128) * U32 * mag
+    return fp32 + UT[dtype] * (ref.abs() + fp32) + 1e-37
+
+
+GEMM = [(1, 1, 128), (1, 7168, 2048), (3, 130, 384), (16, 576, 7168), (17, 64, 128), (33, 257, 1152),
+        (64, 2880, 256), (65, 4096, 896), (100, 100, 640), (128, 128, 128), (129, 1000, 1280),
+        (255, 513, 384), (300, 520, 2048), (513, 768, 512), (1000, 2049, 256), (2048, 1536, 1024)]
+
+
+@pytest.mark.parametrize("b_block", [128, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", GEMM, ids=str)
+def test_gemm_e4m3(device, c, dtype, b_block):
+    m, n, k = c
+    say("gemm_e4m3", c, dtype, b_block)
+    a, sa, b, sb = operands(device, m, n, k, b_block, 13)
+    ref, mag = product(a, sa, b, sb, b_block)
+    need = moe.moe_gemm_e4m3_workspace_bytes(m, n, k)
+    for with_ws in ((False, True) if need else (False,)):
+        ws = Guarded((need,), torch.uint8, device) if with_ws else None
+        c_ = Guarded((m, n), TD[dtype], device)
+        moe.moe_gemm_e4m3(a, sa, b, sb, b_block, c_.t, ws.t if ws else None)
+        torch.cuda.synchronize()
+        assert c_.intact() and (ws is None or ws.intact())
+        close(c_.t, ref, gemm_tol(ref, mag, k, dtype), f"c, workspace {with_ws}")
+        again = torch.empty_like(c_.t)
+        moe.moe_gemm_e4m3(a, sa, b, sb, b_block, again, ws.t if ws else None)
+        torch.cuda.synchronize()
+        assert torch.equal(again, c_.t), "two runs differ"
+
+
+@pytest.mark.parametrize("m,n,k", [(4, 64, 256), (40, 200, 512), (200, 300, 384)])
+def test_gemm_e4m3_special_values(device, m, n, k):
+    """NaN codes, infinite, zero and NaN scales reach exactly their rows and columns."""
+    a, sa, b, sb = operands(device, m, n, k, 1, 14)
+    a.view(torch.uint8)[1, 5] = 0x7F                      # NaN code
+    b.view(torch.uint8)[n - 1, k - 1] = 0xFF
+    a.view(torch.uint8)[0, :128] = 0x38                   # ones times an infinite scale
+    sa[0, 0] = float("inf")
+    b.view(torch.uint8)[:, :128] = 0x38
+    b.view(torch.uint8)[n - 1, k - 1] = 0xFF
+    sa[2, 1], sb[0, 0] = 0.0, float("nan")
+    ref, mag = product(a, sa, b, sb, 1)
+    mag = torch.nan_to_num(mag, 0.0, 0.0, 0.0)
+    for dtype in ("bf16", "f32"):
+        c_ = moe.gemm_e4m3(a, sa, b, sb, out_dtype=TD[dtype], b_block=1)
+        torch.cuda.synchronize()
+        close(c_, ref, gemm_tol(torch.nan_to_num(ref, 0.0, 0.0, 0.0), mag, k, dtype), dtype)
+
+
+GROUPED = [(1, 4, 1, 16, 100, 256, "all"), (64, 8, 2, 16, 576, 512, "all"),
+           (37, 5, 3, 32, 257, 384, "some"), (200, 16, 4, 64, 1000, 256, "some"),
+           (300, 3, 2, 128, 320, 1024, "all"), (20, 4, 2, 128, 128, 128, "none"),
+           (700, 4, 3, 128, 384, 640, "one"), (40, 300, 8, 16, 64, 128, "all"),
+           (90, 2, 2, 32, 130, 1152, "all"), (150, 2, 1, 64, 96, 2048, "all")]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", GROUPED, ids=str)
+def test_grouped_gemm_e4m3(device, c, dtype):
+    T, E, k, bm, n, kk, mode = c
+    say("grouped_gemm_e4m3", c, dtype)
+    p, a, used, ss, held = aligned(device, T, 128, E, k, bm, mode, 15, fp8=True)
+    g = gen(device, 16)
+    rows, rs = row_codes(torch.randn((ss.numel(), kk), generator=g, device=device))
+    rows.view(torch.uint8)[used:] = 0x7F                  # past the last tile: never read
+    w, _ = row_codes(torch.randn((E * n, kk), generator=g, device=device))
+    w = w.view(E, n, kk)
+    ws = torch.rand((E, -(-n // 128), kk // 128), generator=g, device=device) + 0.1
+    out = Guarded((ss.numel(), n), TD[dtype], device)
+    moe.grouped_gemm_e4m3(p, rows, rs, w, ws, a, out=out.t)
+    torch.cuda.synchronize()
+    assert out.intact(used)
+    offs = a["offsets"].tolist()
+    for e in range(E):
+        lo, hi = offs[e], offs[e + 1]
+        if lo == hi:
+            continue
+        ref, mag = product(rows[lo:hi], rs[lo:hi], w[e], ws[e], 128)
+        close(out.t[lo:hi], ref, gemm_tol(ref, mag, kk, dtype), f"expert {e}")
+
+
+@pytest.mark.parametrize("m,n", [(1, 8), (127, 64), (128, 72), (129, 200), (1000, 8), (400, 1032),
+                                 (4001, 2048)])
+def test_quantize_cols(device, m, n):
+    say("quantize_cols", m, n)
+    x = torch.randn((m, n), generator=gen(device, 17), device=device)
+    x = (x * torch.exp(4 * torch.randn((1, n), generator=gen(device, 18), device=device))).bfloat16()
+    x[:, 1] = 0.0
+    x[:, 2] = 1e-40                                        # subnormal, and a subnormal scale
+    x[0, 3] = -0.0
+    x[m - 1, 4], x[m // 2, 5] = float("nan"), float("inf")
+    groups = -(-m // 128)
+    xq, sc = Guarded((n, groups * 128), torch.uint8, device), Guarded((n, groups), torch.float32, device)
+    moe.moe_quantize_cols_e4m3(x, xq.t, sc.t)
+    torch.cuda.synchronize()
+    v = torch.zeros((groups * 128, n), device=device)
+    v[:m] = x.float()
+    v = v.t().contiguous().view(n, groups, 128).cpu()
+    amax = torch.nan_to_num(v.abs(), 0.0, float("inf")).amax(2)
+    s = torch.where(amax == 0, torch.ones_like(amax), amax / 448.0)
+    q = (v / s[:, :, None]).to(E4M3).view(torch.uint8).view(n, -1)
+    got = xq.t.cpu()
+    nan = (q & 0x7F) == 0x7F                               # the sign of a NaN is not specified
+    assert torch.equal(sc.t.cpu(), s)
+    assert torch.equal(got[~nan], q[~nan]) and bool(((got[nan] & 0x7F) == 0x7F).all())
+    assert xq.intact() and sc.intact()
+
+
+def chain_inputs(device, T=200, H=256, n=384, E=8, k=2, bm=32, seed=19):
+    g = gen(device, seed)
+    p = moe.make_problem(T, H, 128, E, k, "bf16", "e4m3", bm)
+    lg = torch.randn((T, E), generator=g, device=device)
+    x = torch.randn((T, H), generator=g, device=device).bfloat16()
+    w, _ = row_codes(torch.randn((E * n, H), generator=g, device=device))
+    ws = 0.02 * (torch.rand((E, n // 128, H // 128), generator=g, device=device) + 0.5)
+    d_out = torch.randn((T, n), generator=g, device=device).bfloat16()
+    return p, lg, x, w.view(E, n, H), ws, d_out
+
+
+def chain(p, lg, x, w, ws, d_out, stream=None, keep=None):
+    """Router to output and back to the logits and the rows, as a training step runs them."""
+    b = keep if keep is not None else {}
+    E, n, H = w.shape
+    pn = b.setdefault("pn", moe.make_problem(p.T, n, 128, p.E, p.top_k, "bf16", "e4m3", p.block_m))
+    dev = x.device
+    a = moe.route_align(p, lg, True, stream=stream)
+    xq = torch.empty(x.shape, dtype=E4M3, device=dev)
+    xs = torch.empty((p.T, H // 128), device=dev)
+    moe.moe_quantize_rows_e4m3(p, x, xq, xs, stream)
+    rows, rs = moe.permute(p, xq, a, xs, stream=stream)
+    y = moe.grouped_gemm_e4m3(p, rows, rs, w, ws, a, stream=stream)
+    out = moe.unpermute(pn, y, a, a["topk_weights"], stream=stream)
+    dy, dwt = moe.unpermute_bwd(pn, d_out, y, a, a["topk_weights"], stream=stream)
+    dlg = moe.route_bwd(p, lg, True, a["topk_ids"], dwt, stream=stream)
+    return a, y, out, dy, dwt, dlg, (xq, xs, rows, rs)      # memory lives until the caller is done
+
+
+def test_chain(device):
+    """route_align, quantise, permute, the experts' products, unpermute and all gradients: each
+    against 64 bits on the values that reached it."""
+    p, lg, x, w, ws, d_out = chain_inputs(device)
+    a, y, out, dy, dwt, dlg, _ = chain(p, lg, x, w, ws, d_out)
+    torch.cuda.synchronize()
+    T, k, E, n = p.T, p.top_k, p.E, w.shape[1]
+    xq, xs = row_codes(x)
+    pr = torch.softmax(lg.double(), 1)
+    wt, ids = pr.topk(k, 1)
+    wt = wt / wt.sum(1, keepdim=True)
+    assert torch.equal(ids.to(torch.int32), a["topk_ids"])
+    ref, mag = torch.zeros((T, n), device=device).double(), torch.zeros((T, n), device=device).double()
+    dots = torch.zeros((T, k), device=device).double()
+    for e in range(E):
+        r, m_ = product(xq, xs, w[e], ws[e], 128)
+        for j in range(k):
+            mine = (ids[:, j] == e)[:, None]
+            ref += torch.where(mine, wt[:, j, None] * r, 0.0)
+            mag += torch.where(mine, wt[:, j, None] * (r.abs() * UBF + (300 + k) * U32 * m_), 0.0)
+            dots[:, j] += torch.where(mine[:, 0], (r * d_out.double()).sum(1), 0.0)
+    # y rounded to bf16, the weights (40 fp32 roundings), the sum, the output's rounding
+    close(out, ref, 1.01 * mag + (UBF + 40 * U32) * ref.abs() + UBF * mag + 1e-30, "out")
+    sl = a["slot_row"].long()
+    yt = y.double()[sl].view(T, k, n)
+    terms = yt * d_out.double()[:, None, :]
+    close(dwt, terms.sum(2), (n / 64 + 8) * U32 * terms.abs().sum(2), "d_weights")
+    lref, lmag = route_reference(lg, True, a["topk_ids"], dwt)
+    close(dlg, lref, 2 * (12 + 30) * U32 * lmag + 1e-37, "d_logits")
+    want = (d_out.double()[:, None, :] * a["topk_weights"].double()[:, :, None]).view(T * k, n)
+    close(dy[sl], want, (UBF + 2 * U32) * want.abs(), "d_rows")
+
+
+def test_chain_on_another_stream(device):
+    """A stream argument and a current stream other than the default give the same bits."""
+    args = chain_inputs(device, seed=20)
+    ref = chain(*args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = chain(*args, stream=side)
+    with torch.cuda.stream(side):
+        inside = chain(*args)
+    torch.cuda.synchronize()
+    used = int(ref[0]["num_tiles"]) * args[0].block_m
+    for r in (got, inside):
+        for i in (2, 4, 5):
+            assert torch.equal(r[i], ref[i])
+        for i in (1, 3):
+            assert torch.equal(r[i][:used], ref[i][:used])
+
+
+def test_chain_in_a_graph(device):
+    """Captured once, replayed on new inputs, with eager work between the replays."""
+    args = chain_inputs(device, seed=21)
+    p, lg, x, w, ws, d_out = args
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        chain(*args)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = chain(*args)
+    for rep in range(4):
+        _, lg2, x2, _, _, d2 = chain_inputs(device, seed=30 + rep)
+        lg.copy_(lg2), x.copy_(x2), d_out.copy_(d2)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = chain(*args)
+        torch.cuda.synchronize()
+        for i in (2, 4, 5):
+            assert torch.equal(held[i], eager[i]), (rep, i)
+
+
+def test_weight_gradient(device):
+    """d_w = d_y^T x from operands quantised along the tokens (an odd number of them), against the
+    product of the dequantised operands and, within e4m3's rounding, of the operands themselves."""
+    m, n, k = 333, 72, 136
+    g = gen(device, 22)
+    dy = torch.randn((m, n), generator=g, device=device).bfloat16()
+    x = torch.randn((m, k), generator=g, device=device).bfloat16()
+    a, sa = moe.quantize_cols_e4m3(dy)
+    b, sb = moe.quantize_cols_e4m3(x)
+    dw = moe.gemm_e4m3(a, sa, b, sb, out_dtype=torch.float32, b_block=1)
+    torch.cuda.synchronize()
+    ref, mag = product(a, sa, b, sb, 1)
+    close(dw, ref, gemm_tol(ref, mag, a.shape[1], "f32"), "d_w")
+    full, fmag = dy.double().t() @ x.double(), dy.double().abs().t() @ x.double().abs()
+    sub = sa.double().amax(1)[:, None] * 2.0 ** -10 * 448 * m  # what underflows to the subnormal grid
+    tol = (2 * 2.0 ** -4 + 2.0 ** -8) * fmag * 1.01 + sub
+    close(dw, full, tol, "d_w of the unquantised operands")
+    # the gradient with respect to the input: the same product with the weight laid out transposed
+    wq, wsc = row_codes(torch.randn((256, 128), generator=g, device=device))
+    blk = torch.rand((2, 1), generator=g, device=device) + 0.1
+    dq, ds = row_codes(torch.randn((50, 256), generator=g, device=device))
+    dx = moe.gemm_e4m3(dq, ds, wq.view(torch.uint8).t().contiguous(), blk.t().contiguous(),
+                       out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    d64 = dq.double() * ds.double().repeat_interleave(128, 1)
+    w64 = wq.double() * blk.double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+    close(dx, d64 @ w64, gemm_tol(d64 @ w64, d64.abs() @ w64.abs(), 256, "f32"), "d_x")
