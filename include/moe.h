@@ -417,23 +417,15 @@ int moe_quantize_cols_e4m3(int32_t m, int32_t n, const void* x, uint8_t* xq, flo
  * ceil(m/16) * ceil(n/16) <= 2^30 (MOE_ERR_SHAPE otherwise).
  * In:  a uint8 [m, k] (e4m3 codes), a_scales fp32 [m, k/128]; b uint8 [n, k], b_scales
  * Out: c c_dtype [m, n]
- * workspace: NULL, or device memory of at least moe_gemm_e4m3_workspace_bytes(m, n, k) bytes,
- *      256-byte aligned (MOE_ERR_WORKSPACE / MOE_ERR_ALIGN otherwise): caller-owned scratch,
- *      contents unspecified afterwards; calls that share one must not overlap.  With it, products
- *      too small to fill the GPU are cut along k, their fp32 parts added in a fixed order: the
- *      result is deterministic, but its rounding differs from a call without workspace.
+ * Deterministic: the order of the additions depends on the sizes alone.
  */
 int moe_gemm_e4m3(int32_t m, int32_t n, int32_t k, const uint8_t* a, const float* a_scales,
                   const uint8_t* b, const float* b_scales, int32_t b_block, void* c,
-                  int32_t c_dtype, void* workspace, size_t workspace_bytes, void* stream);
-
-/* Bytes of the optional workspace of moe_gemm_e4m3 (0: such a product never uses one);
- * negative moe_status for sizes that moe_gemm_e4m3 refuses. */
-int64_t moe_gemm_e4m3_workspace_bytes(int32_t m, int32_t n, int32_t k);
+                  int32_t c_dtype, void* stream);
 
 /*
  * moe_grouped_gemm_e4m3 -- the same product over expert-sorted rows, each with its expert's w:
- * for every valid tile (e, row0) and row r in [row0, row0+block_m):
+ * for every valid tile (e, row0) and row r in [row0, row0+block_m) that holds a slot:
  *   out[r, j] = sum over groups g of row_scales[r, g] * w_scales[e, j/128, g]
  *               * ( rows[r, g-group] . w[e, j, g-group] )
  * Unlike moe_grouped_gemm_up and _down it takes and leaves rows in sorted order, of any widths
@@ -445,15 +437,16 @@ int64_t moe_gemm_e4m3_workspace_bytes(int32_t m, int32_t n, int32_t k);
  * (MOE_ERR_SHAPE otherwise).
  * In:  rows uint8 [moe_max_padded_slots, k] (e4m3 codes), row_scales fp32
  *      [moe_max_padded_slots, k/128]; w uint8 [E, n, k]; w_scales fp32 [E, ceil(n/128), k/128];
- *      offsets, tiles, num_tiles: outputs of moe_align for the same problem
+ *      sorted_slots, offsets, tiles, num_tiles: outputs of moe_align for the same problem
  * Out: out out_dtype (MOE_F32 or MOE_BF16) [moe_max_padded_slots, n]: every row of a valid tile
- *      is written (what its row of `rows` gives: zeros for the padding that moe_permute writes);
- *      rows past the last valid tile are left untouched.
+ *      is written, those that hold no slot as zeros, whatever `rows` has there; rows past the
+ *      last valid tile are left untouched.
  */
 int moe_grouped_gemm_e4m3(const moe_problem* p, int32_t n, int32_t k, const uint8_t* rows,
                           const float* row_scales, const uint8_t* w, const float* w_scales,
-                          const int32_t* offsets, const int32_t* tiles, const int32_t* num_tiles,
-                          void* out, int32_t out_dtype, void* stream);
+                          const int32_t* sorted_slots, const int32_t* offsets,
+                          const int32_t* tiles, const int32_t* num_tiles, void* out,
+                          int32_t out_dtype, void* stream);
 
 /*
  * moe_forward -- the whole layer: align, [quantise X], up, down, combine.

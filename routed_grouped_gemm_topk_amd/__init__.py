@@ -38,7 +38,6 @@ from ._lib import (  # noqa: F401
     moe_forward,
     moe_forward_scratch,
     moe_gemm_e4m3,
-    moe_gemm_e4m3_workspace_bytes,
     moe_grouped_gemm_down,
     moe_grouped_gemm_e4m3,
     moe_grouped_gemm_up,
@@ -205,24 +204,15 @@ def quantize_cols_e4m3(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torc
     return xq, scales
 
 
-def alloc_gemm_e4m3_workspace(m: int, n: int, k: int, device) -> Optional[torch.Tensor]:
-    """The optional workspace of moe_gemm_e4m3 (None when such a product uses none)."""
-    b = moe_gemm_e4m3_workspace_bytes(m, n, k)
-    return torch.empty(b, dtype=torch.uint8, device=device) if b > 0 else None
-
-
 def gemm_e4m3(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
               out_dtype: torch.dtype = torch.bfloat16, b_block: int = 128,
-              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-              stream=None) -> torch.Tensor:
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """a [m, k] times b [n, k] transposed, both e4m3 codes with one scale per 128 values along k,
-    through moe_gemm_e4m3.  Allocates `out` / `workspace` if not given."""
-    with _on(stream):
-        if out is None:
+    through moe_gemm_e4m3."""
+    if out is None:
+        with _on(stream):
             out = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype, device=a.device)
-        if workspace is None:
-            workspace = alloc_gemm_e4m3_workspace(a.shape[0], b.shape[0], a.shape[1], a.device)
-    moe_gemm_e4m3(a, a_scales, b, b_scales, b_block, out, workspace, stream)
+    moe_gemm_e4m3(a, a_scales, b, b_scales, b_block, out, stream)
     return out
 
 
@@ -235,6 +225,6 @@ def grouped_gemm_e4m3(p: Problem, rows: torch.Tensor, row_scales: torch.Tensor, 
         with _on(stream):
             out = torch.empty((moe_max_padded_slots(p), w.shape[1]), dtype=out_dtype,
                               device=rows.device)
-    moe_grouped_gemm_e4m3(p, rows, row_scales, w, w_scales, a["offsets"], a["tiles"],
-                          a["num_tiles"], out, stream)
+    moe_grouped_gemm_e4m3(p, rows, row_scales, w, w_scales, a["sorted_slots"], a["offsets"],
+                          a["tiles"], a["num_tiles"], out, stream)
     return out

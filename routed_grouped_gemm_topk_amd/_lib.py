@@ -36,8 +36,7 @@ EXPORTS = ["moe_status_str", "moe_validate", "moe_pick_block_m", "moe_block_m_fo
            "moe_grouped_gemm_down", "moe_gemm_workspace_bytes",
            "moe_combine", "moe_forward", "moe_scratch_max_bytes", "moe_forward_scratch",
            "moe_permute", "moe_unpermute", "moe_unpermute_bwd", "moe_route_bwd",
-           "moe_quantize_cols_e4m3", "moe_gemm_e4m3", "moe_gemm_e4m3_workspace_bytes",
-           "moe_grouped_gemm_e4m3"]
+           "moe_quantize_cols_e4m3", "moe_gemm_e4m3", "moe_grouped_gemm_e4m3"]
 
 
 class MoeError(RuntimeError):
@@ -105,10 +104,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_unpermute_bwd": (ctypes.c_int, [P, i32] + [vp] * 8 + [vp]),
         "moe_route_bwd": (ctypes.c_int, [P, vp, ctypes.c_int] + [vp] * 3 + [vp]),
         "moe_quantize_cols_e4m3": (ctypes.c_int, [i32] * 2 + [vp] * 3 + [vp]),
-        "moe_gemm_e4m3": (ctypes.c_int, [i32] * 3 + [vp] * 4 + [i32, vp, i32, vp,
-                                                                 ctypes.c_size_t, vp]),
-        "moe_gemm_e4m3_workspace_bytes": (ctypes.c_int64, [i32] * 3),
-        "moe_grouped_gemm_e4m3": (ctypes.c_int, [P, i32, i32] + [vp] * 8 + [i32, vp]),
+        "moe_gemm_e4m3": (ctypes.c_int, [i32] * 3 + [vp] * 4 + [i32, vp, i32, vp]),
+        "moe_grouped_gemm_e4m3": (ctypes.c_int, [P, i32, i32] + [vp] * 9 + [i32, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -447,11 +444,7 @@ def moe_quantize_cols_e4m3(x, xq, scales, stream=None) -> None:
     _checked(load().moe_quantize_cols_e4m3(m, n, *args, _stream(stream)), "moe_quantize_cols_e4m3")
 
 
-def moe_gemm_e4m3_workspace_bytes(m: int, n: int, k: int) -> int:
-    return _checked(load().moe_gemm_e4m3_workspace_bytes(m, n, k), "moe_gemm_e4m3_workspace_bytes")
-
-
-def moe_gemm_e4m3(a, a_scales, b, b_scales, b_block: int, c, workspace=None, stream=None) -> None:
+def moe_gemm_e4m3(a, a_scales, b, b_scales, b_block: int, c, stream=None) -> None:
     for name, t in (("a", a), ("b", b)):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
             raise ValueError(f"{name}: expected a matrix")
@@ -463,14 +456,12 @@ def moe_gemm_e4m3(a, a_scales, b, b_scales, b_block: int, c, workspace=None, str
             _mat(a_scales, "a_scales", torch.float32, (m, k // 128), dev),
             _mat(b, "b", _CODES, (n, k), dev),
             _mat(b_scales, "b_scales", torch.float32, (sb, k // 128), dev), int(b_block),
-            _mat(c, "c", (torch.float32, torch.bfloat16), (m, n), dev), _row_dtype(c, "c"),
-            _ptr(workspace, "workspace", torch.uint8, device=dev),
-            0 if workspace is None else workspace.numel()]
+            _mat(c, "c", (torch.float32, torch.bfloat16), (m, n), dev), _row_dtype(c, "c")]
     _checked(load().moe_gemm_e4m3(m, n, k, *args, _stream(stream)), "moe_gemm_e4m3")
 
 
-def moe_grouped_gemm_e4m3(p: Problem, rows, row_scales, w, w_scales, offsets, tiles, num_tiles,
-                          out, stream=None) -> None:
+def moe_grouped_gemm_e4m3(p: Problem, rows, row_scales, w, w_scales, sorted_slots, offsets, tiles,
+                          num_tiles, out, stream=None) -> None:
     if not isinstance(w, torch.Tensor) or w.dim() != 3 or w.shape[0] != p.E:
         raise ValueError("w: expected [E, n, k]")
     n, k = w.shape[1:]
@@ -480,6 +471,7 @@ def moe_grouped_gemm_e4m3(p: Problem, rows, row_scales, w, w_scales, offsets, ti
             _mat(row_scales, "row_scales", torch.float32, (rm, k // 128), dev),
             _ptr(w, "w", _CODES, device=dev),
             _mat(w_scales, "w_scales", torch.float32, (p.E, -(-n // 128), k // 128), dev),
+            _ptr(sorted_slots, "sorted_slots", torch.int32, rm, dev),
             _ptr(offsets, "offsets", torch.int32, p.E + 1, dev),
             _ptr(tiles, "tiles", torch.int32, 2 * moe_max_tiles(p), dev),
             _ptr(num_tiles, "num_tiles", torch.int32, 1, dev),

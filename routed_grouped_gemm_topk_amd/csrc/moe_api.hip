@@ -507,34 +507,25 @@ int moe_quantize_cols_e4m3(int32_t m, int32_t n, const void* x, uint8_t* xq, flo
   return status_of(launch_quant_cols(m, n, x, xq, scales, (hipStream_t)stream));
 }
 
-int64_t moe_gemm_e4m3_workspace_bytes(int32_t m, int32_t n, int32_t k) {
-  const int v = validate_gemm(m, n, k);
-  return v != MOE_OK ? v : gemm_e4m3_split_bytes(m, n, k);
-}
-
 int moe_gemm_e4m3(int32_t m, int32_t n, int32_t k, const uint8_t* a, const float* a_scales,
                   const uint8_t* b, const float* b_scales, int32_t b_block, void* c,
-                  int32_t c_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+                  int32_t c_dtype, void* stream) {
   int v = validate_gemm(m, n, k);
   if (v) return v;
   if (b_block != 1 && b_block != kGroup) return MOE_ERR_SHAPE;
   if (c_dtype != MOE_F32 && c_dtype != MOE_BF16) return MOE_ERR_DTYPE;
   if (!a || !a_scales || !b || !b_scales || !c) return MOE_ERR_NULL;
-  const int64_t split = gemm_e4m3_split_bytes(m, n, k);
-  if (workspace && (int64_t)workspace_bytes < split) return MOE_ERR_WORKSPACE;
-  if ((v = check_align({{a, 16}, {a_scales, 4}, {b, 16}, {b_scales, 4}, {c, 16},
-                        {workspace, 256}})))
-    return v;
+  if ((v = check_align({{a, 16}, {a_scales, 4}, {b, 16}, {b_scales, 4}, {c, 16}}))) return v;
   if ((v = check_device())) return v;
   return status_of(launch_gemm_e4m3(m, n, k, a, a_scales, b, b_scales, b_block == 1, c,
-                                    c_dtype == MOE_F32, split > 0 ? workspace : nullptr,
-                                    (hipStream_t)stream));
+                                    c_dtype == MOE_F32, (hipStream_t)stream));
 }
 
 int moe_grouped_gemm_e4m3(const moe_problem* p, int32_t n, int32_t k, const uint8_t* rows,
                           const float* row_scales, const uint8_t* w, const float* w_scales,
-                          const int32_t* offsets, const int32_t* tiles, const int32_t* num_tiles,
-                          void* out, int32_t out_dtype, void* stream) {
+                          const int32_t* sorted_slots, const int32_t* offsets,
+                          const int32_t* tiles, const int32_t* num_tiles, void* out,
+                          int32_t out_dtype, void* stream) {
   int v = validate(p);
   if (v) return v;
   if (p->dtype != MOE_BF16 || p->w_dtype != MOE_E4M3) return MOE_ERR_DTYPE;
@@ -544,15 +535,16 @@ int moe_grouped_gemm_e4m3(const moe_problem* p, int32_t n, int32_t k, const uint
     return MOE_ERR_SHAPE;
   const Resolved r = resolve(p);
   if (r.tiles_max * ((n + 15) / 16) > kMaxGemmTiles) return MOE_ERR_SHAPE;   // grid bound
-  if (!rows || !row_scales || !w || !w_scales || !offsets || !tiles || !num_tiles || !out)
+  if (!rows || !row_scales || !w || !w_scales || !sorted_slots || !offsets || !tiles ||
+      !num_tiles || !out)
     return MOE_ERR_NULL;
-  if ((v = check_align({{rows, 16}, {row_scales, 4}, {w, 16}, {w_scales, 4}, {offsets, 4},
-                        {tiles, 4}, {num_tiles, 4}, {out, 16}})))
+  if ((v = check_align({{rows, 16}, {row_scales, 4}, {w, 16}, {w_scales, 4}, {sorted_slots, 4},
+                        {offsets, 4}, {tiles, 4}, {num_tiles, 4}, {out, 16}})))
     return v;
   if ((v = check_device())) return v;
-  return status_of(launch_grouped_gemm_e4m3(r, n, k, rows, row_scales, w, w_scales, offsets,
-                                            tiles, num_tiles, out, out_dtype == MOE_F32,
-                                            (hipStream_t)stream));
+  return status_of(launch_grouped_gemm_e4m3(r, n, k, rows, row_scales, w, w_scales,
+                                            sorted_slots, offsets, tiles, num_tiles, out,
+                                            out_dtype == MOE_F32, (hipStream_t)stream));
 }
 
 int moe_forward(const moe_problem* p, const void* x, const int32_t* topk_ids,

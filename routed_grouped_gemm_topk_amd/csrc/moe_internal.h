@@ -296,15 +296,15 @@ hipError_t launch_route_bwd(const Resolved& r, const float* logits, int renorm,
 // Products of e4m3 codes with one scale per 128 values (moe_gemm_e4m3.hip).
 hipError_t launch_quant_cols(int M, int C, const void* x, uint8_t* xq, float* scales,
                              hipStream_t s);
-int64_t gemm_e4m3_split_bytes(int M, int N, int K);
 hipError_t launch_gemm_e4m3(int M, int N, int K, const uint8_t* a, const float* sa,
                             const uint8_t* b, const float* sb, bool b_rows, void* c, bool c_f32,
-                            void* split_ws, hipStream_t s);
+                            hipStream_t s);
 hipError_t launch_grouped_gemm_e4m3(const Resolved& r, int N, int K, const uint8_t* rows,
                                     const float* row_scales, const uint8_t* w,
-                                    const float* w_scales, const int32_t* offsets,
-                                    const int32_t* tiles, const int32_t* num_tiles, void* out,
-                                    bool out_f32, hipStream_t s);
+                                    const float* w_scales, const int32_t* sorted_slots,
+                                    const int32_t* offsets, const int32_t* tiles,
+                                    const int32_t* num_tiles, void* out, bool out_f32,
+                                    hipStream_t s);
 hipError_t launch_combine(const Resolved& r, const void* slot_out, const int32_t* slot_row,
                           void* out, hipStream_t s);
 

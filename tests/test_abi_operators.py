@@ -7,8 +7,7 @@ import torch
 
 import routed_grouped_gemm_topk_amd as moe
 
-S, D, N, A, W = (moe.MOE_ERR_SHAPE, moe.MOE_ERR_DTYPE, moe.MOE_ERR_NULL, moe.MOE_ERR_ALIGN,
-                 moe.MOE_ERR_WORKSPACE)
+S, D, N, A = moe.MOE_ERR_SHAPE, moe.MOE_ERR_DTYPE, moe.MOE_ERR_NULL, moe.MOE_ERR_ALIGN
 F32, BF16, E4M3 = moe.MOE_F32, moe.MOE_BF16, moe.MOE_E4M3
 ok, odd8, odd2 = (ctypes.c_void_p(4096 + d) for d in (0, 8, 2))
 
@@ -89,16 +88,12 @@ def test_quantize_cols(lib):
 
 
 def test_gemm(lib):
-    def call(m=16, n=32, k=256, ptr=(ok,) * 4, block=128, c=ok, dt=BF16, ws=None, nb=0):
-        return lib.moe_gemm_e4m3(m, n, k, *ptr, block, c, dt, ws, nb, None)
+    def call(m=16, n=32, k=256, ptr=(ok,) * 4, block=128, c=ok, dt=BF16):
+        return lib.moe_gemm_e4m3(m, n, k, *ptr, block, c, dt, None)
     for kw in [dict(m=0), dict(n=0), dict(k=0), dict(k=64), dict(k=200), dict(m=-5),
                dict(m=2 ** 24 + 1), dict(n=2 ** 24 + 1), dict(k=2 ** 22 + 128),
                dict(m=2 ** 24, n=2 ** 24), dict(block=64), dict(block=0)]:
         assert call(**kw) == S, kw
-    for kw in [dict(m=0), dict(k=200), dict(m=2 ** 24, n=2 ** 24)]:
-        a = dict(m=16, n=32, k=256)
-        a.update(kw)
-        assert lib.moe_gemm_e4m3_workspace_bytes(a["m"], a["n"], a["k"]) == S
     assert call(dt=E4M3) == D and call(dt=9) == D
     for i in range(4):
         p = [ok] * 4
@@ -107,26 +102,20 @@ def test_gemm(lib):
         p[i] = odd8 if i in (0, 2) else odd2
         assert call(ptr=p) == A
     assert call(c=None) == N and call(c=odd8) == A
-    assert call(ws=ctypes.c_void_p(4096 + 64), nb=1 << 40) == A
-    for m, n, k in [(16, 32, 256), (300, 512, 7168), (4096, 4096, 4096)]:
-        need = lib.moe_gemm_e4m3_workspace_bytes(m, n, k)
-        assert need >= 0 and need % 256 == 0
-        if need:
-            assert call(m=m, n=n, k=k, ws=ok, nb=need - 1) == W
 
 
 def test_grouped_gemm(lib):
     P8 = problem(H=256, w_dtype="e4m3")
 
-    def call(P=P8, n=32, k=256, ptr=(ok,) * 7, out=ok, dt=BF16):
+    def call(P=P8, n=32, k=256, ptr=(ok,) * 8, out=ok, dt=BF16):
         return lib.moe_grouped_gemm_e4m3(P, n, k, *ptr, out, dt, None)
     assert call(P=problem()) == D and call(P=problem(dtype="f32")) == D
     assert call(dt=E4M3) == D
     assert call(P=problem(H=192, w_dtype="e4m3")) == S
     for kw in [dict(n=0), dict(k=0), dict(k=192), dict(n=32769), dict(k=32768 + 128), dict(n=-1)]:
         assert call(**kw) == S, kw
-    for i in range(7):
-        p = [ok] * 7
+    for i in range(8):
+        p = [ok] * 8
         p[i] = None
         assert call(ptr=p) == N
         p[i] = odd8 if i in (0, 2) else odd2
