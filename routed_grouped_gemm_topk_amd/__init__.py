@@ -124,10 +124,13 @@ def forward(p: Problem, x, topk_ids, topk_weights, w13, w2, w13_scales=None, w2_
 # rows in expert-sorted order, gradients, products of e4m3 codes.  `a` is the alignment that
 # align() or route_align() returns for the same problem.
 # ---------------------------------------------------------------------------------------------
+_HERE = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocate on the stream that the call runs on, so that the buffers' memory belongs to it."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     if stream.device_index != torch.cuda.current_device():

@@ -9,6 +9,7 @@ If libmoe.so is missing, loading raises -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -164,7 +165,8 @@ def moe_gemm_workspace_bytes(p: Problem) -> int:
 # ---------------------------------------------------------------------------------------------
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a torch.cuda.Stream around it costs 3 us per call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -350,15 +352,15 @@ def moe_forward_scratch(p: Problem, x, topk_ids, topk_weights, w13, w13_scales, 
 
 # ---------------------------------------------------------------------------------------------
 # rows in expert-sorted order, gradients, products of e4m3 codes.  Every tensor of a call must be
-# on the current device: the launch goes to that device's stream.
+# on the current device: the launch goes to that device's stream.  A call's host time is that of
+# these checks next to 4 us of launch, so the common case of each is one expression (0.4 us a
+# tensor) and only a tensor that fails it is looked at again, for the reason.
 # ---------------------------------------------------------------------------------------------
 _ROW_DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_E4M3,
            torch.uint8: MOE_E4M3}
 _CODES = (torch.uint8, torch.float8_e4m3fn)
-
-
-def _here() -> torch.device:
-    return torch.device("cuda", torch.cuda.current_device())
+_F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+_OUT = (torch.float32, torch.bfloat16)
 
 
 def _row_dtype(t: torch.Tensor, name: str) -> int:
@@ -368,68 +370,81 @@ def _row_dtype(t: torch.Tensor, name: str) -> int:
     return dt
 
 
-def _mat(t: Optional[torch.Tensor], name: str, dtype, shape, device):
-    """_ptr with the whole shape checked."""
-    if isinstance(t, torch.Tensor) and tuple(t.shape) != tuple(shape):
+def _arg(t: Optional[torch.Tensor], name: str, dtypes: tuple, numel: int, dev: int):
+    """Device pointer of a contiguous tensor of `numel` elements on device `dev` (None: NULL)."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in dtypes
+            and t.numel() == numel and t.is_contiguous()):
+        return t.data_ptr()
+    _ptr(t, name, dtypes, numel, torch.device("cuda", dev))
+    raise ValueError(f"{name}: not a dense tensor of {numel} elements on device {dev}")
+
+
+def _mat(t: Optional[torch.Tensor], name: str, dtypes: tuple, shape: tuple, dev: int):
+    """_arg with the whole shape checked."""
+    if isinstance(t, torch.Tensor) and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return _ptr(t, name, dtype, device=device)
+    return _arg(t, name, dtypes, math.prod(shape), dev)
 
 
 def moe_permute(p: Problem, x, x_scales, slot_row, sorted_slots, num_tiles, rows, row_scales,
                 stream=None) -> None:
     dt = _row_dtype(x, "x")
-    same = _CODES if dt == MOE_E4M3 else x.dtype
+    same = _CODES if dt == MOE_E4M3 else (x.dtype,)
     rm = moe_max_padded_slots(p)
-    dev = _here()
-    args = [_ptr(x, "x", same, p.T * p.H, dev),
-            _ptr(x_scales, "x_scales", torch.float32, p.T * (p.H // 128), dev),
-            _ptr(slot_row, "slot_row", torch.int32, p.T * p.top_k, dev),
-            _ptr(sorted_slots, "sorted_slots", torch.int32, rm, dev),
-            _ptr(num_tiles, "num_tiles", torch.int32, 1, dev),
-            _ptr(rows, "rows", same, rm * p.H, dev),
-            _ptr(row_scales, "row_scales", torch.float32, rm * (p.H // 128), dev)]
-    _checked(load().moe_permute(ctypes.byref(p), dt, *args, _stream(stream)), "moe_permute")
+    dev = torch.cuda.current_device()
+    T, H = p.T, p.H
+    _checked(load().moe_permute(
+        ctypes.byref(p), dt, _arg(x, "x", same, T * H, dev),
+        _arg(x_scales, "x_scales", _F32, T * (H // 128), dev),
+        _arg(slot_row, "slot_row", _I32, T * p.top_k, dev),
+        _arg(sorted_slots, "sorted_slots", _I32, rm, dev),
+        _arg(num_tiles, "num_tiles", _I32, 1, dev), _arg(rows, "rows", same, rm * H, dev),
+        _arg(row_scales, "row_scales", _F32, rm * (H // 128), dev), _stream(stream)),
+        "moe_permute")
 
 
 def moe_unpermute(p: Problem, rows, slot_row, topk_weights, out, stream=None) -> None:
     dt = _row_dtype(rows, "rows")
-    rm = moe_max_padded_slots(p)
-    dev = _here()
-    N = p.T * p.top_k
-    args = [_ptr(rows, "rows", rows.dtype, rm * p.H, dev),
-            _ptr(slot_row, "slot_row", torch.int32, N, dev),
-            _ptr(topk_weights, "topk_weights", torch.float32, N, dev),
-            _ptr(out, "out", rows.dtype, p.T * p.H, dev)]
-    _checked(load().moe_unpermute(ctypes.byref(p), dt, *args, _stream(stream)), "moe_unpermute")
+    same = (rows.dtype,)
+    dev = torch.cuda.current_device()
+    T, H = p.T, p.H
+    N = T * p.top_k
+    _checked(load().moe_unpermute(
+        ctypes.byref(p), dt, _arg(rows, "rows", same, moe_max_padded_slots(p) * H, dev),
+        _arg(slot_row, "slot_row", _I32, N, dev),
+        _arg(topk_weights, "topk_weights", _F32, N, dev), _arg(out, "out", same, T * H, dev),
+        _stream(stream)), "moe_unpermute")
 
 
 def moe_unpermute_bwd(p: Problem, d_out, rows, slot_row, sorted_slots, num_tiles, topk_weights,
                       d_rows, d_weights, stream=None) -> None:
     dt = _row_dtype(d_out, "d_out")
+    same = (d_out.dtype,)
     rm = moe_max_padded_slots(p)
-    dev = _here()
-    N = p.T * p.top_k
-    args = [_ptr(d_out, "d_out", d_out.dtype, p.T * p.H, dev),
-            _ptr(rows, "rows", d_out.dtype, rm * p.H, dev),
-            _ptr(slot_row, "slot_row", torch.int32, N, dev),
-            _ptr(sorted_slots, "sorted_slots", torch.int32, rm, dev),
-            _ptr(num_tiles, "num_tiles", torch.int32, 1, dev),
-            _ptr(topk_weights, "topk_weights", torch.float32, N, dev),
-            _ptr(d_rows, "d_rows", d_out.dtype, rm * p.H, dev),
-            _ptr(d_weights, "d_weights", torch.float32, N, dev)]
-    _checked(load().moe_unpermute_bwd(ctypes.byref(p), dt, *args, _stream(stream)),
-             "moe_unpermute_bwd")
+    dev = torch.cuda.current_device()
+    T, H = p.T, p.H
+    N = T * p.top_k
+    _checked(load().moe_unpermute_bwd(
+        ctypes.byref(p), dt, _arg(d_out, "d_out", same, T * H, dev),
+        _arg(rows, "rows", same, rm * H, dev), _arg(slot_row, "slot_row", _I32, N, dev),
+        _arg(sorted_slots, "sorted_slots", _I32, rm, dev),
+        _arg(num_tiles, "num_tiles", _I32, 1, dev),
+        _arg(topk_weights, "topk_weights", _F32, N, dev),
+        _arg(d_rows, "d_rows", same, rm * H, dev), _arg(d_weights, "d_weights", _F32, N, dev),
+        _stream(stream)), "moe_unpermute_bwd")
 
 
 def moe_route_bwd(p: Problem, logits, renormalize: bool, topk_ids, d_weights, d_logits,
                   stream=None) -> None:
-    dev = _here()
-    N = p.T * p.top_k
-    args = [_ptr(logits, "logits", torch.float32, p.T * p.E, dev), 1 if renormalize else 0,
-            _ptr(topk_ids, "topk_ids", torch.int32, N, dev),
-            _ptr(d_weights, "d_weights", torch.float32, N, dev),
-            _ptr(d_logits, "d_logits", torch.float32, p.T * p.E, dev)]
-    _checked(load().moe_route_bwd(ctypes.byref(p), *args, _stream(stream)), "moe_route_bwd")
+    dev = torch.cuda.current_device()
+    T = p.T
+    N, L = T * p.top_k, T * p.E
+    _checked(load().moe_route_bwd(
+        ctypes.byref(p), _arg(logits, "logits", _F32, L, dev), 1 if renormalize else 0,
+        _arg(topk_ids, "topk_ids", _I32, N, dev), _arg(d_weights, "d_weights", _F32, N, dev),
+        _arg(d_logits, "d_logits", _F32, L, dev), _stream(stream)), "moe_route_bwd")
 
 
 def moe_quantize_cols_e4m3(x, xq, scales, stream=None) -> None:
@@ -437,11 +452,11 @@ def moe_quantize_cols_e4m3(x, xq, scales, stream=None) -> None:
         raise ValueError("x: expected a matrix")
     m, n = x.shape
     groups = -(-m // 128)
-    dev = _here()
-    args = [_ptr(x, "x", torch.bfloat16, device=dev),
-            _mat(xq, "xq", _CODES, (n, groups * 128), dev),
-            _mat(scales, "scales", torch.float32, (n, groups), dev)]
-    _checked(load().moe_quantize_cols_e4m3(m, n, *args, _stream(stream)), "moe_quantize_cols_e4m3")
+    dev = torch.cuda.current_device()
+    _checked(load().moe_quantize_cols_e4m3(
+        m, n, _arg(x, "x", _BF16, m * n, dev), _mat(xq, "xq", _CODES, (n, groups * 128), dev),
+        _mat(scales, "scales", _F32, (n, groups), dev), _stream(stream)),
+        "moe_quantize_cols_e4m3")
 
 
 def moe_gemm_e4m3(a, a_scales, b, b_scales, b_block: int, c, stream=None) -> None:
@@ -450,31 +465,29 @@ def moe_gemm_e4m3(a, a_scales, b, b_scales, b_block: int, c, stream=None) -> Non
             raise ValueError(f"{name}: expected a matrix")
     m, k = a.shape
     n = b.shape[0]
-    dev = _here()
+    dev = torch.cuda.current_device()
     sb = n if b_block == 1 else -(-n // 128)
-    args = [_ptr(a, "a", _CODES, device=dev),
-            _mat(a_scales, "a_scales", torch.float32, (m, k // 128), dev),
-            _mat(b, "b", _CODES, (n, k), dev),
-            _mat(b_scales, "b_scales", torch.float32, (sb, k // 128), dev), int(b_block),
-            _mat(c, "c", (torch.float32, torch.bfloat16), (m, n), dev), _row_dtype(c, "c")]
-    _checked(load().moe_gemm_e4m3(m, n, k, *args, _stream(stream)), "moe_gemm_e4m3")
+    _checked(load().moe_gemm_e4m3(
+        m, n, k, _arg(a, "a", _CODES, m * k, dev),
+        _mat(a_scales, "a_scales", _F32, (m, k // 128), dev), _mat(b, "b", _CODES, (n, k), dev),
+        _mat(b_scales, "b_scales", _F32, (sb, k // 128), dev), int(b_block),
+        _mat(c, "c", _OUT, (m, n), dev), _row_dtype(c, "c"), _stream(stream)), "moe_gemm_e4m3")
 
 
 def moe_grouped_gemm_e4m3(p: Problem, rows, row_scales, w, w_scales, sorted_slots, offsets, tiles,
                           num_tiles, out, stream=None) -> None:
     if not isinstance(w, torch.Tensor) or w.dim() != 3 or w.shape[0] != p.E:
         raise ValueError("w: expected [E, n, k]")
-    n, k = w.shape[1:]
+    E, n, k = w.shape
     rm = moe_max_padded_slots(p)
-    dev = _here()
-    args = [_mat(rows, "rows", _CODES, (rm, k), dev),
-            _mat(row_scales, "row_scales", torch.float32, (rm, k // 128), dev),
-            _ptr(w, "w", _CODES, device=dev),
-            _mat(w_scales, "w_scales", torch.float32, (p.E, -(-n // 128), k // 128), dev),
-            _ptr(sorted_slots, "sorted_slots", torch.int32, rm, dev),
-            _ptr(offsets, "offsets", torch.int32, p.E + 1, dev),
-            _ptr(tiles, "tiles", torch.int32, 2 * moe_max_tiles(p), dev),
-            _ptr(num_tiles, "num_tiles", torch.int32, 1, dev),
-            _mat(out, "out", (torch.float32, torch.bfloat16), (rm, n), dev)]
-    _checked(load().moe_grouped_gemm_e4m3(ctypes.byref(p), n, k, *args, _row_dtype(out, "out"),
-                                          _stream(stream)), "moe_grouped_gemm_e4m3")
+    dev = torch.cuda.current_device()
+    _checked(load().moe_grouped_gemm_e4m3(
+        ctypes.byref(p), n, k, _mat(rows, "rows", _CODES, (rm, k), dev),
+        _mat(row_scales, "row_scales", _F32, (rm, k // 128), dev),
+        _arg(w, "w", _CODES, E * n * k, dev),
+        _mat(w_scales, "w_scales", _F32, (E, -(-n // 128), k // 128), dev),
+        _arg(sorted_slots, "sorted_slots", _I32, rm, dev),
+        _arg(offsets, "offsets", _I32, E + 1, dev),
+        _arg(tiles, "tiles", _I32, 2 * moe_max_tiles(p), dev),
+        _arg(num_tiles, "num_tiles", _I32, 1, dev), _mat(out, "out", _OUT, (rm, n), dev),
+        _row_dtype(out, "out"), _stream(stream)), "moe_grouped_gemm_e4m3")

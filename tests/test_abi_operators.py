@@ -127,11 +127,16 @@ def test_binding_refuses_wrong_tensors():
     """Host tensors, wrong types and shapes are refused before the library is called."""
     p = moe.make_problem(4, 128, 128, 8, 2, "bf16")
     with pytest.raises(ValueError):
-        moe._lib._mat(torch.zeros(4, 4), "x", torch.float32, (4, 5), None)
+        moe._lib._mat(torch.zeros(4, 4), "x", (torch.float32,), (4, 5), 0)
     with pytest.raises(ValueError):
         moe._lib._row_dtype(torch.zeros(4, dtype=torch.float16), "x")
     with pytest.raises(ValueError):
         moe._lib._row_dtype(None, "x")
+    for t in (torch.zeros(4, 4), torch.zeros(4, 4, dtype=torch.bfloat16), torch.zeros(4, 8)[:, ::2]):
+        with pytest.raises(ValueError):
+            moe._lib._arg(t, "x", (torch.float32,), 16, 0)
+    with pytest.raises(TypeError):
+        moe._lib._arg([1.0], "x", (torch.float32,), 1, 0)
     if torch.cuda.is_available():
         with pytest.raises(ValueError):
             moe.moe_unpermute(p, torch.zeros(2), torch.zeros(2), None, torch.zeros(2))
