@@ -34,6 +34,7 @@ struct Args {
   const int32_t* tiles;
   const int32_t* num_tiles;
   int tiles_max, n_slots;
+  bool past_cache;              // c is larger than the last-level cache
   int M, N, K;
 };
 
@@ -54,6 +55,12 @@ __device__ __forceinline__ i32x4 buf_rsrc(const void* base, uint32_t bytes) {
 // 64 lanes x 16 (4) bytes from the buffer at voff + soff straight to LDS at M0.
 __device__ __forceinline__ void buf_dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               ::"v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
+}
+// The same for memory that is read once: it does not push others out of the caches.
+__device__ __forceinline__ void buf_dma16_once(i32x4 rsrc, uint32_t voff, uint32_t soff,
+                                               uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
                ::"v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
 }
 __device__ __forceinline__ void buf_dma4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
@@ -159,7 +166,11 @@ struct TileGemm {
   static constexpr int OPS = NQW + NSW;
   static constexpr int RING = NS * KG * (STAGE + SSTAGE);
   static constexpr int SUMS = (KG - 1) * NW * FM * FN * kWave * 16;
-  static constexpr int LDS = RING > SUMS ? RING : SUMS;
+  static constexpr int ES = F32 ? 4 : 2;                    // bytes per value of c
+  static constexpr int PITCH = WTN * ES + 16;
+  static constexpr int OUT_OFF = KG > 1 ? SUMS : 0;         // waves' parts of c on their way out
+  static constexpr int OUT = OUT_OFF + NW * 16 * PITCH;
+  static constexpr int LDS = RING > OUT ? RING : OUT;
   // A slice's copies go out in parts: PART of each wave (and the scales) right after the barrier
   // that frees the stage, PART more before each of the next slice's fragments.  All at once they
   // held up the waves' matrix instructions behind the load unit (16 cycles per copy, 72 copies
@@ -172,7 +183,8 @@ struct TileGemm {
   static_assert((NQW + PART - 1) / PART <= FM, "every part goes out within its slice");
 
   // PARTIAL: tiles may hold few rows (a loop of its own for waves that have fragments without any)
-  template <bool PARTIAL>
+  // ONCE: nothing else reads this tile's part of b
+  template <bool PARTIAL, bool ONCE = false>
   __device__ static __forceinline__ void run(const Args& g, const Tile& t, char* lds) {
     const int lane = threadIdx.x & (kWave - 1);
     const int all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -180,10 +192,11 @@ struct TileGemm {
     const int wn = wave % WN, wm = wave / WN;
     const int K = g.K, KT = K / ROWB, steps = (KT + KG - 1) / KG;
 
-    // ---- this wave's copies: rows past the operand's end read as zeros -------------------------
+    // ---- this wave's copies: rows past the operand's end (an offset past the descriptor's) read
+    // as zeros --------------------------------------------------------------------------------
     const i32x4 ra = buf_rsrc(g.a + (size_t)t.row0 * K, (uint32_t)t.rows * (uint32_t)K);
-    const i32x4 rb = buf_rsrc(t.b + (size_t)t.n0 * K, (uint32_t)t.cols * (uint32_t)K);
     const i32x4 rsa = buf_rsrc(g.sa + (size_t)t.row0 * KT, (uint32_t)t.rows * KT * 4);
+    const i32x4 rb = buf_rsrc(t.b + (size_t)t.n0 * K, (uint32_t)t.cols * (uint32_t)K);
     const int sb0 = BROW ? t.n0 : t.n0 / kGroup;
     const int sbn = BROW ? t.cols : (t.n0 % kGroup + t.cols + kGroup - 1) / kGroup;
     const i32x4 rsb = buf_rsrc(t.sb + (size_t)sb0 * KT, (uint32_t)sbn * KT * 4);
@@ -195,8 +208,7 @@ struct TileGemm {
       const int cc = (lane & 7) ^ swz(r);
       const bool is_a = q < BM / 8;
       if (!is_a) r -= BM;
-      voff[i] = r < (is_a ? t.rows : t.cols) && q < NQ_REAL
-                    ? (uint32_t)r * (uint32_t)K + cc * 16 : kPastEnd;
+      voff[i] = q < NQ_REAL ? (uint32_t)r * (uint32_t)K + cc * 16 : kPastEnd;
     }
     uint32_t soff[NSW];
     #pragma unroll
@@ -204,7 +216,7 @@ struct TileGemm {
       const int q = wave * NSW + i;
       const bool is_a = q < SA;
       const int r = (is_a ? q : q - SA) * 64 + lane;
-      soff[i] = r < (is_a ? t.rows : sbn) ? (uint32_t)r * KT * 4 : kPastEnd;
+      soff[i] = q < SA + SB ? (uint32_t)r * KT * 4 : kPastEnd;
     }
     const uint32_t lds_base = lds_u32(lds);
     // part p of the group's slice of `step` into stage buf; past the last slice that one is
@@ -217,7 +229,12 @@ struct TileGemm {
       for (int i = 0; i < NQW; ++i) {
         if (i / PART != p) continue;
         const int q = wave * NQW + i;
-        buf_dma16(q < BM / 8 ? ra : rb, voff[i], (uint32_t)kt * ROWB, st + q * 1024);
+        if constexpr (ONCE) {
+          if (q < BM / 8) buf_dma16(ra, voff[i], (uint32_t)kt * ROWB, st + q * 1024);
+          else buf_dma16_once(rb, voff[i], (uint32_t)kt * ROWB, st + q * 1024);
+        } else {
+          buf_dma16(q < BM / 8 ? ra : rb, voff[i], (uint32_t)kt * ROWB, st + q * 1024);
+        }
       }
       if (p == 0) {
         #pragma unroll
@@ -230,9 +247,10 @@ struct TileGemm {
     };
 
     // ---- fragments (fragment i of wave row wm: rows [(i * WM + wm) * 16, +16), so that a tile
-    // whose rows end early leaves every wave its share): lane holds row lane & 15, bytes [(lane >> 4) * 32, +32) of the slice.  The
-    // lane's addresses (of the two 16-byte chunks and of the scales) step from stage to stage in
-    // place; everything else about an address is an immediate offset. ------------------------------
+    // whose rows end early leaves every wave its share): lane holds row lane & 15, bytes
+    // [(lane >> 4) * 32, +32) of the slice.  The lane's addresses (of the two 16-byte chunks and
+    // of the scales) step from stage to stage in place; everything else about an address is an
+    // immediate offset. -------------------------------------------------------------------------
     const int fr = lane & 15, fq = lane >> 4;
     const uint32_t o0 = fr * ROWB + (((2 * fq) ^ swz(fr)) << 4);
     const uint32_t o1 = fr * ROWB + (((2 * fq + 1) ^ swz(fr)) << 4);
@@ -268,9 +286,9 @@ struct TileGemm {
     f32x4 s4[BROW ? FN : 1], s4p[BROW ? FN : 1];
     float s1 = 0.0f, sa_cur = 0.0f, sa_nxt = 0.0f, sp = 0.0f;
     #pragma unroll
-    for (int j = 0; j < FN; ++j) part[1][j] = part[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FN; ++j) part[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};   // before fragment 0
     #pragma unroll
-    for (int j = 0; j < (BROW ? FN : 1); ++j) s4[j] = s4p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < (BROW ? FN : 1); ++j) s4p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     auto read_a = [&](int i, i32x8& f, float& sc) {
       f = frag(a0, a1, i * WM * 16 * ROWB);
@@ -438,19 +456,50 @@ struct TileGemm {
           for (int j = 0; j < FN; ++j) acc[i][j] += sums[at(g_, i, j)];
     }
 
-    // ---- c: lane holds row lane & 15 of a, b's rows (lane >> 4) * 4 + v -------------------------
+    // ---- c: lane holds row lane & 15 of a, b's rows (lane >> 4) * 4 + v.  Stored from there, a
+    // row's line would be written in pieces of 32 bytes (bf16): each wave turns its fragments
+    // around in LDS, 16 rows at a time, and stores 16 bytes a lane, WTN neighbouring values a row
+    // (grouped 7168 x 2048 over 256 experts: 889 -> 863 us). ------------------------------------
+    auto value = [&](int i, int j) {
+      return (i * WM + wm) * 16 + fr < t.rows ? acc[i][j] : f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+    if (g.N % (16 / ES) == 0) {
+      if (KG == 1) __syncthreads();                    // the ring is done with (KG > 1: above)
+      char* mine = lds + OUT_OFF + wave * 16 * PITCH;
+      constexpr int CPR = WTN * ES / 16;               // 16-byte chunks per row
+      constexpr int RPP = kWave / CPR < 16 ? kWave / CPR : 16;   // rows per store
+      #pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        #pragma unroll
+        for (int j = 0; j < FN; ++j)
+          store4<F32>(mine, (fr * PITCH + (j * 16 + fq * 4) * ES) / ES, value(i, j), 4, true);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        #pragma unroll
+        for (int r0 = 0; r0 < 16; r0 += RPP) {
+          const int r = r0 + lane / CPR, m = (i * WM + wm) * 16 + r;
+          const int n = wn * WTN + lane % CPR * (16 / ES);
+          if (lane < RPP * CPR && m < t.zero_rows && n < t.cols) {
+            const i32x4 v = *reinterpret_cast<const i32x4*>(mine + r * PITCH + lane % CPR * 16);
+            i32x4* to = reinterpret_cast<i32x4*>(
+                (char*)g.c + ((t.row0 + m) * (int64_t)g.N + t.n0 + n) * ES);
+            if (g.past_cache) __builtin_nontemporal_store(v, to);
+            else *to = v;
+          }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      }
+      return;
+    }
     const bool vec = (g.N & 3) == 0;
     #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int m = (i * WM + wm) * 16 + fr;
       if (m >= t.zero_rows) continue;
-      const bool held = m < t.rows;
       #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int n = wn * WTN + j * 16 + fq * 4;
         if (n < t.cols)
-          store4<F32>(g.c, (t.row0 + m) * (int64_t)g.N + t.n0 + n,
-                      held ? acc[i][j] : f32x4{0.f, 0.f, 0.f, 0.f}, t.cols - n, vec);
+          store4<F32>(g.c, (t.row0 + m) * (int64_t)g.N + t.n0 + n, value(i, j), t.cols - n, vec);
       }
     }
   }
@@ -635,8 +684,10 @@ __global__ __launch_bounds__(NW * kWave) void stream_kernel(Args g) {
   G::run(g, dense_tile<G::BM, G::BN>(g, blockIdx.x), lds);
 }
 
-template <int BM, int BN, int WM, int WN, int KG, int NS, bool F32>
-__global__ __launch_bounds__(WM * WN * KG * kWave) void grouped_kernel(Args g) {
+// The alignment's tiles, expert by expert, m-blocks of one expert side by side (grouped_tile).
+// WPS: waves per SIMD to fit in registers, so that workgroups overlap on a compute unit.
+template <int BM, int BN, int WM, int WN, int KG, int NS, int WPS, bool F32>
+__global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void grouped_kernel(Args g) {
   using G = TileGemm<BM, BN, WM, WN, KG, NS, false, F32>;
   __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
   const int nblk = (g.N + BN - 1) / BN;
@@ -660,6 +711,14 @@ __global__ __launch_bounds__(WM * WN * KG * kWave) void grouped_kernel(Args g) {
   t.n0 = r.nt * BN;
   t.cols = min(BN, g.N - t.n0);
   t.zero_rows = BM;
+  // An expert with one m-block reads its weights once: past 64 rows a block the plain loads are
+  // the faster ones all the same (128 x 256: 822 against 1772 us), up to 64 rows the others
+  // (32 rows, 8 experts of 4096 x 14336: 75 against 85 us; 16 rows, 256 experts of 4096 x 7168:
+  // 957 against 1059 us; equal at K = 2048).  With several m-blocks they would read the weights
+  // from memory again for each.
+  if constexpr (BM <= 64) {
+    if (g.offsets[r.e + 1] - g.offsets[r.e] == BM) return G::template run<true, true>(g, t, lds);
+  }
   G::template run<true>(g, t, lds);
 }
 
@@ -681,14 +740,14 @@ hipError_t run_stream(const Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, int KG, int NS>
+template <int BM, int BN, int WM, int WN, int KG, int NS, int WPS = 2>
 hipError_t run_grouped(const Args& a, bool f32, hipStream_t s) {
   const int64_t tiles = (int64_t)a.tiles_max * ((a.N + BN - 1) / BN);
   const dim3 grid((unsigned)xcd_chunked_grid<kChunk>(tiles)), block(WM * WN * KG * kWave);
   if (f32)
-    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, true>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, WPS, true>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, WPS, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -766,11 +825,29 @@ hipError_t launch_grouped_gemm_e4m3(const Resolved& r, int N, int K, const uint8
   g.tiles_max = (int)r.tiles_max;
   g.n_slots = (int)r.N;
   g.M = (int)r.rows_max; g.N = N; g.K = K;
+  // Stores around the last-level cache (256 MB) for an output that does not fit it (128-row blocks,
+  // 2048 x 8 slots of 256 experts to 7168: 857 -> 822 us; 64-row blocks 745 -> 708 us).
+  g.past_cache = r.rows_max * N * (out_f32 ? 4 : 2) > (256LL << 20);
+  // 256 columns a tile while its last n-block wastes little (N = 7168: 857 us against 882 with 128;
+  // N = 2880, 7% past the end: 788 against 807; N = 1408, 9%: 152 against 128).
+  const bool wide = ((int64_t)N + 255) / 256 * 256 * 100 <= (int64_t)N * 108;
+  // Few tiles: the k-groups of the dense product (run_dense).
+  const int cus = std::max(device_cu_count(), 8);
+  const bool few = r.tiles_max * ((N + 63) / 64) <= cus;
   switch (r.BM) {
-    case 16: return q8::run_grouped<16, 128, 1, 4, 1, 3>(g, out_f32, s);
-    case 32: return q8::run_grouped<32, 128, 1, 4, 1, 3>(g, out_f32, s);
-    case 64: return q8::run_grouped<64, 128, 1, 4, 1, 3>(g, out_f32, s);
-    case 128: return q8::run_grouped<128, 128, 2, 4, 1, 2>(g, out_f32, s);
+    case 16:
+      if (few) return q8::run_grouped<16, 64, 1, 2, 4, 3>(g, out_f32, s);
+      return q8::run_grouped<16, 128, 1, 4, 1, 3>(g, out_f32, s);
+    case 32:
+      if (few) return q8::run_grouped<32, 64, 1, 4, 2, 3>(g, out_f32, s);
+      return q8::run_grouped<32, 128, 1, 4, 1, 3>(g, out_f32, s);
+    case 64:
+      if (few) return q8::run_grouped<64, 64, 2, 2, 2, 3>(g, out_f32, s);
+      if (wide) return q8::run_grouped<64, 256, 2, 4, 1, 3>(g, out_f32, s);
+      return q8::run_grouped<64, 128, 2, 4, 1, 3>(g, out_f32, s);
+    case 128:
+      if (wide) return q8::run_grouped<128, 256, 2, 4, 1, 3>(g, out_f32, s);
+      return q8::run_grouped<128, 128, 2, 4, 1, 2, 4>(g, out_f32, s);
     default: return hipErrorInvalidValue;
   }
 }

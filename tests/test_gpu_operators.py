@@ -393,7 +393,10 @@ GROUPED = [(1, 4, 1, 16, 100, 256, "all"), (64, 8, 2, 16, 576, 512, "all"),
            (37, 5, 3, 32, 257, 384, "some"), (200, 16, 4, 64, 1000, 256, "some"),
            (300, 3, 2, 128, 320, 1024, "all"), (20, 4, 2, 128, 128, 128, "none"),
            (700, 4, 3, 128, 384, 640, "one"), (40, 300, 8, 16, 64, 128, "all"),
-           (90, 2, 2, 32, 130, 1152, "all"), (150, 2, 1, 64, 96, 2048, "all")]
+           (90, 2, 2, 32, 130, 1152, "all"), (150, 2, 1, 64, 96, 2048, "all"),
+           (60, 64, 4, 16, 4096, 256, "all"), (500, 20, 4, 32, 1536, 128, "some"),
+           (700, 40, 3, 64, 1024, 384, "all"), (900, 12, 2, 128, 1024, 384, "all"),
+           (400, 12, 3, 128, 1400, 256, "some"), (30, 2, 1, 16, 2052, 640, "one")]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
