@@ -7,7 +7,6 @@ and call them.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import Optional, Tuple
 
 import torch
@@ -124,19 +123,17 @@ def forward(p: Problem, x, topk_ids, topk_weights, w13, w2, w13_scales=None, w2_
 # rows in expert-sorted order, gradients, products of e4m3 codes.  `a` is the alignment that
 # align() or route_align() returns for the same problem.
 # ---------------------------------------------------------------------------------------------
-_HERE = contextlib.nullcontext()
-
-
-def _on(stream):
-    """Allocate on the stream that the call runs on, so that the buffers' memory belongs to it."""
+def _new(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
+    """A buffer allocated on the stream that the call runs on, so that its memory belongs to it."""
     if stream is None:
-        return _HERE
+        return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     if stream.device_index != torch.cuda.current_device():
         raise ValueError(f"stream: of device {stream.device_index}, the current device is "
                          f"{torch.cuda.current_device()}")
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def permute(p: Problem, x: torch.Tensor, a: dict, x_scales: Optional[torch.Tensor] = None,
@@ -144,12 +141,10 @@ def permute(p: Problem, x: torch.Tensor, a: dict, x_scales: Optional[torch.Tenso
             stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Token rows (fp32, bf16 or e4m3 codes with optional scales per 128 columns) in
     expert-sorted order through moe_permute; returns (rows, row_scales or None)."""
-    with _on(stream):
-        if rows is None:
-            rows = torch.empty((moe_max_padded_slots(p), p.H), dtype=x.dtype, device=x.device)
-        if row_scales is None and x_scales is not None:
-            row_scales = torch.empty((moe_max_padded_slots(p), p.H // 128), dtype=torch.float32,
-                                     device=x.device)
+    if rows is None:
+        rows = _new(x, (moe_max_padded_slots(p), p.H), x.dtype, stream)
+    if row_scales is None and x_scales is not None:
+        row_scales = _new(x, (moe_max_padded_slots(p), p.H // 128), torch.float32, stream)
     moe_permute(p, x, x_scales, a["slot_row"], a["sorted_slots"], a["num_tiles"], rows,
                 row_scales, stream)
     return rows, row_scales
@@ -161,8 +156,7 @@ def unpermute(p: Problem, rows: torch.Tensor, a: dict,
     """Expert-sorted rows added per token with the routing weights (1 without them: the gradient
     of permute) through moe_unpermute."""
     if out is None:
-        with _on(stream):
-            out = torch.empty((p.T, p.H), dtype=rows.dtype, device=rows.device)
+        out = _new(rows, (p.T, p.H), rows.dtype, stream)
     moe_unpermute(p, rows, a["slot_row"], topk_weights, out, stream)
     return out
 
@@ -173,12 +167,10 @@ def unpermute_bwd(p: Problem, d_out: torch.Tensor, rows: torch.Tensor, a: dict,
                   d_weights: Optional[torch.Tensor] = None,
                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Gradient of unpermute through moe_unpermute_bwd; returns (d_rows, d_weights)."""
-    with _on(stream):
-        if d_rows is None:
-            d_rows = torch.empty((moe_max_padded_slots(p), p.H), dtype=d_out.dtype,
-                                 device=d_out.device)
-        if d_weights is None:
-            d_weights = torch.empty((p.T, p.top_k), dtype=torch.float32, device=d_out.device)
+    if d_rows is None:
+        d_rows = _new(d_out, (moe_max_padded_slots(p), p.H), d_out.dtype, stream)
+    if d_weights is None:
+        d_weights = _new(d_out, (p.T, p.top_k), torch.float32, stream)
     moe_unpermute_bwd(p, d_out, rows, a["slot_row"], a["sorted_slots"], a["num_tiles"],
                       topk_weights, d_rows, d_weights, stream)
     return d_rows, d_weights
@@ -189,8 +181,7 @@ def route_bwd(p: Problem, logits: torch.Tensor, renormalize: bool, topk_ids: tor
               stream=None) -> torch.Tensor:
     """Gradient of route's weights with respect to the logits through moe_route_bwd."""
     if d_logits is None:
-        with _on(stream):
-            d_logits = torch.empty((p.T, p.E), dtype=torch.float32, device=logits.device)
+        d_logits = _new(logits, (p.T, p.E), torch.float32, stream)
     moe_route_bwd(p, logits, renormalize, topk_ids, d_weights, d_logits, stream)
     return d_logits
 
@@ -200,9 +191,8 @@ def quantize_cols_e4m3(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torc
     (codes [n, mp], scales [n, mp/128]), mp = m rounded up to 128."""
     m, n = x.shape
     groups = -(-m // 128)
-    with _on(stream):
-        xq = torch.empty((n, groups * 128), dtype=torch.float8_e4m3fn, device=x.device)
-        scales = torch.empty((n, groups), dtype=torch.float32, device=x.device)
+    xq = _new(x, (n, groups * 128), torch.float8_e4m3fn, stream)
+    scales = _new(x, (n, groups), torch.float32, stream)
     moe_quantize_cols_e4m3(x, xq, scales, stream)
     return xq, scales
 
@@ -213,8 +203,7 @@ def gemm_e4m3(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales
     """a [m, k] times b [n, k] transposed, both e4m3 codes with one scale per 128 values along k,
     through moe_gemm_e4m3."""
     if out is None:
-        with _on(stream):
-            out = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype, device=a.device)
+        out = _new(a, (a.shape[0], b.shape[0]), out_dtype, stream)
     moe_gemm_e4m3(a, a_scales, b, b_scales, b_block, out, stream)
     return out
 
@@ -225,9 +214,7 @@ def grouped_gemm_e4m3(p: Problem, rows: torch.Tensor, row_scales: torch.Tensor, 
     """Expert-sorted rows (e4m3 codes) times their experts' w [E, n, k] transposed, through
     moe_grouped_gemm_e4m3."""
     if out is None:
-        with _on(stream):
-            out = torch.empty((moe_max_padded_slots(p), w.shape[1]), dtype=out_dtype,
-                              device=rows.device)
+        out = _new(rows, (moe_max_padded_slots(p), w.shape[1]), out_dtype, stream)
     moe_grouped_gemm_e4m3(p, rows, row_scales, w, w_scales, a["sorted_slots"], a["offsets"],
                           a["tiles"], a["num_tiles"], out, stream)
     return out

@@ -36,6 +36,7 @@ struct Args {
   int T, K, vpr;                // tokens, slots per token, 16-byte vectors per row
   int BM, rows_max, tiles_max, groups;   // groups: scales per row (0: none)
   int64_t n_slots;
+  bool past_cache;              // unpermute_bwd: the rows are larger than the last-level cache
   int token_blocks;             // blocks [0, token_blocks) walk tokens, the rest clear padding
   int blocks;                   // all of them; a launch runs at most kMaxGrid and strides
 };
@@ -71,10 +72,10 @@ __device__ __forceinline__ void permute_block(const Args& g, int block) {
     clear_padding(g, block - g.token_blocks);
     return;
   }
-  const int64_t idx = (int64_t)block * kThreads + threadIdx.x;
-  if (idx >= (int64_t)g.T * g.vpr) return;
-  const int t = (int)(idx / g.vpr);
-  const int c = (int)(idx - (int64_t)t * g.vpr);
+  const uint32_t idx = (uint32_t)block * kThreads + threadIdx.x;
+  if (idx >= (uint32_t)g.T * (uint32_t)g.vpr) return;    // T * H < 2^31, so T * vpr < 2^29 + 1
+  const int t = (int)(idx / (uint32_t)g.vpr);
+  const int c = (int)(idx - (uint32_t)t * (uint32_t)g.vpr);
   const i32x4 v = g.x[idx];
   const bool scale = g.row_scales && (c & 7) == 0;   // e4m3: 8 vectors per 128 columns
   const float sc = scale ? g.x_scales[(int64_t)t * g.groups + (c >> 3)] : 0.0f;
@@ -127,10 +128,10 @@ __device__ __forceinline__ i32x4 pack(const float* f) {
 // batch issued before the first product.  The sum is carried in fp32 and rounded once.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(Args g) {
-  const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (idx >= (int64_t)g.T * g.vpr) return;
-  const int t = (int)(idx / g.vpr);
-  const int c = (int)(idx - (int64_t)t * g.vpr);
+  const uint32_t idx = (uint32_t)blockIdx.x * kThreads + threadIdx.x;
+  if (idx >= (uint32_t)g.T * (uint32_t)g.vpr) return;
+  const int t = (int)(idx / (uint32_t)g.vpr);
+  const int c = (int)(idx - (uint32_t)t * (uint32_t)g.vpr);
   constexpr int L = BF16 ? 8 : 4;
   float acc[L];
   #pragma unroll
@@ -163,68 +164,84 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(Args g) {
   g.rows[idx] = pack<BF16>(acc);
 }
 
-// One wavefront per slot: the token's d_out row and the slot's row are walked once, giving the
-// slot's d_rows row and (wave sum in a fixed order) its d_w.  The waves of a workgroup belong
-// to neighbouring slots, most of them of one token, whose d_out row then comes from L1/L2.
-template <bool BF16>
-__device__ __forceinline__ void unpermute_bwd_block(const Args& g, int block) {
+// WPS wavefronts per slot: the token's d_out row and the slot's row are walked once, giving the
+// slot's d_rows row and (sums in a fixed order) its d_w.  With one wavefront the waves of a
+// workgroup belong to neighbouring slots, most of them of one token, whose d_out row then comes
+// from L1/L2.  With few slots a workgroup's four share one (one token, top 8, 7168 columns: 8.1 us
+// with one).  Stores go around the last-level cache (256 MB) when rows and d_rows do not fit it:
+// 8192 tokens, top 6, 2048 columns 97 -> 74 us; below that whoever reads d_rows next is slower by
+// more than the stores gain (35 MB: 19.3 -> 20.9 us with a reader behind it).
+template <bool BF16, int WPS>
+__device__ __forceinline__ void unpermute_bwd_block(const Args& g, int block, float* sums) {
   if (block >= g.token_blocks) {
     clear_padding(g, block - g.token_blocks);
     return;
   }
   constexpr int L = BF16 ? 8 : 4;
+  constexpr int SPB = kThreads / kWave / WPS;            // slots per workgroup
   const int lane = threadIdx.x & (kWave - 1);
-  const int64_t s = (int64_t)block * (kThreads / kWave) +
-                    __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  if (s >= g.n_slots) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t s = (int64_t)block * SPB + wave / WPS;
+  if (s >= g.n_slots) return;                            // SPB > 1 only: whole wavefronts
   const int r = g.slot_row[s];
-  if ((uint32_t)r >= (uint32_t)g.rows_max) {            // excluded id: no row, no gradient
-    if (g.d_w && lane == 0) g.d_w[s] = 0.0f;
-    return;
-  }
-  const float w = g.w ? g.w[s] : 1.0f;
-  const i32x4* d = g.d_out + (s / g.K) * g.vpr;
-  const i32x4* x = g.x + (int64_t)r * g.vpr;
-  i32x4* o = g.rows + (int64_t)r * g.vpr;
+  const bool there = (uint32_t)r < (uint32_t)g.rows_max;   // else an excluded id: no gradient
   float dot = 0.0f;
-  constexpr int U = 4;
-  for (int c0 = lane; c0 < g.vpr; c0 += U * kWave) {
-    i32x4 dv[U], xv[U];
-    #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = min(c0 + u * kWave, g.vpr - 1);
-      dv[u] = d[c];
-      if (g.d_w) xv[u] = x[c];
-    }
-    #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * kWave;
-      if (c >= g.vpr) continue;
-      float df[L];
-      unpack<BF16>(dv[u], df);
-      if (g.d_w) {
-        float xf[L];
-        unpack<BF16>(xv[u], xf);
-        #pragma unroll
-        for (int i = 0; i < L; ++i) dot = __builtin_fmaf(df[i], xf[i], dot);
+  if (there) {
+    const float w = g.w ? g.w[s] : 1.0f;
+    const i32x4* d = g.d_out + (s / g.K) * g.vpr;
+    const i32x4* x = g.x + (int64_t)r * g.vpr;
+    i32x4* o = g.rows + (int64_t)r * g.vpr;
+    constexpr int U = 4;
+    for (int c0 = wave % WPS * kWave + lane; c0 < g.vpr; c0 += U * WPS * kWave) {
+      i32x4 dv[U], xv[U];
+      #pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = min(c0 + u * WPS * kWave, g.vpr - 1);
+        dv[u] = d[c];
+        if (g.d_w) xv[u] = x[c];
       }
-      if (g.rows) {
-        #pragma unroll
-        for (int i = 0; i < L; ++i) df[i] *= w;
-        o[c] = pack<BF16>(df);
+      #pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * WPS * kWave;
+        if (c >= g.vpr) continue;
+        float df[L];
+        unpack<BF16>(dv[u], df);
+        if (g.d_w) {
+          float xf[L];
+          unpack<BF16>(xv[u], xf);
+          #pragma unroll
+          for (int i = 0; i < L; ++i) dot = __builtin_fmaf(df[i], xf[i], dot);
+        }
+        if (g.rows) {
+          #pragma unroll
+          for (int i = 0; i < L; ++i) df[i] *= w;
+          const i32x4 v = pack<BF16>(df);
+          if (g.past_cache) __builtin_nontemporal_store(v, &o[c]);
+          else o[c] = v;
+        }
       }
     }
   }
-  if (g.d_w) {
+  if (!g.d_w) return;
+  #pragma unroll
+  for (int m = kWave / 2; m >= 1; m >>= 1) dot += __shfl_xor(dot, m, kWave);
+  if constexpr (WPS > 1) {
+    if (lane == 0) sums[wave] = dot;
+    __syncthreads();
+    dot = 0.0f;
     #pragma unroll
-    for (int m = kWave / 2; m >= 1; m >>= 1) dot += __shfl_xor(dot, m, kWave);
-    if (lane == 0) g.d_w[s] = dot;
+    for (int i = 0; i < WPS; ++i) dot += sums[i];
+    __syncthreads();                                     // before the next block's sums
+    if (wave > 0) return;
   }
+  if (lane == 0) g.d_w[s] = dot;
 }
 
-template <bool BF16>
+template <bool BF16, int WPS>
 __global__ __launch_bounds__(kThreads) void unpermute_bwd_kernel(Args g) {
-  for (int b = blockIdx.x; b < g.blocks; b += gridDim.x) unpermute_bwd_block<BF16>(g, b);
+  static_assert(WPS == 1 || WPS == kThreads / kWave, "one slot per workgroup, or one per wave");
+  __shared__ float sums[kThreads / kWave];
+  for (int b = blockIdx.x; b < g.blocks; b += gridDim.x) unpermute_bwd_block<BF16, WPS>(g, b, sums);
 }
 
 Args args(const Resolved& r, int row_dtype) {
@@ -291,14 +308,19 @@ hipError_t launch_unpermute_bwd(const Resolved& r, int row_dtype, const void* d_
   a.w = topk_w;
   a.rows = (i32x4*)d_rows;
   a.d_w = d_w;
-  constexpr int kWavesPerBlock = pm::kThreads / kWave;
-  a.token_blocks = (int)((r.N + kWavesPerBlock - 1) / kWavesPerBlock);
+  a.past_cache = 2 * r.rows_max * a.vpr * 16 > (256LL << 20);
+  constexpr int kWaves = pm::kThreads / kWave;
+  const bool few = r.N < 2048;          // fewer waves than 8 per compute unit of 256
+  a.token_blocks = (int)(few ? r.N : (r.N + kWaves - 1) / kWaves);
   a.blocks = a.token_blocks + (d_rows ? pm::pad_blocks(r) : 0);
-  const unsigned blocks = (unsigned)std::min(a.blocks, pm::kMaxGrid);
-  if (row_dtype == MOE_BF16)
-    hipLaunchKernelGGL(pm::unpermute_bwd_kernel<true>, dim3(blocks), dim3(pm::kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL(pm::unpermute_bwd_kernel<false>, dim3(blocks), dim3(pm::kThreads), 0, s, a);
+  const dim3 grid((unsigned)std::min(a.blocks, pm::kMaxGrid)), block(pm::kThreads);
+  if (row_dtype == MOE_BF16) {
+    if (few) hipLaunchKernelGGL((pm::unpermute_bwd_kernel<true, kWaves>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((pm::unpermute_bwd_kernel<true, 1>), grid, block, 0, s, a);
+  } else {
+    if (few) hipLaunchKernelGGL((pm::unpermute_bwd_kernel<false, kWaves>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((pm::unpermute_bwd_kernel<false, 1>), grid, block, 0, s, a);
+  }
   return hipGetLastError();
 }
 

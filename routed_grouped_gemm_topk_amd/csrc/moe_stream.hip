@@ -59,12 +59,18 @@ hipError_t launch_quant_rows(const Resolved& r, const void* x, uint8_t* xq, floa
 // ---------------------------------------------------------------------------------------------
 // The same quantisation along the rows, transposed: x [M, C] -> codes [C, Mp], scales
 // [C, Mp/128], Mp = M rounded up to 128.  Operand of a weight gradient, whose sum runs over the
-// tokens.  One workgroup takes 128 rows x 64 columns: the tile goes through LDS (pitch 33 words,
-// so that the 4 lanes of a column and the 16 columns of a wave read different banks but for a
-// two-way conflict), 4 lanes per column take 32 rows each and store them as 32 bytes.  Rows past
-// M are zeros.  The quotients are IEEE fp32 and at most 448 up to their rounding (up to 450 where
-// the scale itself is subnormal), below the 464 from which e4m3 would overflow, so the gfx950
-// convert (nearest even, NaN kept) needs no clamp.
+// tokens.  One workgroup takes 128 rows x 64 columns: the tile goes through LDS, a thread takes
+// 16 rows of two neighbouring columns (pitch 33 words: the 8 threads of a column pair and the 8
+// pairs of a wave read different banks but for a two-way conflict) and stores 16 bytes of each;
+// a column's 8 threads write its 128 bytes together.  Rows past M are zeros.
+//
+// Quotients: IEEE fp32, x / s for one s and 16 values of x.  With r = 1/s to rounding (v_rcp_f32
+// and one Newton step, once), q = x r, then twice q += r (x - s q) by fma: the steps of the
+// correctly rounded division for operands that need no scaling, 6 operations a value instead of
+// 11.  s outside [2^-96, 2^96] takes the division itself; a quotient too small for the steps to
+// be exact is far below the 2^-10 that e4m3 rounds to 0.  They are at most 448 up to their
+// rounding (up to 450 where s is subnormal), below the 464 from which e4m3 would overflow, so the
+// gfx950 convert (nearest even, NaN kept) needs no clamp.
 // ---------------------------------------------------------------------------------------------
 constexpr int kQuantCols = 64;
 
@@ -72,6 +78,8 @@ __global__ __launch_bounds__(kQuantThreads) void quant_cols_e4m3_kernel(
     const uint16_t* __restrict__ x, uint8_t* __restrict__ xq, float* __restrict__ scales, int M,
     int C, int groups) {
   constexpr int PITCH = kQuantCols / 2 + 1;              // words
+  constexpr int ROWS = 16;                               // of a thread
+  constexpr int PARTS = kGroup / ROWS;
   __shared__ uint32_t tile[kGroup * PITCH];
   const int g = blockIdx.x % groups;
   const int c0 = (blockIdx.x / groups) * kQuantCols;
@@ -87,29 +95,47 @@ __global__ __launch_bounds__(kQuantThreads) void quant_cols_e4m3_kernel(
     for (int k = 0; k < 4; ++k) tile[r * PITCH + c / 2 + k] = (uint32_t)v[k];
   }
   __syncthreads();
-  const int c = threadIdx.x >> 2, part = threadIdx.x & 3;
-  float v[32];
-  float m = 0.0f;
+  const int part = threadIdx.x % PARTS, pair = threadIdx.x / PARTS;
+  float v[2][ROWS];
+  float m[2] = {0.0f, 0.0f};
   #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const uint32_t w = tile[(part * 32 + i) * PITCH + (c >> 1)];
-    v[i] = bf16_bits_to_f32((c & 1) ? w >> 16 : w & 0xFFFFu);
-    m = fmaxf(m, fabsf(v[i]));
+  for (int i = 0; i < ROWS; ++i) {
+    const uint32_t w = tile[(part * ROWS + i) * PITCH + pair];
+    v[0][i] = bf16_bits_to_f32(w & 0xFFFFu);
+    v[1][i] = __uint_as_float(w & 0xFFFF0000u);
+    m[0] = fmaxf(m[0], fabsf(v[0][i]));
+    m[1] = fmaxf(m[1], fabsf(v[1][i]));
   }
-  m = fmaxf(m, __shfl_xor(m, 1, kWave));
-  m = fmaxf(m, __shfl_xor(m, 2, kWave));
-  if (c0 + c >= C) return;
-  const float s = (m == 0.0f) ? 1.0f : m / kE4M3Max;
-  uint32_t o[8];
   #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    o[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(
-        v[4 * i + 2] / s, v[4 * i + 3] / s,
-        __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] / s, v[4 * i + 1] / s, 0, false), true);
-  i32x4* dst = reinterpret_cast<i32x4*>(xq + (size_t)(c0 + c) * groups * kGroup + m0 + part * 32);
-  dst[0] = i32x4{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
-  dst[1] = i32x4{(int)o[4], (int)o[5], (int)o[6], (int)o[7]};
-  if (part == 0) scales[(size_t)(c0 + c) * groups + g] = s;
+  for (int h = 0; h < 2; ++h) {
+    #pragma unroll
+    for (int d = 1; d < PARTS; d *= 2) m[h] = fmaxf(m[h], __shfl_xor(m[h], d, kWave));
+    const int c = c0 + 2 * pair + h;
+    if (c >= C) continue;
+    const float s = (m[h] == 0.0f) ? 1.0f : m[h] / kE4M3Max;
+    if (s >= 0x1p-96f && s <= 0x1p96f) {
+      const float r0 = __builtin_amdgcn_rcpf(s);
+      const float r = __builtin_fmaf(__builtin_fmaf(-s, r0, 1.0f), r0, r0);
+      #pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        float q = v[h][i] * r;
+        q = __builtin_fmaf(__builtin_fmaf(-s, q, v[h][i]), r, q);
+        q = __builtin_fmaf(__builtin_fmaf(-s, q, v[h][i]), r, q);
+        v[h][i] = __builtin_copysignf(q, v[h][i]);       // -0 stays -0
+      }
+    } else {
+      #pragma unroll
+      for (int i = 0; i < ROWS; ++i) v[h][i] = v[h][i] / s;
+    }
+    i32x4 o;
+    #pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = __builtin_amdgcn_cvt_pk_fp8_f32(
+          v[h][4 * i + 2], v[h][4 * i + 3],
+          __builtin_amdgcn_cvt_pk_fp8_f32(v[h][4 * i], v[h][4 * i + 1], 0, false), true);
+    *reinterpret_cast<i32x4*>(xq + (size_t)c * groups * kGroup + m0 + part * ROWS) = o;
+    if (part == 0) scales[(size_t)c * groups + g] = s;
+  }
 }
 
 hipError_t launch_quant_cols(int M, int C, const void* x, uint8_t* xq, float* scales,

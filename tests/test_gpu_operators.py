@@ -431,6 +431,7 @@ def test_quantize_cols(device, m, n):
     say("quantize_cols", m, n)
     x = torch.randn((m, n), generator=gen(device, 17), device=device)
     x = (x * torch.exp(4 * torch.randn((1, n), generator=gen(device, 18), device=device))).bfloat16()
+    x[:, 6], x[:, 7] = x[:, 6] * 2.0 ** 100, x[:, 7] * 2.0 ** -110   # scales that 1/s would not fit
     x[:, 1] = 0.0
     x[:, 2] = 1e-40                                        # subnormal, and a subnormal scale
     x[0, 3] = -0.0
