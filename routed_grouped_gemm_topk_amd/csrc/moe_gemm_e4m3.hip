@@ -34,7 +34,6 @@ struct Args {
   const int32_t* tiles;
   const int32_t* num_tiles;
   int tiles_max, n_slots;
-  bool past_cache;              // c is larger than the last-level cache
   int M, N, K;
 };
 
@@ -184,7 +183,8 @@ struct TileGemm {
 
   // PARTIAL: tiles may hold few rows (a loop of its own for waves that have fragments without any)
   // ONCE: nothing else reads this tile's part of b
-  template <bool PARTIAL, bool ONCE = false>
+  // PAST: c is larger than the last-level cache
+  template <bool PARTIAL, bool ONCE = false, bool PAST = false>
   __device__ static __forceinline__ void run(const Args& g, const Tile& t, char* lds) {
     const int lane = threadIdx.x & (kWave - 1);
     const int all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -482,7 +482,7 @@ struct TileGemm {
             const i32x4 v = *reinterpret_cast<const i32x4*>(mine + r * PITCH + lane % CPR * 16);
             i32x4* to = reinterpret_cast<i32x4*>(
                 (char*)g.c + ((t.row0 + m) * (int64_t)g.N + t.n0 + n) * ES);
-            if (g.past_cache) __builtin_nontemporal_store(v, to);
+            if constexpr (PAST) __builtin_nontemporal_store(v, to);
             else *to = v;
           }
         }
@@ -686,7 +686,7 @@ __global__ __launch_bounds__(NW * kWave) void stream_kernel(Args g) {
 
 // The alignment's tiles, expert by expert, m-blocks of one expert side by side (grouped_tile).
 // WPS: waves per SIMD to fit in registers, so that workgroups overlap on a compute unit.
-template <int BM, int BN, int WM, int WN, int KG, int NS, int WPS, bool F32>
+template <int BM, int BN, int WM, int WN, int KG, int NS, int WPS, bool PAST, bool F32>
 __global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void grouped_kernel(Args g) {
   using G = TileGemm<BM, BN, WM, WN, KG, NS, false, F32>;
   __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
@@ -717,9 +717,9 @@ __global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void grouped_kernel(Args
   // 957 against 1059 us; equal at K = 2048).  With several m-blocks they would read the weights
   // from memory again for each.
   if constexpr (BM <= 64) {
-    if (g.offsets[r.e + 1] - g.offsets[r.e] == BM) return G::template run<true, true>(g, t, lds);
+    if (g.offsets[r.e + 1] - g.offsets[r.e] == BM) return G::template run<true, true, PAST>(g, t, lds);
   }
-  G::template run<true>(g, t, lds);
+  G::template run<true, false, PAST>(g, t, lds);
 }
 
 template <int BM, int BN, int WM, int WN, int KG, int NS, bool BROW, bool F32>
@@ -740,14 +740,14 @@ hipError_t run_stream(const Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, int KG, int NS, int WPS = 2>
+template <int BM, int BN, int WM, int WN, int KG, int NS, int WPS = 2, bool PAST = false>
 hipError_t run_grouped(const Args& a, bool f32, hipStream_t s) {
   const int64_t tiles = (int64_t)a.tiles_max * ((a.N + BN - 1) / BN);
   const dim3 grid((unsigned)xcd_chunked_grid<kChunk>(tiles)), block(WM * WN * KG * kWave);
   if (f32)
-    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, WPS, true>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, WPS, PAST, true>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, WPS, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, WPS, PAST, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -825,9 +825,10 @@ hipError_t launch_grouped_gemm_e4m3(const Resolved& r, int N, int K, const uint8
   g.tiles_max = (int)r.tiles_max;
   g.n_slots = (int)r.N;
   g.M = (int)r.rows_max; g.N = N; g.K = K;
-  // Stores around the last-level cache (256 MB) for an output that does not fit it (128-row blocks,
-  // 2048 x 8 slots of 256 experts to 7168: 857 -> 822 us; 64-row blocks 745 -> 708 us).
-  g.past_cache = r.rows_max * N * (out_f32 ? 4 : 2) > (256LL << 20);
+  // Stores past the last-level cache (256 MB) for an output that does not fit it (slots of 256
+  // experts to 7168 columns: 16384 in 128-row blocks 851 -> 814 us, 8192 in 64-row blocks 783 ->
+  // 704 us); a smaller output stays in reach of whoever reads it next.
+  const bool past = r.rows_max * N * (out_f32 ? 4 : 2) > (256LL << 20);
   // 256 columns a tile while its last n-block wastes little (N = 7168: 857 us against 882 with 128;
   // N = 2880, 7% past the end: 788 against 807; N = 1408, 9%: 152 against 128).
   const bool wide = ((int64_t)N + 255) / 256 * 256 * 100 <= (int64_t)N * 108;
@@ -843,9 +844,11 @@ hipError_t launch_grouped_gemm_e4m3(const Resolved& r, int N, int K, const uint8
       return q8::run_grouped<32, 128, 1, 4, 1, 3>(g, out_f32, s);
     case 64:
       if (few) return q8::run_grouped<64, 64, 2, 2, 2, 3>(g, out_f32, s);
+      if (wide && past) return q8::run_grouped<64, 256, 2, 4, 1, 3, 2, true>(g, out_f32, s);
       if (wide) return q8::run_grouped<64, 256, 2, 4, 1, 3>(g, out_f32, s);
       return q8::run_grouped<64, 128, 2, 4, 1, 3>(g, out_f32, s);
     case 128:
+      if (wide && past) return q8::run_grouped<128, 256, 2, 4, 1, 3, 2, true>(g, out_f32, s);
       if (wide) return q8::run_grouped<128, 256, 2, 4, 1, 3>(g, out_f32, s);
       return q8::run_grouped<128, 128, 2, 4, 1, 2, 4>(g, out_f32, s);
     default: return hipErrorInvalidValue;

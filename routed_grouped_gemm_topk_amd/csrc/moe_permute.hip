@@ -12,6 +12,7 @@
 // the sorted rows, so each token row (x, d_out) is read once for its top_k slots, and a token's
 // slots are added by one thread in ascending j: no atomics, same bits on every run.
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_internal.h"
 
@@ -36,7 +37,6 @@ struct Args {
   int T, K, vpr;                // tokens, slots per token, 16-byte vectors per row
   int BM, rows_max, tiles_max, groups;   // groups: scales per row (0: none)
   int64_t n_slots;
-  bool past_cache;              // unpermute_bwd: the rows are larger than the last-level cache
   int token_blocks;             // blocks [0, token_blocks) walk tokens, the rest clear padding
   int blocks;                   // all of them; a launch runs at most kMaxGrid and strides
 };
@@ -124,9 +124,19 @@ __device__ __forceinline__ i32x4 pack(const float* f) {
   return o;
 }
 
+template <bool LARGE>
+__device__ __forceinline__ i32x4 load_row(const i32x4* p) {
+  if constexpr (LARGE) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+
 // A thread owns 16 bytes of one token's output row; slots in batches of 4, every row load of a
 // batch issued before the first product.  The sum is carried in fp32 and rounded once.
-template <bool BF16>
+// LARGE (rows of more than 128 MB, half of the last-level cache): every row is read once and loaded
+// past the caches, 8192 tokens, top 6, 2048 columns (201 MB) from memory 48.7 -> 42.3 us
+// (5.6 TB/s), behind the permute that wrote them 93.6 -> 83.7 us together, before the gradient
+// that reads them again 144.7 -> 139.5 us; with 67 MB that last pair takes 58.6 us against 54.4.
+template <bool BF16, bool LARGE>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(Args g) {
   const uint32_t idx = (uint32_t)blockIdx.x * kThreads + threadIdx.x;
   if (idx >= (uint32_t)g.T * (uint32_t)g.vpr) return;
@@ -150,7 +160,8 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(Args g) {
     #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (j0 + u >= g.K || (uint32_t)r[u] >= (uint32_t)g.rows_max) r[u] = -1;
-      v[u] = r[u] >= 0 ? g.x[(int64_t)r[u] * g.vpr + c] : i32x4{0, 0, 0, 0};
+      v[u] = i32x4{0, 0, 0, 0};
+      if (r[u] >= 0) v[u] = load_row<LARGE>(g.x + (int64_t)r[u] * g.vpr + c);
     }
     #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -168,10 +179,9 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(Args g) {
 // slot's d_rows row and (sums in a fixed order) its d_w.  With one wavefront the waves of a
 // workgroup belong to neighbouring slots, most of them of one token, whose d_out row then comes
 // from L1/L2.  With few slots a workgroup's four share one (one token, top 8, 7168 columns: 8.1 us
-// with one).  Stores go around the last-level cache (256 MB) when rows and d_rows do not fit it:
-// 8192 tokens, top 6, 2048 columns 97 -> 74 us; below that whoever reads d_rows next is slower by
-// more than the stores gain (35 MB: 19.3 -> 20.9 us with a reader behind it).
-template <bool BF16, int WPS>
+// with one).  LARGE as above (97.8 -> 93.3 us from memory); stores past them, 86 us, cost whoever reads d_rows next more than
+// they gain (with a reader behind it 119 -> 137 us).
+template <bool BF16, int WPS, bool LARGE>
 __device__ __forceinline__ void unpermute_bwd_block(const Args& g, int block, float* sums) {
   if (block >= g.token_blocks) {
     clear_padding(g, block - g.token_blocks);
@@ -198,7 +208,7 @@ __device__ __forceinline__ void unpermute_bwd_block(const Args& g, int block, fl
       for (int u = 0; u < U; ++u) {
         const int c = min(c0 + u * WPS * kWave, g.vpr - 1);
         dv[u] = d[c];
-        if (g.d_w) xv[u] = x[c];
+        if (g.d_w) xv[u] = load_row<LARGE>(&x[c]);
       }
       #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -215,9 +225,7 @@ __device__ __forceinline__ void unpermute_bwd_block(const Args& g, int block, fl
         if (g.rows) {
           #pragma unroll
           for (int i = 0; i < L; ++i) df[i] *= w;
-          const i32x4 v = pack<BF16>(df);
-          if (g.past_cache) __builtin_nontemporal_store(v, &o[c]);
-          else o[c] = v;
+          o[c] = pack<BF16>(df);
         }
       }
     }
@@ -237,11 +245,11 @@ __device__ __forceinline__ void unpermute_bwd_block(const Args& g, int block, fl
   if (lane == 0) g.d_w[s] = dot;
 }
 
-template <bool BF16, int WPS>
+template <bool BF16, int WPS, bool LARGE>
 __global__ __launch_bounds__(kThreads) void unpermute_bwd_kernel(Args g) {
   static_assert(WPS == 1 || WPS == kThreads / kWave, "one slot per workgroup, or one per wave");
   __shared__ float sums[kThreads / kWave];
-  for (int b = blockIdx.x; b < g.blocks; b += gridDim.x) unpermute_bwd_block<BF16, WPS>(g, b, sums);
+  for (int b = blockIdx.x; b < g.blocks; b += gridDim.x) unpermute_bwd_block<BF16, WPS, LARGE>(g, b, sums);
 }
 
 Args args(const Resolved& r, int row_dtype) {
@@ -255,6 +263,16 @@ Args args(const Resolved& r, int row_dtype) {
   a.groups = r.H / kGroup;
   a.n_slots = r.N;
   return a;
+}
+
+bool large(const Resolved& r, const Args& a) { return r.N * a.vpr * 16 > (128LL << 20); }
+
+template <class F>
+void by_type(bool bf16, bool large, F f) {
+  if (bf16 && large) f(std::true_type{}, std::true_type{});
+  else if (bf16) f(std::true_type{}, std::false_type{});
+  else if (large) f(std::false_type{}, std::true_type{});
+  else f(std::false_type{}, std::false_type{});
 }
 
 int pad_blocks(const Resolved& r) { return (int)((r.rows_max + kPadRows - 1) / kPadRows); }
@@ -287,11 +305,11 @@ hipError_t launch_unpermute(const Resolved& r, int row_dtype, const void* rows,
   a.slot_row = slot_row;
   a.w = topk_w;
   a.rows = (i32x4*)out;
-  const unsigned blocks = (unsigned)(((int64_t)r.T * a.vpr + pm::kThreads - 1) / pm::kThreads);
-  if (row_dtype == MOE_BF16)
-    hipLaunchKernelGGL(pm::unpermute_kernel<true>, dim3(blocks), dim3(pm::kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL(pm::unpermute_kernel<false>, dim3(blocks), dim3(pm::kThreads), 0, s, a);
+  const dim3 grid((unsigned)(((int64_t)r.T * a.vpr + pm::kThreads - 1) / pm::kThreads));
+  pm::by_type(row_dtype == MOE_BF16, pm::large(r, a), [&](auto bf16, auto large) {
+    hipLaunchKernelGGL((pm::unpermute_kernel<bf16.value, large.value>), grid, dim3(pm::kThreads), 0,
+                       s, a);
+  });
   return hipGetLastError();
 }
 
@@ -308,19 +326,17 @@ hipError_t launch_unpermute_bwd(const Resolved& r, int row_dtype, const void* d_
   a.w = topk_w;
   a.rows = (i32x4*)d_rows;
   a.d_w = d_w;
-  a.past_cache = 2 * r.rows_max * a.vpr * 16 > (256LL << 20);
   constexpr int kWaves = pm::kThreads / kWave;
   const bool few = r.N < 2048;          // fewer waves than 8 per compute unit of 256
   a.token_blocks = (int)(few ? r.N : (r.N + kWaves - 1) / kWaves);
   a.blocks = a.token_blocks + (d_rows ? pm::pad_blocks(r) : 0);
   const dim3 grid((unsigned)std::min(a.blocks, pm::kMaxGrid)), block(pm::kThreads);
-  if (row_dtype == MOE_BF16) {
-    if (few) hipLaunchKernelGGL((pm::unpermute_bwd_kernel<true, kWaves>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((pm::unpermute_bwd_kernel<true, 1>), grid, block, 0, s, a);
-  } else {
-    if (few) hipLaunchKernelGGL((pm::unpermute_bwd_kernel<false, kWaves>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((pm::unpermute_bwd_kernel<false, 1>), grid, block, 0, s, a);
-  }
+  pm::by_type(row_dtype == MOE_BF16, pm::large(r, a), [&](auto bf16, auto large) {
+    if (few)
+      hipLaunchKernelGGL((pm::unpermute_bwd_kernel<bf16.value, kWaves, false>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((pm::unpermute_bwd_kernel<bf16.value, 1, large.value>), grid, block, 0, s, a);
+  });
   return hipGetLastError();
 }
 
