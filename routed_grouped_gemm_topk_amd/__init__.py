@@ -181,7 +181,8 @@ def route_bwd(p: Problem, logits: torch.Tensor, renormalize: bool, topk_ids: tor
               stream=None) -> torch.Tensor:
     """Gradient of route's weights with respect to the logits through moe_route_bwd."""
     if d_logits is None:
-        d_logits = _new(logits, (p.T, p.E), torch.float32, stream)
+        d_logits = (torch.empty_like(logits) if stream is None
+                    else _new(logits, logits.shape, torch.float32, stream))
     moe_route_bwd(p, logits, renormalize, topk_ids, d_weights, d_logits, stream)
     return d_logits
 

@@ -353,14 +353,15 @@ def moe_forward_scratch(p: Problem, x, topk_ids, topk_weights, w13, w13_scales, 
 # ---------------------------------------------------------------------------------------------
 # rows in expert-sorted order, gradients, products of e4m3 codes.  Every tensor of a call must be
 # on the current device: the launch goes to that device's stream.  A call's host time is that of
-# these checks next to 4 us of launch, so the common case of each is one expression (0.4 us a
+# these checks next to 3.5 us of launch, so the common case of each is one expression (0.3 us a
 # tensor) and only a tensor that fails it is looked at again, for the reason.
 # ---------------------------------------------------------------------------------------------
 _ROW_DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_E4M3,
            torch.uint8: MOE_E4M3}
-_CODES = (torch.uint8, torch.float8_e4m3fn)
+_CODES = (torch.float8_e4m3fn, torch.uint8)
 _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
-_OUT = (torch.float32, torch.bfloat16)
+_OUT = (torch.bfloat16, torch.float32)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _row_dtype(t: torch.Tensor, name: str) -> int:
@@ -382,10 +383,18 @@ def _arg(t: Optional[torch.Tensor], name: str, dtypes: tuple, numel: int, dev: i
 
 
 def _mat(t: Optional[torch.Tensor], name: str, dtypes: tuple, shape: tuple, dev: int):
-    """_arg with the whole shape checked."""
+    """The same with the whole shape checked."""
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.get_device() == dev
+            and t.dtype in dtypes and t.is_contiguous()):
+        return t.data_ptr()
     if isinstance(t, torch.Tensor) and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     return _arg(t, name, dtypes, math.prod(shape), dev)
+
+
+def _where(stream, dev: int):
+    """The stream's handle; by default the current stream of `dev`."""
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 def moe_permute(p: Problem, x, x_scales, slot_row, sorted_slots, num_tiles, rows, row_scales,
@@ -401,7 +410,7 @@ def moe_permute(p: Problem, x, x_scales, slot_row, sorted_slots, num_tiles, rows
         _arg(slot_row, "slot_row", _I32, T * p.top_k, dev),
         _arg(sorted_slots, "sorted_slots", _I32, rm, dev),
         _arg(num_tiles, "num_tiles", _I32, 1, dev), _arg(rows, "rows", same, rm * H, dev),
-        _arg(row_scales, "row_scales", _F32, rm * (H // 128), dev), _stream(stream)),
+        _arg(row_scales, "row_scales", _F32, rm * (H // 128), dev), _where(stream, dev)),
         "moe_permute")
 
 
@@ -415,7 +424,7 @@ def moe_unpermute(p: Problem, rows, slot_row, topk_weights, out, stream=None) ->
         ctypes.byref(p), dt, _arg(rows, "rows", same, moe_max_padded_slots(p) * H, dev),
         _arg(slot_row, "slot_row", _I32, N, dev),
         _arg(topk_weights, "topk_weights", _F32, N, dev), _arg(out, "out", same, T * H, dev),
-        _stream(stream)), "moe_unpermute")
+        _where(stream, dev)), "moe_unpermute")
 
 
 def moe_unpermute_bwd(p: Problem, d_out, rows, slot_row, sorted_slots, num_tiles, topk_weights,
@@ -433,7 +442,7 @@ def moe_unpermute_bwd(p: Problem, d_out, rows, slot_row, sorted_slots, num_tiles
         _arg(num_tiles, "num_tiles", _I32, 1, dev),
         _arg(topk_weights, "topk_weights", _F32, N, dev),
         _arg(d_rows, "d_rows", same, rm * H, dev), _arg(d_weights, "d_weights", _F32, N, dev),
-        _stream(stream)), "moe_unpermute_bwd")
+        _where(stream, dev)), "moe_unpermute_bwd")
 
 
 def moe_route_bwd(p: Problem, logits, renormalize: bool, topk_ids, d_weights, d_logits,
@@ -444,7 +453,7 @@ def moe_route_bwd(p: Problem, logits, renormalize: bool, topk_ids, d_weights, d_
     _checked(load().moe_route_bwd(
         ctypes.byref(p), _arg(logits, "logits", _F32, L, dev), 1 if renormalize else 0,
         _arg(topk_ids, "topk_ids", _I32, N, dev), _arg(d_weights, "d_weights", _F32, N, dev),
-        _arg(d_logits, "d_logits", _F32, L, dev), _stream(stream)), "moe_route_bwd")
+        _arg(d_logits, "d_logits", _F32, L, dev), _where(stream, dev)), "moe_route_bwd")
 
 
 def moe_quantize_cols_e4m3(x, xq, scales, stream=None) -> None:
@@ -455,23 +464,25 @@ def moe_quantize_cols_e4m3(x, xq, scales, stream=None) -> None:
     dev = torch.cuda.current_device()
     _checked(load().moe_quantize_cols_e4m3(
         m, n, _arg(x, "x", _BF16, m * n, dev), _mat(xq, "xq", _CODES, (n, groups * 128), dev),
-        _mat(scales, "scales", _F32, (n, groups), dev), _stream(stream)),
+        _mat(scales, "scales", _F32, (n, groups), dev), _where(stream, dev)),
         "moe_quantize_cols_e4m3")
 
 
 def moe_gemm_e4m3(a, a_scales, b, b_scales, b_block: int, c, stream=None) -> None:
-    for name, t in (("a", a), ("b", b)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 2:
-            raise ValueError(f"{name}: expected a matrix")
+    if not isinstance(a, torch.Tensor) or a.dim() != 2:
+        raise ValueError("a: expected a matrix")
+    if not isinstance(b, torch.Tensor) or b.dim() != 2:
+        raise ValueError("b: expected a matrix")
     m, k = a.shape
     n = b.shape[0]
+    g = k // 128
     dev = torch.cuda.current_device()
-    sb = n if b_block == 1 else -(-n // 128)
     _checked(load().moe_gemm_e4m3(
-        m, n, k, _arg(a, "a", _CODES, m * k, dev),
-        _mat(a_scales, "a_scales", _F32, (m, k // 128), dev), _mat(b, "b", _CODES, (n, k), dev),
-        _mat(b_scales, "b_scales", _F32, (sb, k // 128), dev), int(b_block),
-        _mat(c, "c", _OUT, (m, n), dev), _row_dtype(c, "c"), _stream(stream)), "moe_gemm_e4m3")
+        m, n, k, _arg(a, "a", _CODES, m * k, dev), _mat(a_scales, "a_scales", _F32, (m, g), dev),
+        _arg(b, "b", _CODES, n * k, dev),
+        _mat(b_scales, "b_scales", _F32, (n if b_block == 1 else -(-n // 128), g), dev), b_block,
+        _mat(c, "c", _OUT, (m, n), dev), _row_dtype(c, "c"), _where(stream, dev)),
+        "moe_gemm_e4m3")
 
 
 def moe_grouped_gemm_e4m3(p: Problem, rows, row_scales, w, w_scales, sorted_slots, offsets, tiles,
@@ -490,4 +501,4 @@ def moe_grouped_gemm_e4m3(p: Problem, rows, row_scales, w, w_scales, sorted_slot
         _arg(offsets, "offsets", _I32, E + 1, dev),
         _arg(tiles, "tiles", _I32, 2 * moe_max_tiles(p), dev),
         _arg(num_tiles, "num_tiles", _I32, 1, dev), _mat(out, "out", _OUT, (rm, n), dev),
-        _row_dtype(out, "out"), _stream(stream)), "moe_grouped_gemm_e4m3")
+        _row_dtype(out, "out"), _where(stream, dev)), "moe_grouped_gemm_e4m3")
