@@ -64,13 +64,14 @@ hipError_t launch_quant_rows(const Resolved& r, const void* x, uint8_t* xq, floa
 // pairs of a wave read different banks but for a two-way conflict) and stores 16 bytes of each;
 // a column's 8 threads write its 128 bytes together.  Rows past M are zeros.
 //
-// Quotients: IEEE fp32, x / s for one s and 16 values of x.  With r = 1/s to rounding (v_rcp_f32
-// and one Newton step, once), q = x r, then twice q += r (x - s q) by fma: the steps of the
-// correctly rounded division for operands that need no scaling, 6 operations a value instead of
-// 11.  s outside [2^-96, 2^96] takes the division itself; a quotient too small for the steps to
-// be exact is far below the 2^-10 that e4m3 rounds to 0.  They are at most 448 up to their
-// rounding (up to 450 where s is subnormal), below the 464 from which e4m3 would overflow, so the
-// gfx950 convert (nearest even, NaN kept) needs no clamp.
+// Quotients: IEEE fp32, x / s for one s and 16 values of x: with r = v_rcp_f32(s), q = x r, then
+// q += r (x - s q) by two fma, 4 operations a value with its sign instead of 11.  x and the
+// amax / 448 behind s have 8 significant bits each, so there are 128 x 128 pairs up to powers of
+// two, and every one of them gives the quotient of the division (tests go through them all;
+// without the correction 3 of 1000 codes near a midpoint differ).  s outside [2^-96, 2^96] takes
+// the division itself.  Quotients are at most 448 up to their rounding (up to 450 where s is
+// subnormal), below the 464 from which e4m3 would overflow, so the gfx950 convert (nearest even,
+// NaN kept) needs no clamp.
 // ---------------------------------------------------------------------------------------------
 constexpr int kQuantCols = 64;
 
@@ -114,12 +115,10 @@ __global__ __launch_bounds__(kQuantThreads) void quant_cols_e4m3_kernel(
     if (c >= C) continue;
     const float s = (m[h] == 0.0f) ? 1.0f : m[h] / kE4M3Max;
     if (s >= 0x1p-96f && s <= 0x1p96f) {
-      const float r0 = __builtin_amdgcn_rcpf(s);
-      const float r = __builtin_fmaf(__builtin_fmaf(-s, r0, 1.0f), r0, r0);
+      const float r = __builtin_amdgcn_rcpf(s);
       #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         float q = v[h][i] * r;
-        q = __builtin_fmaf(__builtin_fmaf(-s, q, v[h][i]), r, q);
         q = __builtin_fmaf(__builtin_fmaf(-s, q, v[h][i]), r, q);
         v[h][i] = __builtin_copysignf(q, v[h][i]);       // -0 stays -0
       }

@@ -453,6 +453,27 @@ def test_quantize_cols(device, m, n):
     assert xq.intact() and sc.intact()
 
 
+def test_quantize_cols_every_quotient(device):
+    """Every pair of bf16 significands of a value and of its group's largest, at 24 distances of
+    their exponents and two places of the pair: the codes of the IEEE quotient, bit for bit."""
+    for shift in (0, -70):
+        big = (1 + torch.arange(128) / 128.0)[None, :] * 2.0 ** shift        # one column each
+        x = torch.zeros((24, 2, 128, 128))
+        small = 1 + torch.arange(128).view(2, 64) / 128.0
+        for e in range(24):
+            x[e, :, 1:65] = (small * 2.0 ** (shift - e) * (-1.0) ** e)[:, :, None]
+        x = torch.where(x.abs() <= big, x, 0.0)
+        x[:, :, 0] = big
+        x = x.view(-1, 128)
+        assert torch.equal(x.bfloat16().float(), x)
+        xq, sc = moe.quantize_cols_e4m3(x.bfloat16().to(device))
+        torch.cuda.synchronize()
+        s = big[0] / torch.full((128,), 448.0)
+        want = (x / s[None, :]).to(E4M3).view(torch.uint8).t()
+        assert torch.equal(sc.cpu(), s[:, None].expand(128, 48))
+        assert torch.equal(xq.view(torch.uint8).cpu(), want)
+
+
 def chain_inputs(device, T=200, H=256, n=384, E=8, k=2, bm=32, seed=19):
     g = gen(device, seed)
     p = moe.make_problem(T, H, 128, E, k, "bf16", "e4m3", bm)
