@@ -26,6 +26,7 @@
  *                          expert, a dense projection, their gradients)
  *   moe_grouped_gemm_e4m3  the same over expert-sorted rows
  *   moe_quantize_cols_e4m3 transposed quantisation, the operands of a weight gradient
+ * The outputs of these must not overlap their inputs.
  *
  * Conventions shared by every entry point
  *   - Pointers named as tensors are DEVICE pointers owned by the caller; the
@@ -358,8 +359,8 @@ int moe_unpermute(const moe_problem* p, int32_t row_dtype, const void* rows,
  *   d_weights[t, j] = d_out[t, :] . rows[r, :]            (fp32, a fixed order of additions)
  * d_weights of excluded slots is 0.  Rows of d_rows in valid tiles that hold no slot are zeros;
  * rows past the last valid tile are left untouched.  Either output may be NULL (not both);
- * rows is read for d_weights only and may be NULL without it.  The outputs must not overlap the
- * inputs.  topk_weights NULL: every weight is 1.
+ * rows is read for d_weights only and may be NULL without it.  topk_weights NULL: every weight
+ * is 1.
  * row_dtype: MOE_F32 or MOE_BF16 (d_out, rows and d_rows).
  * In:  d_out row_dtype [T,H]; rows row_dtype [moe_max_padded_slots, H]; slot_row, sorted_slots,
  *      num_tiles: outputs of moe_align for the same problem; topk_weights fp32 [T,top_k]
@@ -414,7 +415,7 @@ int moe_quantize_cols_e4m3(int32_t m, int32_t n, const void* x, uint8_t* xq, flo
  *   d_x  a = d_y by rows,            b = w transposed (codes [k, n], scales [k/128, n/128])
  *   d_w  a = d_y by columns [n, mp], b = x by columns [k, mp], b_block 1
  * Needs m, n >= 1; k a positive multiple of 128, at most 2^22; m and n at most 2^24; and
- * ceil(m/16) * ceil(n/16) <= 2^30 (MOE_ERR_SHAPE otherwise).
+ * ceil(m/16) * ceil(n/16) <= 2^29 (MOE_ERR_SHAPE otherwise).
  * In:  a uint8 [m, k] (e4m3 codes), a_scales fp32 [m, k/128]; b uint8 [n, k], b_scales
  * Out: c c_dtype [m, n]
  * Deterministic: the order of the additions depends on the sizes alone.
@@ -433,8 +434,8 @@ int moe_gemm_e4m3(int32_t m, int32_t n, int32_t k, const uint8_t* a, const float
  * of layers that those two do not describe, and the gradient with respect to the rows (w
  * transposed).
  * Problem: dtype BF16, w_dtype E4M3 (MOE_ERR_DTYPE otherwise); of its sizes T, E, top_k and
- * block_m count.  n >= 1 and k a positive multiple of 128, at most 32768 each; n*k < 2^31
- * (MOE_ERR_SHAPE otherwise).
+ * block_m count.  n >= 1 and k a positive multiple of 128, at most 32768 each; n*k < 2^31 and
+ * moe_max_tiles * ceil(n/128) < 2^23 - 256 (MOE_ERR_SHAPE otherwise).
  * In:  rows uint8 [moe_max_padded_slots, k] (e4m3 codes), row_scales fp32
  *      [moe_max_padded_slots, k/128]; w uint8 [E, n, k]; w_scales fp32 [E, ceil(n/128), k/128];
  *      sorted_slots, offsets, tiles, num_tiles: outputs of moe_align for the same problem

@@ -93,10 +93,14 @@ Resolved resolve(const moe_problem* p) {
   return r;
 }
 
-// Sizes of moe_gemm_e4m3.  k below 2^22 keeps a tile's 256 operand rows within the 31-bit offsets
-// of one buffer descriptor; the tile bound keeps every launch's threads within 32 bits.
+// Sizes of moe_gemm_e4m3 and moe_grouped_gemm_e4m3.  k up to 2^22 keeps a tile's 256 operand rows
+// within the 31-bit offsets of one buffer descriptor.  A launch counts its threads in 32 bits:
+// 2^29 tiles of 16x16 are 2^22 of 128x256 (512 threads each, the smallest that a large dense
+// product runs on), and a grouped launch has at most one workgroup of 512 threads per 128 columns
+// of an m-block, rounded up to a multiple of 256 workgroups.
 constexpr int kGemmMaxK = 1 << 22, kGemmMaxDim = 1 << 24, kQuantMaxDim = 1 << 22;
-constexpr int64_t kMaxGemmTiles = 1LL << 30;   // of 16x16
+constexpr int64_t kMaxGemmTiles = 1LL << 29;   // of 16x16
+constexpr int64_t kMaxGroupedTiles = (1LL << 23) - 257;
 
 int validate_gemm(int32_t m, int32_t n, int32_t k) {
   if (m < 1 || n < 1 || m > kGemmMaxDim || n > kGemmMaxDim) return MOE_ERR_SHAPE;
@@ -534,7 +538,7 @@ int moe_grouped_gemm_e4m3(const moe_problem* p, int32_t n, int32_t k, const uint
       (int64_t)n * k > kI32Max)
     return MOE_ERR_SHAPE;
   const Resolved r = resolve(p);
-  if (r.tiles_max * ((n + 15) / 16) > kMaxGemmTiles) return MOE_ERR_SHAPE;   // grid bound
+  if (r.tiles_max * ((n + 127) / 128) > kMaxGroupedTiles) return MOE_ERR_SHAPE;   // grid bound
   if (!rows || !row_scales || !w || !w_scales || !sorted_slots || !offsets || !tiles ||
       !num_tiles || !out)
     return MOE_ERR_NULL;

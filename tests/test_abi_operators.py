@@ -92,7 +92,8 @@ def test_gemm(lib):
         return lib.moe_gemm_e4m3(m, n, k, *ptr, block, c, dt, None)
     for kw in [dict(m=0), dict(n=0), dict(k=0), dict(k=64), dict(k=200), dict(m=-5),
                dict(m=2 ** 24 + 1), dict(n=2 ** 24 + 1), dict(k=2 ** 22 + 128),
-               dict(m=2 ** 24, n=2 ** 24), dict(block=64), dict(block=0)]:
+               dict(m=2 ** 24, n=2 ** 24), dict(block=64), dict(block=0),
+               dict(m=2 ** 22, n=2 ** 15 + 16), dict(m=2 ** 15 + 1, n=2 ** 22)]:
         assert call(**kw) == S, kw
     assert call(dt=E4M3) == D and call(dt=9) == D
     for i in range(4):
@@ -114,6 +115,9 @@ def test_grouped_gemm(lib):
     assert call(P=problem(H=192, w_dtype="e4m3")) == S
     for kw in [dict(n=0), dict(k=0), dict(k=192), dict(n=32769), dict(k=32768 + 128), dict(n=-1)]:
         assert call(**kw) == S, kw
+    # more workgroups than a launch's thread count holds: 2^19 m-blocks of 16 rows, 17 n-blocks
+    many = problem(T=2 ** 20, H=256, E=8, top_k=8, w_dtype="e4m3", block_m=16)
+    assert call(P=many, n=16 * 128 + 1) == S
     for i in range(8):
         p = [ok] * 8
         p[i] = None
