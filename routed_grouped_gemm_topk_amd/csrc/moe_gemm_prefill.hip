@@ -110,7 +110,7 @@ __device__ __forceinline__ i32x4 buf_rsrc(const void* base, uint32_t bytes) {
 // 64 lanes x 16 bytes from the buffer at voff + soff straight to LDS at M0 (MUBUF
 // buffer_load_dwordx4 ... lds).
 __device__ __forceinline__ void buf_dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                ::"v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
 }
 

@@ -180,14 +180,15 @@ inline int64_t xcd_chunked_grid(int64_t g) {
 // Direct-to-LDS copies (gfx950 global_load_lds_dwordx4 / _dword): each wave instruction lands
 // 64 lanes x 16 (or 4) bytes contiguously in LDS at M0.  Issued from inline assembly with
 // explicit vmcnt waits: the compiler's own tracking of LDS DMA makes every LDS read wait for
-// every outstanding copy, which would drain a multi-stage ring each k-slice.
+// every outstanding copy, which would drain a multi-stage ring each k-slice.  A load to LDS needs
+// one wait state after a scalar write of M0; the compiler does not look into assembly for it.
 __device__ __forceinline__ void lds_dma16(const void* src, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_addr)
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_addr)
                : "memory");
 }
 
 __device__ __forceinline__ void lds_dma4(const void* src, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_addr)
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_addr)
                : "memory");
 }
 

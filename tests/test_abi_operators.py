@@ -1,6 +1,9 @@
 """Refusals of the operators around the layer (rows in expert-sorted order, gradients, products of
 e4m3 codes): every bad argument is turned down on the host, before any HIP call."""
 import ctypes
+import glob
+import os
+import re
 
 import pytest
 import torch
@@ -144,3 +147,14 @@ def test_binding_refuses_wrong_tensors():
     if torch.cuda.is_available():
         with pytest.raises(ValueError):
             moe.moe_unpermute(p, torch.zeros(2), torch.zeros(2), None, torch.zeros(2))
+
+
+def test_copies_to_lds_wait_for_m0():
+    """A load to LDS needs a wait state after the write of M0, which assembly has to hold itself."""
+    found = 0
+    for path in glob.glob(os.path.join(os.path.dirname(moe.__file__), "csrc", "*")):
+        with open(path) as f:
+            for rest in re.findall(r"s_mov_b32 m0, %\d\\n\\t(\w+)", f.read()):
+                assert rest == "s_nop", path
+                found += 1
+    assert found >= 6
