@@ -56,6 +56,7 @@ from ._lib import (  # noqa: F401
     moe_validate,
     moe_workspace_bytes,
     status_str,
+    _where,
 )
 
 
@@ -129,9 +130,7 @@ def _new(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
         return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
-    if stream.device_index != torch.cuda.current_device():
-        raise ValueError(f"stream: of device {stream.device_index}, the current device is "
-                         f"{torch.cuda.current_device()}")
+    _where(stream, torch.cuda.current_device())          # of the current device, or refused
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 

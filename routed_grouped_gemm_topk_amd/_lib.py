@@ -361,7 +361,7 @@ _ROW_DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
 _OUT = (torch.bfloat16, torch.float32)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # None: torch without GPUs
 
 
 def _row_dtype(t: torch.Tensor, name: str) -> int:
@@ -394,7 +394,11 @@ def _mat(t: Optional[torch.Tensor], name: str, dtypes: tuple, shape: tuple, dev:
 
 def _where(stream, dev: int):
     """The stream's handle; by default the current stream of `dev`."""
-    return _raw_stream(dev) if stream is None else _stream(stream)
+    if stream is None:
+        return _raw_stream(dev)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"stream: of device {stream.device_index}, the current device is {dev}")
+    return _stream(stream)
 
 
 def moe_permute(p: Problem, x, x_scales, slot_row, sorted_slots, num_tiles, rows, row_scales,
