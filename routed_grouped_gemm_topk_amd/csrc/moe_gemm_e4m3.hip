@@ -356,11 +356,12 @@ struct TileGemm {
           }
         }
         sp = BROW ? sa_cur : sa_cur * s1;
-        if (KG > 1 && kt * KG + kg >= KT) sp = 0.0f;
+        const bool repeated = KG > 1 && kt * KG + kg >= KT;   // adds 0, also under infinite scales
+        if (repeated) sp = 0.0f;
         if constexpr (BROW) {
           if (i == 0)
             #pragma unroll
-            for (int j = 0; j < FN; ++j) s4p[j] = s4[j];
+            for (int j = 0; j < FN; ++j) s4p[j] = repeated ? f32x4{0.f, 0.f, 0.f, 0.f} : s4[j];
         }
         sa_cur = sa_nxt;
         if (i + 1 == FM) read_sb();

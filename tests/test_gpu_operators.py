@@ -338,9 +338,12 @@ def gemm_tol(ref, mag, k, dtype):
 
 
 def gemm_norm(got, ref, dtype):
-    """Relative error in the 2-norm: rounding to bf16 alone is at most 2^-8 per value, the sums
-    below it 2^-15 (bf16) and 2^-21 (fp32: an eighth of the 2^-18 or so that a chain of 60
-    additions and a group's 128 may reach one on top of the other)."""
+    """Relative error in the 2-norm, for operands whose sums wander like sqrt(g) over G <= 56
+    groups.  fp32: one rounding of the running sum per group, each at most u and uniform, so
+    u / sqrt(3) * sqrt(g / G) of the result in the mean square, together u sqrt(G / 6) = 3.1 u; a
+    group's own product at most 7 roundings (4 instructions, 2 scales, 1 fma), together u sqrt(7 /
+    3) = 1.5 u; both 3.4 u, held at 8 u = 2^-21.  bf16: at most 2^-8 per value from the rounding,
+    and the instruction's 2^-16 (1.4e-5, its measured error on such operands) held at 2^-15."""
     err = float((got.double() - ref).norm() / ref.norm()) if ref.numel() else 0.0
     assert err <= (UBF + 2.0 ** -15 if dtype == "bf16" else 2.0 ** -21), err
 
@@ -387,6 +390,134 @@ def test_gemm_e4m3_special_values(device, m, n, k):
         c_ = moe.gemm_e4m3(a, sa, b, sb, out_dtype=TD[dtype], b_block=1)
         torch.cuda.synchronize()
         close(c_, ref, gemm_tol(torch.nan_to_num(ref, 0.0, 0.0, 0.0), mag, k, dtype), dtype)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 33, 640), (17, 64, 128), (17, 64, 640), (33, 2048, 384),
+                                   (128, 7168, 128), (130, 2048, 640)])
+@pytest.mark.parametrize("b_block", [128, 1])
+def test_gemm_e4m3_infinite_last_scales(device, m, n, k, b_block):
+    """Infinite scales of the last group, on either side: an infinity of the product's sign, for
+    any number of groups."""
+    say("infinite scales", m, n, k, b_block)
+    a = torch.full((m, k), 0x38, dtype=torch.uint8, device=device)        # ones
+    b = torch.full((n, k), 0x38, dtype=torch.uint8, device=device)
+    b[::2] = 0xB8                                                        # and rows of minus ones
+    sa = torch.ones((m, k // 128), device=device)
+    sb = torch.ones((n if b_block == 1 else -(-n // 128), k // 128), device=device)
+    sb[0, -1] = sa[m - 1, -1] = float("inf")
+    sign = torch.where(torch.arange(n, device=device) % 2 == 0, -1.0, 1.0).double()
+    ref = (sign * k).expand(m, n).clone()
+    ref[m - 1] = sign * float("inf")
+    ref[:, : b_block] = (sign * float("inf"))[: b_block]
+    for dtype in ("bf16", "f32"):
+        c_ = moe.gemm_e4m3(a, sa, b, sb, out_dtype=TD[dtype], b_block=b_block)
+        torch.cuda.synchronize()
+        assert torch.equal(c_.double(), ref), dtype       # multiples of 128 below 2^10: exact
+
+
+def test_past_32_bits(device):
+    """Rows, products and codes whose last elements lie past 2^32 bytes and 2^31 elements."""
+    def rows_of(t):                                        # first and last ones, and some between
+        n = t.shape[0]
+        return torch.tensor([0, 1, n // 3, n // 2 + 1, n - 2, n - 1], device=device)
+    T, H, E, k, bm = 34000, 16384, 4, 4, 128
+    say("rows", T, H)
+    p, a, used, ss, held = aligned(device, T, H, E, k, bm, "all", 40)
+    assert used * H > 2 ** 31
+    g = gen(device, 41)
+    x = torch.randn((T, H), generator=g, device=device).bfloat16()
+    w = torch.rand((T, k), generator=g, device=device) + 0.5
+    rows, _ = moe.permute(p, x, a)
+    out = moe.unpermute(p, rows, a, w)
+    d_rows, d_w = moe.unpermute_bwd(p, x, rows, a, w)
+    torch.cuda.synchronize()
+    r = rows_of(rows[:used])
+    tok = (ss[r] // k).clamp(max=T - 1)
+    want = torch.where(held[r, None], x[tok], 0.0)
+    assert torch.equal(rows[r], want)
+    wr = w.view(-1)[ss[r].clamp(max=T * k - 1)][:, None].double()
+    close(d_rows[r], wr * want.double(), (UBF + 2 * U32) * wr * want.double().abs(), "d_rows")
+    t = rows_of(x)
+    xt, wt = x[t].double(), w[t].double().sum(1, keepdim=True)
+    close(out[t], xt * wt, (UBF + 2 * (k + 1) * U32) * xt.abs() * wt, "out")
+    sq = (xt * xt).sum(1, keepdim=True).expand(-1, k)
+    close(d_w[t], sq, (H / 64 + 8) * U32 * sq, "d_weights")
+    del x, rows, out, d_rows
+    m, n, kk = 70000, 32768, 128
+    for dtype, b_block in (("bf16", 128), ("f32", 1)):
+        say("gemm", m, n, dtype)
+        aa, sa, b, sb = operands(device, m, n, kk, b_block, 42)
+        c = moe.gemm_e4m3(aa, sa, b, sb, out_dtype=TD[dtype], b_block=b_block)
+        torch.cuda.synchronize()
+        t = rows_of(c)
+        ref, mag = product(aa.view(torch.uint8)[t], sa[t], b, sb, b_block)
+        close(c[t], ref, gemm_tol(ref, mag, kk, dtype), "c")
+        del c
+    say("grouped")
+    T, E, k, bm, n = 20000, 4, 4, 64, 32768
+    p, a, used, ss, held = aligned(device, T, 128, E, k, bm, "all", 43, fp8=True)
+    assert used * n > 2 ** 31
+    rows, rs, w, _ = operands(device, ss.numel(), E * n, kk, 128, 44)
+    ws = torch.rand((E, n // 128, 1), generator=g, device=device) + 0.1
+    c = moe.grouped_gemm_e4m3(p, rows, rs, w.view(E, n, kk), ws, a)
+    torch.cuda.synchronize()
+    of = a["offsets"].tolist()
+    for e in range(E):
+        t = of[e] + rows_of(c[of[e]:of[e + 1]])
+        ref, mag = product(rows.view(torch.uint8)[t], rs[t], w[e * n:(e + 1) * n], ws[e], 128)
+        ref, mag = (torch.where(held[t, None], v, 0.0) for v in (ref, mag))
+        close(c[t], ref, gemm_tol(ref, mag, kk, "bf16"), f"expert {e}")
+    del c
+    m, n = 2 ** 17 + 5, 16384 + 8
+    say("quantize_cols", m, n)
+    x = torch.randn((m, n), generator=g, device=device).bfloat16()
+    xq, sc = moe.quantize_cols_e4m3(x)
+    torch.cuda.synchronize()
+    t = rows_of(xq)
+    part, s1 = moe.quantize_cols_e4m3(x[:, t].repeat(1, 4).contiguous())   # the same columns alone
+    torch.cuda.synchronize()
+    assert torch.equal(xq.view(torch.uint8)[t], part.view(torch.uint8)[:6])
+    assert torch.equal(sc[t], s1[:6])
+
+
+def test_two_streams_at_once(device):
+    """The operators share no memory: calls that overlap on two streams give the bits of calls
+    one after the other."""
+    args = [chain_inputs(device, T=1500, n=1024, bm=64, seed=50 + i) for i in range(2)]
+    big = [operands(device, 1024, 4096, 2048, 128, 60 + i) for i in range(2)]
+    few = [operands(device, 100, 1024, 2048, 128, 70 + i) for i in range(2)]
+
+    def work(i, stream=None):
+        out = chain(*args[i], stream=stream)
+        return [out[2], out[4], out[5], moe.gemm_e4m3(*big[i], stream=stream),
+                moe.gemm_e4m3(*few[i], out_dtype=torch.float32, stream=stream),
+                *moe.quantize_cols_e4m3(args[i][2], stream=stream), out]
+    ref = [work(i) for i in range(2)]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = [[work(i, side[i]) for i in range(2)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for i in range(2):
+            for x, y in zip(pair[i][:-1], ref[i][:-1]):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_stream_arguments(device):
+    """A raw handle (0 is the default stream) or a Stream; one of no use is refused."""
+    p, lg, x, w, ws, d_out = chain_inputs(device, seed=23)
+    a = moe.route_align(p, lg, True)
+    want, _ = moe.permute(p, x, a)
+    torch.cuda.synchronize()
+    used = int(a["num_tiles"]) * p.block_m
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for s in (0, side.cuda_stream, side):
+        rows, _ = moe.permute(p, x, a, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(rows[:used], want[:used])
+    with pytest.raises((TypeError, ValueError)):
+        moe.permute(p, x, a, stream="side")
 
 
 GROUPED = [(1, 4, 1, 16, 100, 256, "all"), (64, 8, 2, 16, 576, 512, "all"),
