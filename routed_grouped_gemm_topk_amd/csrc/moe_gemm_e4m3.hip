@@ -241,7 +241,8 @@ struct TileGemm {
         for (int i = 0; i < NSW; ++i) {
           const int q = wave * NSW + i;
           buf_dma4(q < SA ? rsa : rsb, soff[i], (uint32_t)kt * 4,
-                   __builtin_amdgcn_readfirstlane(lds_base + SC_OFF + (buf * KG + kg) * SSTAGE) + q * 256);
+                   __builtin_amdgcn_readfirstlane(lds_base + SC_OFF + (buf * KG + kg) * SSTAGE) +
+                       q * 256);
         }
       }
     };
@@ -459,16 +460,21 @@ struct TileGemm {
 
     // ---- c: lane holds row lane & 15 of a, b's rows (lane >> 4) * 4 + v.  Stored from there, a
     // row's line would be written in pieces of 32 bytes (bf16): each wave turns its fragments
-    // around in LDS, 16 rows at a time, and stores 16 bytes a lane, WTN neighbouring values a row
-    // (grouped 7168 x 2048 over 256 experts: 889 -> 863 us). ------------------------------------
+    // around in LDS, 16 rows at a time, and stores WTN neighbouring values a row: 16 bytes a lane
+    // where every row of c begins on such a bound (grouped 7168 x 2048 over 256 experts: 889 ->
+    // 863 us), else 4 bytes, or the 2 of a bf16 value where N is odd (6418 x 666 x 896: to fp32
+    // 35.3 -> 27.0 us, to bf16 22.6 -> 14.4; 346 x 8243 x 256: to bf16 12.3 -> 8.7). ------------
     auto value = [&](int i, int j) {
       return (i * WM + wm) * 16 + fr < t.rows ? acc[i][j] : f32x4{0.f, 0.f, 0.f, 0.f};
     };
-    if (g.N % (16 / ES) == 0) {
-      if (KG == 1) __syncthreads();                    // the ring is done with (KG > 1: above)
-      char* mine = lds + OUT_OFF + wave * 16 * PITCH;
-      constexpr int CPR = WTN * ES / 16;               // 16-byte chunks per row
-      constexpr int RPP = kWave / CPR < 16 ? kWave / CPR : 16;   // rows per store
+    if (KG == 1) __syncthreads();                      // the ring is done with (KG > 1: above)
+    char* mine = lds + OUT_OFF + wave * 16 * PITCH;
+    auto store = [&](auto type) {
+      using V = decltype(type);
+      constexpr int VPR = WTN * ES / sizeof(V);        // stores per row
+      constexpr int RPP = kWave / VPR < 16 ? kWave / VPR : 16;   // rows per instruction
+      static_assert(VPR <= kWave, "a row per instruction");
+      const int c = lane % VPR, n = wn * WTN + c * (int)sizeof(V) / ES;
       #pragma unroll
       for (int i = 0; i < FM; ++i) {
         #pragma unroll
@@ -477,32 +483,23 @@ struct TileGemm {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         #pragma unroll
         for (int r0 = 0; r0 < 16; r0 += RPP) {
-          const int r = r0 + lane / CPR, m = (i * WM + wm) * 16 + r;
-          const int n = wn * WTN + lane % CPR * (16 / ES);
-          if (lane < RPP * CPR && m < t.zero_rows && n < t.cols) {
-            const i32x4 v = *reinterpret_cast<const i32x4*>(mine + r * PITCH + lane % CPR * 16);
-            i32x4* to = reinterpret_cast<i32x4*>(
-                (char*)g.c + ((t.row0 + m) * (int64_t)g.N + t.n0 + n) * ES);
-            if constexpr (PAST) __builtin_nontemporal_store(v, to);
+          const int r = r0 + lane / VPR, m = (i * WM + wm) * 16 + r;
+          if (lane < RPP * VPR && m < t.zero_rows && n < t.cols) {
+            const V v = *reinterpret_cast<const V*>(mine + r * PITCH + c * sizeof(V));
+            V* to = reinterpret_cast<V*>((char*)g.c +
+                                         ((t.row0 + m) * (int64_t)g.N + t.n0 + n) * ES);
+            if constexpr (PAST && sizeof(V) == 16) __builtin_nontemporal_store(v, to);
             else *to = v;
           }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
-      return;
+    };
+    if (g.N % (16 / ES) == 0) return store(i32x4{});
+    if constexpr (!F32) {
+      if (g.N & 1) return store(uint16_t{});
     }
-    const bool vec = (g.N & 3) == 0;
-    #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int m = (i * WM + wm) * 16 + fr;
-      if (m >= t.zero_rows) continue;
-      #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int n = wn * WTN + j * 16 + fq * 4;
-        if (n < t.cols)
-          store4<F32>(g.c, (t.row0 + m) * (int64_t)g.N + t.n0 + n, value(i, j), t.cols - n, vec);
-      }
-    }
+    store(uint32_t{});
   }
 };
 
@@ -658,10 +655,9 @@ __global__ __launch_bounds__(WM * WN * KG * kWave) void tile_kernel(Args g) {
 // where the last round would fill at most half of the units, its tiles run as two halves of
 // 128 x 256 each, so that the round takes about half as long.  Every element's sum is the same
 // either way.
-template <bool BROW>
 __global__ __launch_bounds__(512) void large_kernel(Args g, int full, int full_grid) {
-  using G = TileGemm<256, 256, 2, 4, 1, 2, BROW, false>;
-  using H = TileGemm<128, 256, 2, 4, 1, 2, BROW, false>;
+  using G = TileGemm<256, 256, 2, 4, 1, 2, false, false>;
+  using H = TileGemm<128, 256, 2, 4, 1, 2, false, false>;
   __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
   if ((int)blockIdx.x < full_grid) {
     const int logical = xcd_chunked<kChunk>(blockIdx.x, full);
@@ -718,7 +714,8 @@ __global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void grouped_kernel(Args
   // 957 against 1059 us; equal at K = 2048).  With several m-blocks they would read the weights
   // from memory again for each.
   if constexpr (BM <= 64) {
-    if (g.offsets[r.e + 1] - g.offsets[r.e] == BM) return G::template run<true, true, PAST>(g, t, lds);
+    if (g.offsets[r.e + 1] - g.offsets[r.e] == BM)
+      return G::template run<true, true, PAST>(g, t, lds);
   }
   G::template run<true, false, PAST>(g, t, lds);
 }
@@ -727,8 +724,8 @@ template <int BM, int BN, int WM, int WN, int KG, int NS, bool BROW, bool F32>
 hipError_t run_tile(const Args& a, hipStream_t s) {
   const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
   hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, KG, NS, BROW, F32>),
-                     dim3((unsigned)xcd_chunked_grid<kChunk>(tiles)), dim3(WM * WN * KG * kWave), 0, s,
-                     a);
+                     dim3((unsigned)xcd_chunked_grid<kChunk>(tiles)), dim3(WM * WN * KG * kWave), 0,
+                     s, a);
   return hipGetLastError();
 }
 
@@ -746,39 +743,34 @@ hipError_t run_grouped(const Args& a, bool f32, hipStream_t s) {
   const int64_t tiles = (int64_t)a.tiles_max * ((a.N + BN - 1) / BN);
   const dim3 grid((unsigned)xcd_chunked_grid<kChunk>(tiles)), block(WM * WN * KG * kWave);
   if (f32)
-    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, WPS, PAST, true>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, WPS, PAST, true>), grid, block, 0, s,
+                       a);
   else
-    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, WPS, PAST, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((grouped_kernel<BM, BN, WM, WN, KG, NS, WPS, PAST, false>), grid, block, 0,
+                       s, a);
   return hipGetLastError();
 }
 
-}  // namespace q8
-
-namespace q8 {
-
-template <bool BROW>
 hipError_t run_large(const Args& a, int cus, hipStream_t s) {
   const int total = (int)(((int64_t)a.M + 255) / 256 * (((int64_t)a.N + 255) / 256));
   const int rem = total % cus;
   const int full = total > cus && rem * 2 <= cus ? total - rem : total;
   const int full_grid = (int)xcd_chunked_grid<kChunk>(full);
   const int halves = ((total - full) * 2 + 7) / 8 * 8;
-  hipLaunchKernelGGL(large_kernel<BROW>, dim3((unsigned)(full_grid + halves)), dim3(512), 0, s, a,
+  hipLaunchKernelGGL(large_kernel, dim3((unsigned)(full_grid + halves)), dim3(512), 0, s, a,
                      full, full_grid);
   return hipGetLastError();
 }
 
-// Which kernel: the largest tile whose tiles still are about as many as the compute units (C),
-// since a product that leaves units idle takes the time of one tile, and a small tile's time is
-// that of its steps along K.  Measured with K of 512, 2048 and 7168, M and N from 1 to 7168
+// Which kernel, for few tiles: the largest one whose tiles still are at most as many as the compute
+// units, since a product that leaves units idle takes the time of one tile, and a small tile's time
+// is that of its steps along K.  Measured with K of 512, 2048 and 7168, M and N from 1 to 7168
 // (us, K = 2048; the tile chosen against the next larger and smaller ones):
 //   M = 1,    N = 7168: 16-row stream 4.9-5.1, 16x64 5.7
 //   M = 64,   N = 2048: 16x64 5.9,  32x64 6.5
 //   M = 64,   N = 7168: 32x64 6.4,  16x64 8.3,  64x64 8.2
 //   M = 128,  N = 7168: 64x64 8.1,  32x64 9.3,  64x128 10.9
 //   M = 256,  N = 7168: 64x128 10.7, 64x64 14.4, 128x128 15.2
-//   M = 1024, N = 7168: 128x128 25.3, 64x128 30.5, 256x256 40
-//   M = 2048, N = 7168: 256x256 40.7, 128x128 47.2
 template <bool BROW, bool F32>
 hipError_t run_dense(const Args& a, int cus, hipStream_t s) {
   auto tiles = [&](int bm, int bn) {
@@ -794,11 +786,46 @@ hipError_t run_dense(const Args& a, int cus, hipStream_t s) {
   if (tiles(32, 64) <= cus) return run_tile<32, 64, 1, 4, 2, 3, BROW, F32>(a, s);
   if (tiles(64, 64) <= cus) return run_tile<64, 64, 2, 2, 2, 3, BROW, F32>(a, s);
   if (tiles(64, 128) <= cus) return run_tile<64, 128, 2, 4, 1, 3, BROW, F32>(a, s);
-  // 128x128 tiles run two to a unit (0.73 of a 256x256 tile's 1.88 us per slice each)
-  if (tiles(128, 128) * 2 <= cus * 5) return run_tile<128, 128, 2, 4, 1, 2, BROW, F32>(a, s);
-  // the bf16 multiplication of an fp32 result does not fit 256x256 tiles in registers
-  if constexpr (F32) return run_tile<128, 256, 2, 4, 1, 2, BROW, true>(a, s);
-  else return run_large<BROW>(a, cus, s);
+  // More tiles than that: the size whose rounds over the units take least.  `whole` is the time of
+  // a round per slice (1/100 us), `half` that of a last round which fills at most half of its
+  // places (two per unit for 128x128 tiles; 256x256 tiles run as halves then), `ends` the slices
+  // that a round's start and end are worth; all fitted to 80 shapes of 300 to 8192 rows (rms 4-7%).
+  // The size chosen takes 0.3-0.9% more than the best one of each shape; the best single one,
+  // 128x128 (bf16) and 64x128 (fp32), 5-10%.
+  auto price = [&](int bm, int bn, int places, int whole, int half, int ends) {
+    const int64_t n = tiles(bm, bn), per = (int64_t)cus * places, rem = n % per;
+    return (n / per * whole + (rem == 0 ? 0 : rem * 2 <= per ? half : whole)) *
+           (a.K / ROWB + ends);
+  };
+  if constexpr (F32) {
+    // the bf16 multiplication does not fit larger tiles in registers
+    const int64_t p64 = BROW ? price(64, 128, 1, 73, 61, 2) : price(64, 128, 1, 62, 51, 3);
+    const int64_t p128 = BROW ? price(128, 128, 2, 258, 132, 3) : price(128, 128, 2, 230, 117, 3);
+    const int64_t p256 = BROW ? price(128, 256, 1, 201, 201, 3) : price(128, 256, 1, 185, 185, 3);
+    if (p64 < std::min(p128, p256)) return run_tile<64, 128, 2, 4, 1, 3, BROW, true>(a, s);
+    if (p256 < p128) return run_tile<128, 256, 2, 4, 1, 2, BROW, true>(a, s);
+    return run_tile<128, 128, 2, 4, 1, 2, BROW, true>(a, s);
+  } else {
+    const int64_t p128 = BROW ? price(128, 128, 2, 140, 86, 2) : price(128, 128, 2, 114, 72, 3);
+    const int64_t p256 = BROW ? price(128, 256, 1, 130, 130, 4) : price(128, 256, 1, 99, 99, 5);
+    const int64_t p192 = BROW ? price(192, 256, 1, 159, 159, 4) : price(192, 256, 1, 128, 128, 5);
+    const int64_t least = std::min({p128, p256, p192});
+    // scales per row of b do not fit 256x256 tiles in registers (2.8 us per slice)
+    if constexpr (!BROW) {
+      if (price(256, 256, 1, 153, 99, 5) < least) return run_large(a, cus, s);
+    }
+    if (p128 > least) {
+      if (p192 < p256) return run_tile<192, 256, 2, 4, 1, 2, BROW, false>(a, s);
+      return run_tile<128, 256, 2, 4, 1, BROW ? 2 : 3, BROW, false>(a, s);
+    }
+  }
+  // One tile on a unit has no other's work to wait behind: a third stage, once K is long enough
+  // for its longer start (2048 x 2048: K = 4096 30.5 -> 27.6 us; 1024 x 4096: K = 2048 15.2 -> 17.0).
+  if constexpr (!F32) {
+    if (tiles(128, 128) <= cus && a.K >= 24 * ROWB)
+      return run_tile<128, 128, 2, 4, 1, 3, BROW, false>(a, s);
+    return run_tile<128, 128, 2, 4, 1, 2, BROW, false>(a, s);
+  }
 }
 
 }  // namespace q8
@@ -810,7 +837,8 @@ hipError_t launch_gemm_e4m3(int M, int N, int K, const uint8_t* a, const float* 
   g.a = a; g.sa = sa; g.b = b; g.sb = sb; g.c = c;
   g.M = M; g.N = N; g.K = K;
   const int cus = std::max(device_cu_count(), 8);
-  if (b_rows) return c_f32 ? q8::run_dense<true, true>(g, cus, s) : q8::run_dense<true, false>(g, cus, s);
+  if (b_rows)
+    return c_f32 ? q8::run_dense<true, true>(g, cus, s) : q8::run_dense<true, false>(g, cus, s);
   return c_f32 ? q8::run_dense<false, true>(g, cus, s) : q8::run_dense<false, false>(g, cus, s);
 }
 

@@ -179,8 +179,8 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(Args g) {
 // slot's d_rows row and (sums in a fixed order) its d_w.  With one wavefront the waves of a
 // workgroup belong to neighbouring slots, most of them of one token, whose d_out row then comes
 // from L1/L2.  With few slots a workgroup's four share one (one token, top 8, 7168 columns: 8.1 us
-// with one).  LARGE as above (97.8 -> 93.3 us from memory); stores past them, 86 us, cost whoever reads d_rows next more than
-// they gain (with a reader behind it 119 -> 137 us).
+// with one).  LARGE as above (97.8 -> 93.3 us from memory); stores past the caches as well, 86 us,
+// cost whoever reads d_rows next more than they gain (with a reader behind it 119 -> 137 us).
 template <bool BF16, int WPS, bool LARGE>
 __device__ __forceinline__ void unpermute_bwd_block(const Args& g, int block, float* sums) {
   if (block >= g.token_blocks) {
@@ -249,7 +249,8 @@ template <bool BF16, int WPS, bool LARGE>
 __global__ __launch_bounds__(kThreads) void unpermute_bwd_kernel(Args g) {
   static_assert(WPS == 1 || WPS == kThreads / kWave, "one slot per workgroup, or one per wave");
   __shared__ float sums[kThreads / kWave];
-  for (int b = blockIdx.x; b < g.blocks; b += gridDim.x) unpermute_bwd_block<BF16, WPS, LARGE>(g, b, sums);
+  for (int b = blockIdx.x; b < g.blocks; b += gridDim.x)
+    unpermute_bwd_block<BF16, WPS, LARGE>(g, b, sums);
 }
 
 Args args(const Resolved& r, int row_dtype) {
@@ -333,9 +334,11 @@ hipError_t launch_unpermute_bwd(const Resolved& r, int row_dtype, const void* d_
   const dim3 grid((unsigned)std::min(a.blocks, pm::kMaxGrid)), block(pm::kThreads);
   pm::by_type(row_dtype == MOE_BF16, pm::large(r, a), [&](auto bf16, auto large) {
     if (few)
-      hipLaunchKernelGGL((pm::unpermute_bwd_kernel<bf16.value, kWaves, false>), grid, block, 0, s, a);
+      hipLaunchKernelGGL((pm::unpermute_bwd_kernel<bf16.value, kWaves, false>), grid, block, 0, s,
+                         a);
     else
-      hipLaunchKernelGGL((pm::unpermute_bwd_kernel<bf16.value, 1, large.value>), grid, block, 0, s, a);
+      hipLaunchKernelGGL((pm::unpermute_bwd_kernel<bf16.value, 1, large.value>), grid, block, 0, s,
+                         a);
   });
   return hipGetLastError();
 }
