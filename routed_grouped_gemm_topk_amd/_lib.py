@@ -362,6 +362,7 @@ _CODES = (torch.float8_e4m3fn, torch.uint8)
 _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
 _OUT = (torch.bfloat16, torch.float32)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # None: torch without GPUs
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _row_dtype(t: torch.Tensor, name: str) -> int:
@@ -406,7 +407,7 @@ def moe_permute(p: Problem, x, x_scales, slot_row, sorted_slots, num_tiles, rows
     dt = _row_dtype(x, "x")
     same = _CODES if dt == MOE_E4M3 else (x.dtype,)
     rm = moe_max_padded_slots(p)
-    dev = torch.cuda.current_device()
+    dev = _device()
     T, H = p.T, p.H
     _checked(load().moe_permute(
         ctypes.byref(p), dt, _arg(x, "x", same, T * H, dev),
@@ -421,7 +422,7 @@ def moe_permute(p: Problem, x, x_scales, slot_row, sorted_slots, num_tiles, rows
 def moe_unpermute(p: Problem, rows, slot_row, topk_weights, out, stream=None) -> None:
     dt = _row_dtype(rows, "rows")
     same = (rows.dtype,)
-    dev = torch.cuda.current_device()
+    dev = _device()
     T, H = p.T, p.H
     N = T * p.top_k
     _checked(load().moe_unpermute(
@@ -436,7 +437,7 @@ def moe_unpermute_bwd(p: Problem, d_out, rows, slot_row, sorted_slots, num_tiles
     dt = _row_dtype(d_out, "d_out")
     same = (d_out.dtype,)
     rm = moe_max_padded_slots(p)
-    dev = torch.cuda.current_device()
+    dev = _device()
     T, H = p.T, p.H
     N = T * p.top_k
     _checked(load().moe_unpermute_bwd(
@@ -451,7 +452,7 @@ def moe_unpermute_bwd(p: Problem, d_out, rows, slot_row, sorted_slots, num_tiles
 
 def moe_route_bwd(p: Problem, logits, renormalize: bool, topk_ids, d_weights, d_logits,
                   stream=None) -> None:
-    dev = torch.cuda.current_device()
+    dev = _device()
     T = p.T
     N, L = T * p.top_k, T * p.E
     _checked(load().moe_route_bwd(
@@ -465,7 +466,7 @@ def moe_quantize_cols_e4m3(x, xq, scales, stream=None) -> None:
         raise ValueError("x: expected a matrix")
     m, n = x.shape
     groups = -(-m // 128)
-    dev = torch.cuda.current_device()
+    dev = _device()
     _checked(load().moe_quantize_cols_e4m3(
         m, n, _arg(x, "x", _BF16, m * n, dev), _mat(xq, "xq", _CODES, (n, groups * 128), dev),
         _mat(scales, "scales", _F32, (n, groups), dev), _where(stream, dev)),
@@ -480,7 +481,7 @@ def moe_gemm_e4m3(a, a_scales, b, b_scales, b_block: int, c, stream=None) -> Non
     m, k = a.shape
     n = b.shape[0]
     g = k // 128
-    dev = torch.cuda.current_device()
+    dev = _device()
     _checked(load().moe_gemm_e4m3(
         m, n, k, _arg(a, "a", _CODES, m * k, dev), _mat(a_scales, "a_scales", _F32, (m, g), dev),
         _arg(b, "b", _CODES, n * k, dev),
@@ -495,7 +496,7 @@ def moe_grouped_gemm_e4m3(p: Problem, rows, row_scales, w, w_scales, sorted_slot
         raise ValueError("w: expected [E, n, k]")
     E, n, k = w.shape
     rm = moe_max_padded_slots(p)
-    dev = torch.cuda.current_device()
+    dev = _device()
     _checked(load().moe_grouped_gemm_e4m3(
         ctypes.byref(p), n, k, _mat(rows, "rows", _CODES, (rm, k), dev),
         _mat(row_scales, "row_scales", _F32, (rm, k // 128), dev),
