@@ -10,7 +10,10 @@
 //
 // All three move rows and compute next to nothing: HBM bounds them.  They walk the tokens, not
 // the sorted rows, so each token row (x, d_out) is read once for its top_k slots, and a token's
-// slots are added by one thread in ascending j: no atomics, same bits on every run.
+// slots are added by one thread in ascending j: no atomics, same bits on every run.  Walking the
+// sorted rows instead, each gathering its token's, permute takes 64 us of the 53 that it takes for
+// 8192 tokens, top 6, 2048 bf16 columns (235 MB: 4.4 TB/s; a fill of as many bytes runs at 6.6, a
+// copy at 6.0); one workgroup per slot of a token 59 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -21,7 +24,10 @@ namespace moe {
 namespace pm {
 
 constexpr int kThreads = 256;
-constexpr int kPadRows = 8;      // sorted rows whose padding one workgroup clears
+// Sorted rows whose padding one workgroup clears.  Fewer leave more workgroups without any (4 rows:
+// 8192 tokens, top 6 of 64, 2048 columns 53.5 -> 56.3 us), more clear it one after the other (16
+// rows: 2048 tokens, top 8 of 256, 7168 codes, half of the rows padding, 54.5 -> 58.8 us).
+constexpr int kPadRows = 8;
 
 struct Args {
   const i32x4* x;               // permute: x; unpermute(_bwd): rows

@@ -62,7 +62,8 @@ hipError_t launch_quant_rows(const Resolved& r, const void* x, uint8_t* xq, floa
 // tokens.  One workgroup takes 128 rows x 64 columns: the tile goes through LDS, a thread takes
 // 16 rows of two neighbouring columns (pitch 33 words: the 8 threads of a column pair and the 8
 // pairs of a wave read different banks but for a two-way conflict) and stores 16 bytes of each;
-// a column's 8 threads write its 128 bytes together.  Rows past M are zeros.
+// a column's 8 threads write its 128 bytes together.  Rows past M are zeros.  HBM bounds it:
+// 4001 x 7168 in 22.8 us (89 MB, 3.9 TB/s), 4001 x 2048 in 10.5 us.
 //
 // Quotients: IEEE fp32, x / s for one s and 16 values of x: with r = v_rcp_f32(s), q = x r, then
 // q += r (x - s q) by two fma, 4 operations a value with its sign instead of 11.  x and the
