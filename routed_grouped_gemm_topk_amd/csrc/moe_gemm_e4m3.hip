@@ -829,7 +829,7 @@ hipError_t run_dense(const Args& a, int cus, hipStream_t s) {
   // One tile on a unit has no other's work to wait behind: a third stage, once K is long enough for
   // its longer start (2048 x 2048, K = 4096: 30.5 -> 27.6 us; 1024 x 4096, K = 2048: 15.2 -> 17.0).
   if constexpr (!F32) {
-    if (tiles(128, 128) <= cus && a.K >= 24 * ROWB)
+    if (tiles(128, 128) <= cus && a.K >= 26 * ROWB)
       return run_tile<128, 128, 2, 4, 1, 3, BROW, false>(a, s);
     return run_tile<128, 128, 2, 4, 1, 2, BROW, false>(a, s);
   }

@@ -24,10 +24,7 @@ namespace moe {
 namespace pm {
 
 constexpr int kThreads = 256;
-// Sorted rows whose padding one workgroup clears.  Fewer leave more workgroups without any (4 rows:
-// 8192 tokens, top 6 of 64, 2048 columns 53.5 -> 56.3 us), more clear it one after the other (16
-// rows: 2048 tokens, top 8 of 256, 7168 codes, half of the rows padding, 54.5 -> 58.8 us).
-constexpr int kPadRows = 8;
+constexpr int kPadRows = 8;      // sorted rows whose padding one workgroup clears, at most
 
 struct Args {
   const i32x4* x;               // permute: x; unpermute(_bwd): rows
@@ -43,6 +40,7 @@ struct Args {
   int T, K, vpr;                // tokens, slots per token, 16-byte vectors per row
   int BM, rows_max, tiles_max, groups;   // groups: scales per row (0: none)
   int64_t n_slots;
+  int pad_rows;                 // sorted rows whose padding one workgroup clears
   int token_blocks;             // blocks [0, token_blocks) walk tokens, the rest clear padding
   int blocks;                   // all of them; a launch runs at most kMaxGrid and strides
 };
@@ -52,15 +50,15 @@ struct Args {
 constexpr int kMaxGrid = 1 << 22;
 
 // Rows of valid tiles that hold no slot: zeros (and scales 1, what a row of zeros quantises
-// to).  One workgroup looks at kPadRows rows; rows past the last valid tile are left alone.
+// to).  One workgroup looks at pad_rows rows; rows past the last valid tile are left alone.
 __device__ __forceinline__ void clear_padding(const Args& g, int block) {
   const int64_t used = (int64_t)min(max(*g.num_tiles, 0), g.tiles_max) * g.BM;
-  const int64_t r0 = (int64_t)block * kPadRows;
+  const int64_t r0 = (int64_t)block * g.pad_rows;
   if (r0 >= used) return;
   int slot[kPadRows];
   #pragma unroll
   for (int i = 0; i < kPadRows; ++i)
-    slot[i] = (r0 + i < used) ? g.sorted_slots[r0 + i] : 0;
+    slot[i] = (i < g.pad_rows && r0 + i < used) ? g.sorted_slots[r0 + i] : 0;
   #pragma unroll
   for (int i = 0; i < kPadRows; ++i) {
     if ((uint32_t)slot[i] < (uint32_t)g.n_slots) continue;
@@ -269,6 +267,11 @@ Args args(const Resolved& r, int row_dtype) {
   a.tiles_max = (int)r.tiles_max;
   a.groups = r.H / kGroup;
   a.n_slots = r.N;
+  // A workgroup's rows are cleared one after the other, and one that finds none to clear costs its
+  // launch: 4 rows where every expert may leave a block and these are as many rows as the slots
+  // (2048 tokens, top 8 of 256 in blocks of 128, 7168 codes: 51.5 us, with 8 rows 54.5, with 16
+  // 58.8), else 8 (8192 tokens, top 6 of 64 in blocks of 256, 2048 columns: 53.5 us, with 4 56.3).
+  a.pad_rows = r.rows_max - r.N >= r.N ? kPadRows / 2 : kPadRows;
   return a;
 }
 
@@ -282,7 +285,9 @@ void by_type(bool bf16, bool large, F f) {
   else f(std::false_type{}, std::false_type{});
 }
 
-int pad_blocks(const Resolved& r) { return (int)((r.rows_max + kPadRows - 1) / kPadRows); }
+int pad_blocks(const Args& a) {
+  return (int)(((int64_t)a.rows_max + a.pad_rows - 1) / a.pad_rows);
+}
 
 }  // namespace pm
 
@@ -298,7 +303,7 @@ hipError_t launch_permute(const Resolved& r, int row_dtype, const void* x, const
   a.rows = (i32x4*)rows;
   a.row_scales = row_scales;
   a.token_blocks = (int)(((int64_t)r.T * a.vpr + pm::kThreads - 1) / pm::kThreads);
-  a.blocks = a.token_blocks + pm::pad_blocks(r);
+  a.blocks = a.token_blocks + pm::pad_blocks(a);
   hipLaunchKernelGGL(pm::permute_kernel, dim3((unsigned)std::min(a.blocks, pm::kMaxGrid)),
                      dim3(pm::kThreads), 0, s, a);
   return hipGetLastError();
@@ -336,7 +341,7 @@ hipError_t launch_unpermute_bwd(const Resolved& r, int row_dtype, const void* d_
   constexpr int kWaves = pm::kThreads / kWave;
   const bool few = r.N < 2048;          // fewer waves than 8 per compute unit of 256
   a.token_blocks = (int)(few ? r.N : (r.N + kWaves - 1) / kWaves);
-  a.blocks = a.token_blocks + (d_rows ? pm::pad_blocks(r) : 0);
+  a.blocks = a.token_blocks + (d_rows ? pm::pad_blocks(a) : 0);
   const dim3 grid((unsigned)std::min(a.blocks, pm::kMaxGrid)), block(pm::kThreads);
   pm::by_type(row_dtype == MOE_BF16, pm::large(r, a), [&](auto bf16, auto large) {
     if (few)

@@ -353,7 +353,7 @@ GEMM = [(1, 1, 128), (1, 7168, 2048), (3, 130, 384), (16, 576, 7168), (17, 64, 1
         (255, 513, 384), (300, 520, 2048), (513, 768, 512), (1000, 2049, 256), (2048, 1536, 1024),
         # one each at least of the tile sizes of large products (256 units), rows of c that begin
         # on any byte: 128x128 with two and three stages, 128x256, 192x256, 256x256 with halves
-        (4121, 405, 3200), (408, 8254, 2048), (905, 8233, 256), (6569, 1797, 256),
+        (4121, 405, 3456), (408, 8254, 2048), (905, 8233, 256), (6569, 1797, 256),
         (3718, 5402, 384), (401, 8258, 3200), (911, 8313, 384), (6605, 385, 128),
         (5907, 771, 128), (6176, 390, 1152)]
 
