@@ -406,7 +406,10 @@ int moe_quantize_cols_e4m3(int32_t m, int32_t n, const void* x, uint8_t* xq, flo
  * moe_gemm_e4m3 -- product of e4m3 codes with one scale per 128 values along k.
  *   c[i, j] = sum over groups g of 128 along k, ascending, of
  *             a_scales[i, g] * b_scales[., g] * ( a[i, g-group] . b[j, g-group] )
- * accumulated in fp32 and rounded once to c_dtype (MOE_F32 or MOE_BF16).
+ * accumulated in fp32 and rounded once to c_dtype (MOE_F32 or MOE_BF16).  The two scales are
+ * multiplied first, in fp32, so their product has to be a normal number.  The 128 products of a
+ * group are added in fp32 for MOE_F32; for MOE_BF16 by the fp8 matrix instructions, which drop
+ * what lies more than 13 bits below the largest of 8 products (1e-5 of a result, typically).
  * b_block says what a scale of b covers: 128: a block of 128 rows (b_scales [ceil(n/128), k/128],
  * the layout of the layer's e4m3 weights); 1: one row (b_scales [n, k/128], the layout of
  * moe_quantize_rows_e4m3 and moe_quantize_cols_e4m3).
