@@ -797,8 +797,8 @@ hipError_t run_dense(const Args& a, int cus, hipStream_t s) {
   // a round per slice (1/100 us), `half` that of a last round which fills at most half of its
   // places (two per unit for 128x128 tiles; 256x256 tiles run as halves then), `ends` the slices
   // that a round's start and end are worth; all fitted to 80 shapes of 300 to 8192 rows (rms 4-7%).
-  // The size chosen takes 0.3-0.9% more than the best one of each shape; the best single one,
-  // 128x128 (bf16) and 64x128 (fp32), 5-10%.
+  // The size chosen takes at most 1.1% more than the best one of each shape, on average; the best
+  // single one, 128x128 (bf16) and 64x128 (fp32), 5-10%.
   auto price = [&](int bm, int bn, int places, int whole, int half, int ends) {
     const int64_t n = tiles(bm, bn), per = (int64_t)cus * places, rem = n % per;
     return (n / per * whole + (rem == 0 ? 0 : rem * 2 <= per ? half : whole)) *
