@@ -402,6 +402,12 @@ def _where(stream, dev: int):
     return _stream(stream)
 
 
+def _refuse_past_int32(where: str, *sizes: int) -> None:
+    """Sizes read off a tensor, before ctypes would drop their upper bits."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise MoeError(MOE_ERR_SHAPE, where)
+
+
 def moe_permute(p: Problem, x, x_scales, slot_row, sorted_slots, num_tiles, rows, row_scales,
                 stream=None) -> None:
     dt = _row_dtype(x, "x")
@@ -465,6 +471,7 @@ def moe_quantize_cols_e4m3(x, xq, scales, stream=None) -> None:
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x: expected a matrix")
     m, n = x.shape
+    _refuse_past_int32("moe_quantize_cols_e4m3", m, n)
     groups = -(-m // 128)
     dev = _device()
     _checked(load().moe_quantize_cols_e4m3(
@@ -480,6 +487,9 @@ def moe_gemm_e4m3(a, a_scales, b, b_scales, b_block: int, c, stream=None) -> Non
         raise ValueError("b: expected a matrix")
     m, k = a.shape
     n = b.shape[0]
+    _refuse_past_int32("moe_gemm_e4m3", m, n, k)
+    if b_block != 1 and b_block != 128:           # it says how many b_scales there are
+        raise MoeError(MOE_ERR_SHAPE, "moe_gemm_e4m3")
     g = k // 128
     dev = _device()
     _checked(load().moe_gemm_e4m3(
@@ -495,6 +505,7 @@ def moe_grouped_gemm_e4m3(p: Problem, rows, row_scales, w, w_scales, sorted_slot
     if not isinstance(w, torch.Tensor) or w.dim() != 3 or w.shape[0] != p.E:
         raise ValueError("w: expected [E, n, k]")
     E, n, k = w.shape
+    _refuse_past_int32("moe_grouped_gemm_e4m3", n, k)
     rm = moe_max_padded_slots(p)
     dev = _device()
     _checked(load().moe_grouped_gemm_e4m3(
