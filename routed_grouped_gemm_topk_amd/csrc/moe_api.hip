@@ -95,8 +95,8 @@ Resolved resolve(const moe_problem* p) {
 
 // Sizes of moe_gemm_e4m3 and moe_grouped_gemm_e4m3.  k up to 2^22 keeps a tile's 256 operand rows
 // within the 31-bit offsets of one buffer descriptor.  A launch counts its threads in 32 bits:
-// 2^29 tiles of 16x16 are 2^22 of 128x256 (512 threads each, the smallest that a large dense
-// product runs on), and a grouped launch has at most one workgroup of 512 threads per 128 columns
+// 2^29 tiles of 16x16 are little more than 2^22 of 128x256 (512 threads each; choose_dense passes
+// over the smaller ones where these would be too many), and a grouped launch has at most one workgroup of 512 threads per 128 columns
 // of an m-block, rounded up to a multiple of 256 workgroups.
 constexpr int kGemmMaxK = 1 << 22, kGemmMaxDim = 1 << 24, kQuantMaxDim = 1 << 22;
 constexpr int64_t kMaxGemmTiles = 1LL << 29;   // of 16x16

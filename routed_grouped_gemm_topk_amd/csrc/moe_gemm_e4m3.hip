@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "moe_gemm_e4m3_choice.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -20,7 +21,6 @@ namespace moe {
 namespace q8 {
 
 constexpr int ROWB = 128;      // bytes per row per k-slice: one scale group
-constexpr int kChunk = 32;     // logical tiles per chunk dealt to one XCD (xcd_chunked)
 constexpr int kGroupM = 8;     // m-blocks that sweep the n-blocks together
 
 struct Args {
@@ -724,8 +724,17 @@ __global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void grouped_kernel(Args
   G::template run<true, false, PAST>(g, t, lds);
 }
 
+// The dense kernels of these tiles, as moe_gemm_e4m3_choice.h knows them.
+template <int BM, int BN, int THREADS>
+constexpr bool listed() {
+  for (const DenseSize& d : kDenseSize)
+    if (d.bm == BM && d.bn == BN && d.threads == THREADS) return true;
+  return false;
+}
+
 template <int BM, int BN, int WM, int WN, int KG, int NS, bool BROW, bool F32>
 hipError_t run_tile(const Args& a, hipStream_t s) {
+  static_assert(listed<BM, BN, WM * WN * KG * kWave>(), "the choice counts these tiles and threads");
   const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
   hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, KG, NS, BROW, F32>),
                      dim3((unsigned)xcd_chunked_grid<kChunk>(tiles)), dim3(WM * WN * KG * kWave), 0,
@@ -735,6 +744,7 @@ hipError_t run_tile(const Args& a, hipStream_t s) {
 
 template <int FM, int FN, int NW, int U, bool BROW, bool F32>
 hipError_t run_stream(const Args& a, hipStream_t s) {
+  static_assert(listed<16 * FM, 16 * FN, NW * kWave>(), "the choice counts these tiles and threads");
   const int64_t tiles = (((int64_t)a.M + 16 * FM - 1) / (16 * FM)) *
                         (((int64_t)a.N + 16 * FN - 1) / (16 * FN));
   hipLaunchKernelGGL((stream_kernel<FM, FN, NW, U, BROW, F32>), dim3((unsigned)tiles),
@@ -766,73 +776,29 @@ hipError_t run_large(const Args& a, int cus, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Which kernel, for few tiles: the largest one whose tiles still are at most as many as the compute
-// units, since a product that leaves units idle takes the time of one tile, and a small tile's time
-// is that of its steps along K.  Measured with K of 512, 2048 and 7168, M and N from 1 to 7168
-// (us, K = 2048; the tile chosen against the next larger and smaller ones):
-//   M = 1,    N = 7168: 16-row stream 4.9-5.1, 16x64 5.7
-//   M = 64,   N = 2048: 16x64 5.9,  32x64 6.5
-//   M = 64,   N = 7168: 32x64 6.4,  16x64 8.3,  64x64 8.2
-//   M = 128,  N = 7168: 64x64 8.1,  32x64 9.3,  64x128 10.9
-//   M = 256,  N = 7168: 64x128 10.7, 64x64 14.4, 128x128 15.2
 template <bool BROW, bool F32>
 hipError_t run_dense(const Args& a, int cus, hipStream_t s) {
-  auto tiles = [&](int bm, int bn) {
-    return ((int64_t)a.M + bm - 1) / bm * (((int64_t)a.N + bn - 1) / bn);
-  };
-  if (a.M <= 16) {
-    // two fragments of b per workgroup once that still fills the units (7168 x 7168: 11.1 against
-    // 11.7; 4096 x 7168, which it does not fill: 10.3 against 7.4)
-    if (tiles(16, 32) * 8 >= cus * 7) return run_stream<1, 2, 8, 2, BROW, F32>(a, s);
-    return run_stream<1, 1, 8, 2, BROW, F32>(a, s);
+  switch (choose_dense(a.M, a.N, a.K, BROW, F32, cus)) {
+    case kStream16x16: return run_stream<1, 1, 8, 2, BROW, F32>(a, s);
+    case kStream16x32: return run_stream<1, 2, 8, 2, BROW, F32>(a, s);
+    case kTile16x64: return run_tile<16, 64, 1, 2, 4, 3, BROW, F32>(a, s);
+    case kTile32x64: return run_tile<32, 64, 1, 4, 2, 3, BROW, F32>(a, s);
+    case kTile64x64: return run_tile<64, 64, 2, 2, 2, 3, BROW, F32>(a, s);
+    case kTile64x128: return run_tile<64, 128, 2, 4, 1, 3, BROW, F32>(a, s);
+    case kTile128x128: return run_tile<128, 128, 2, 4, 1, 2, BROW, F32>(a, s);
+    case kTile128x256: return run_tile<128, 256, 2, 4, 1, BROW || F32 ? 2 : 3, BROW, F32>(a, s);
+    case kTile128x128Ring3:
+      if constexpr (!F32) return run_tile<128, 128, 2, 4, 1, 3, BROW, false>(a, s);
+      break;
+    case kTile192x256:
+      if constexpr (!F32) return run_tile<192, 256, 2, 4, 1, 2, BROW, false>(a, s);
+      break;
+    case kLarge256x256:
+      if constexpr (!F32 && !BROW) return run_large(a, cus, s);
+      break;
+    case kDenseKernels: break;
   }
-  if (tiles(16, 64) <= cus) return run_tile<16, 64, 1, 2, 4, 3, BROW, F32>(a, s);
-  if (tiles(32, 64) <= cus) return run_tile<32, 64, 1, 4, 2, 3, BROW, F32>(a, s);
-  if (tiles(64, 64) <= cus) return run_tile<64, 64, 2, 2, 2, 3, BROW, F32>(a, s);
-  // two to a unit, before larger ones that leave units idle (92 x 9544, K = 4096: to bf16 15.0
-  // against 17.0 us with 64x128, to fp32 18.9 against 25.5)
-  if (tiles(32, 64) <= 2 * cus) return run_tile<32, 64, 1, 4, 2, 3, BROW, F32>(a, s);
-  if (tiles(64, 128) <= cus) return run_tile<64, 128, 2, 4, 1, 3, BROW, F32>(a, s);
-  // More tiles than that: the size whose rounds over the units take least.  `whole` is the time of
-  // a round per slice (1/100 us), `half` that of a last round which fills at most half of its
-  // places (two per unit for 128x128 tiles; 256x256 tiles run as halves then), `ends` the slices
-  // that a round's start and end are worth; all fitted to 80 shapes of 300 to 8192 rows (rms 4-7%).
-  // The size chosen takes at most 1.1% more than the best one of each shape, on average; the best
-  // single one, 128x128 (bf16) and 64x128 (fp32), 5-10%.
-  auto price = [&](int bm, int bn, int places, int whole, int half, int ends) {
-    const int64_t n = tiles(bm, bn), per = (int64_t)cus * places, rem = n % per;
-    return (n / per * whole + (rem == 0 ? 0 : rem * 2 <= per ? half : whole)) *
-           (a.K / ROWB + ends);
-  };
-  if constexpr (F32) {
-    // the bf16 multiplication does not fit larger tiles in registers
-    const int64_t p64 = BROW ? price(64, 128, 1, 73, 61, 2) : price(64, 128, 1, 62, 51, 3);
-    const int64_t p128 = BROW ? price(128, 128, 2, 258, 132, 3) : price(128, 128, 2, 230, 117, 3);
-    const int64_t p256 = BROW ? price(128, 256, 1, 201, 201, 3) : price(128, 256, 1, 185, 185, 3);
-    if (p64 < std::min(p128, p256)) return run_tile<64, 128, 2, 4, 1, 3, BROW, true>(a, s);
-    if (p256 < p128) return run_tile<128, 256, 2, 4, 1, 2, BROW, true>(a, s);
-    return run_tile<128, 128, 2, 4, 1, 2, BROW, true>(a, s);
-  } else {
-    const int64_t p128 = BROW ? price(128, 128, 2, 140, 86, 2) : price(128, 128, 2, 114, 72, 3);
-    const int64_t p256 = BROW ? price(128, 256, 1, 130, 130, 4) : price(128, 256, 1, 99, 99, 5);
-    const int64_t p192 = BROW ? price(192, 256, 1, 159, 159, 4) : price(192, 256, 1, 128, 128, 5);
-    const int64_t least = std::min({p128, p256, p192});
-    // scales per row of b do not fit 256x256 tiles in registers (2.8 us per slice)
-    if constexpr (!BROW) {
-      if (price(256, 256, 1, 153, 99, 5) < least) return run_large(a, cus, s);
-    }
-    if (p128 > least) {
-      if (p192 < p256) return run_tile<192, 256, 2, 4, 1, 2, BROW, false>(a, s);
-      return run_tile<128, 256, 2, 4, 1, BROW ? 2 : 3, BROW, false>(a, s);
-    }
-  }
-  // One tile on a unit has no other's work to wait behind: a third stage, once K is long enough for
-  // its longer start (2048 x 2048, K = 4096: 30.5 -> 27.6 us; 1024 x 4096, K = 2048: 15.2 -> 17.0).
-  if constexpr (!F32) {
-    if (tiles(128, 128) <= cus && a.K >= 26 * ROWB)
-      return run_tile<128, 128, 2, 4, 1, 3, BROW, false>(a, s);
-    return run_tile<128, 128, 2, 4, 1, 2, BROW, false>(a, s);
-  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace q8

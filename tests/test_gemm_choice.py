@@ -1,0 +1,70 @@
+"""The choice of a dense e4m3 product's kernel (csrc/moe_gemm_e4m3_choice.h), compiled by itself for
+the host."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+import routed_grouped_gemm_topk_amd as moe
+
+CSRC = os.path.join(os.path.dirname(moe.__file__), "csrc")
+KERNELS = ["16x16 stream", "16x32 stream", "16x64", "32x64", "64x64", "64x128", "128x128",
+           "128x128 ring of 3", "128x256", "192x256", "256x256"]
+VARIANTS = [(brow, f32) for brow in (False, True) for f32 in (False, True)]
+SHIM = """
+#include "moe_gemm_e4m3_choice.h"
+using namespace moe::q8;
+extern "C" int kernels() { return kDenseKernels; }
+extern "C" int choose(int m, int n, int k, bool brow, bool f32, int cus) {
+  return choose_dense(m, n, k, brow, f32, cus);
+}
+extern "C" int64_t tiles(int kernel, int m, int n) { return dense_tiles((DenseKernel)kernel, m, n); }
+extern "C" int threads(int kernel) { return kDenseSize[kernel].threads; }
+"""
+
+
+@pytest.fixture(scope="module")
+def choice(tmp_path_factory):
+    d = tmp_path_factory.mktemp("choice")
+    src, out = d / "shim.cpp", d / "shim.so"
+    src.write_text(SHIM)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC,
+                    "-o", str(out), str(src)], check=True)
+    lib = ctypes.CDLL(str(out))
+    lib.choose.argtypes = [ctypes.c_int] * 3 + [ctypes.c_bool] * 2 + [ctypes.c_int]
+    lib.tiles.restype = ctypes.c_int64
+    assert lib.kernels() == len(KERNELS)
+    return lib
+
+
+def accepted(m, n, k):
+    """Whether the library takes these sizes (it looks at them before the output's type, which is
+    wrong here, so that no call goes through)."""
+    ok = ctypes.c_void_p(4096)
+    status = moe.load().moe_gemm_e4m3(m, n, k, ok, ok, ok, ok, 128, ok, 99, None)
+    assert status in (moe.MOE_ERR_SHAPE, moe.MOE_ERR_DTYPE)
+    return status == moe.MOE_ERR_DTYPE
+
+
+# the largest products that are accepted, square and narrow, of any K
+LARGEST = [(2 ** 24, 8192), (8192, 2 ** 24), (2 ** 22, 2 ** 15), (2 ** 18, 2 ** 19),
+           (2 ** 24 - 7, 8191), (18334, 7475545), (2423788, 56589), (2 ** 24, 17), (17, 2 ** 24),
+           (1, 2 ** 24), (2 ** 24, 1), (65, 2 ** 24), (193, 2 ** 24)]
+
+
+@pytest.mark.parametrize("k", [128, 256, 384, 512, 4096, 2 ** 22])
+@pytest.mark.parametrize("m,n", LARGEST)
+def test_launches_count_their_threads_in_32_bits(choice, m, n, k):
+    assert accepted(m, n, k)
+    for cus in (8, 64, 256, 304):
+        for brow, f32 in VARIANTS:
+            kernel = choice.choose(m, n, k, brow, f32, cus)
+            # rounded up to whole chunks of 32 tiles for each of 8 XCDs
+            groups = -(-choice.tiles(kernel, m, n) // 256) * 256
+            assert groups * choice.threads(kernel) < 2 ** 32, (KERNELS[kernel], brow, f32, cus)
+
+
+def test_just_past_the_largest_is_refused():
+    for m, n in [(2 ** 24, 8193), (2 ** 18 + 1, 2 ** 19), (2 ** 24 + 1, 1)]:
+        assert not accepted(m, n, 128)
