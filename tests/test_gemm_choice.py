@@ -68,3 +68,31 @@ def test_launches_count_their_threads_in_32_bits(choice, m, n, k):
 def test_just_past_the_largest_is_refused():
     for m, n in [(2 ** 24, 8193), (2 ** 18 + 1, 2 ** 19), (2 ** 24 + 1, 1)]:
         assert not accepted(m, n, 128)
+
+
+def test_every_kernel_is_run_by_the_gpu_tests(choice):
+    """The shapes of test_gpu_gemm_tiles reach every kernel that the choice can give, in each form:
+    scales of b by block and by row, both result types, rows of c on 16 bytes, on an even and on an
+    odd number of values; with ragged tiles, a number of slices that is no multiple of the groups of
+    waves along k, and more steps than stages, so that every stage is filled again."""
+    from test_gpu_gemm_tiles import TILES, UNITS
+    bm = [16, 16, 16, 32, 64, 64, 128, 128, 128, 192, 256]
+    bn = [16, 32, 64, 64, 64, 128, 128, 128, 256, 256, 256]
+    groups = [8, 8, 4, 2, 2, 1, 1, 1, 1, 1, 1]             # of waves that cut k
+    stages = [2, 2, 3, 3, 3, 3, 2, 3, 3, 2, 2]             # streams: slices in flight, 2 a step
+    only_bf16, only_blocks = {7, 9, 10}, {10}
+    hit = set()
+    for m, n, k in TILES:
+        for brow, f32 in VARIANTS:
+            q = choice.choose(m, n, k, brow, f32, UNITS)
+            slices = k // 128
+            ragged = q < 2 or (m % bm[q] and n % bn[q])
+            if ragged and -(-slices // groups[q]) > stages[q] + 1 and (
+                    groups[q] == 1 or slices % groups[q]):
+                hit.add((q, brow, f32, "odd" if n % 2 else "16 bytes" if n % 8 == 0 else "even"))
+    for q, name in enumerate(KERNELS):
+        for brow, f32 in VARIANTS:
+            if (f32 and q in only_bf16) or (brow and q in only_blocks):
+                continue
+            for rows in ("odd", "16 bytes", "even"):
+                assert (q, brow, f32, rows) in hit, (name, brow, f32, rows)
