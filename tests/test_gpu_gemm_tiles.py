@@ -5,6 +5,19 @@ block and by row, results in bf16 and fp32, rows of c that begin on 16 bytes, on
 number of values), with ragged last tiles and so many slices of k that every ring of stages is refilled
 (test_gemm_choice.py holds it to that).  Grouped: one case at least per kernel of
 launch_grouped_gemm_e4m3, with experts of one m-block and of several.
+
+Tolerances: gemm_tol bounds every element from the sum of magnitudes.  Random operands stay far below
+it, so two statements about them are held as well.  fp32 results: gemm_norm, 2^-21.  bf16 results: the
+error of the product BEFORE its rounding, which `beyond_rounding` reads off the rounded one.  With
+r = bf16(ref), v = ref + d the computed sum and got = bf16(v): |got - ref| <= |got - v| + |d| <=
+|r - v| + |d| <= |r - ref| + 2 |d|, so the excess |got - ref| - |r - ref| of an element is between 0 and
+2 |d|.  An element is rounded the other way where its distance m to a rounding border is below |d|; ref
+lies anywhere in a step s, so that happens with probability |d| / s, m is uniform up to |d| and the
+excess is 2 m: the excess times s has the mean d^2.  The fp8 instruction's d is 2^-16 of a result in the
+root mean square (1.4e-5, measured on fp32 results of the same sums), by the row's and the column's
+products a normal variable of many terms.  Held: 16 of its standard deviations, 2^-12 of
+sqrt(sum of the squared products), for every element; 2^-15 in the root mean square where at least 50000
+elements (some 150 of them rounded the other way, so the estimate of d^2 is good to 10%) tell it.
 """
 import pytest
 import torch
@@ -26,6 +39,27 @@ TILES = [(13, 56, 4224), (16, 60, 4224), (5, 61, 4224), (19, 56, 2176), (17, 63,
          (5818, 2062, 512), (2576, 4728, 512)]
 
 
+def squares(a, sa, b, sb, b_block):
+    """sqrt(sum of the squared products) of every element."""
+    sbr = sb if b_block == 1 else sb.repeat_interleave(128, 0)[: b.shape[0]]
+    a64 = a.view(torch.float8_e4m3fn).double() * sa.double().repeat_interleave(128, 1)
+    b64 = b.view(torch.float8_e4m3fn).double() * sbr.double().repeat_interleave(128, 1)
+    return ((a64 * a64) @ (b64 * b64).t()).sqrt()
+
+
+def beyond_rounding(got, ref, scale):
+    """Holds the error of a bf16 result before its rounding (see above); returns its estimate."""
+    near = ref.bfloat16().double()            # through fp32: off by 2^-24 of ref at most
+    excess = (got.double() - ref).abs() - (near - ref).abs()
+    worst = (excess - 2 * 2.0 ** -12 * scale - 2 * 2.0 ** -24 * ref.abs()).max()
+    assert float(worst) <= 0.0, f"{float(worst):.3e} beyond the product's own error"
+    step = torch.exp2(torch.floor(torch.log2(ref.abs().clamp(min=1e-30))) - 7)
+    rms = float(((excess * step).sum().clamp(min=0.0) / (ref * ref).sum()).sqrt())
+    if ref.numel() >= 50000:
+        assert rms <= 2.0 ** -15, rms
+    return rms
+
+
 @pytest.mark.parametrize("b_block", [128, 1])
 @pytest.mark.parametrize("c", TILES, ids=str)
 def test_dense(device, c, b_block):
@@ -39,7 +73,21 @@ def test_dense(device, c, b_block):
         torch.cuda.synchronize()
         assert c_.intact(), dtype
         close(c_.t, ref, gemm_tol(ref, mag, k, dtype), dtype)
-        gemm_norm(c_.t, ref, dtype)
+        if dtype == "f32":
+            gemm_norm(c_.t, ref, dtype)
+        else:
+            say("before rounding", beyond_rounding(c_.t, ref, squares(a, sa, b, sb, b_block)))
+
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("m,n,k", [(1, 50000, 7168), (16, 8192, 2048), (700, 2880, 4096)])
+def test_dense_before_rounding(device, m, n, k, seed):
+    """The same for more operands, one row among them."""
+    a, sa, b, sb = operands(device, m, n, k, 128, 81 + seed)
+    ref, _ = product(a, sa, b, sb, 128)
+    got = moe.gemm_e4m3(a, sa, b, sb)
+    torch.cuda.synchronize()
+    say("before rounding", (m, n, k), beyond_rounding(got, ref, squares(a, sa, b, sb, 128)))
 
 
 # (T, E, k, block_m, n, kk)
@@ -72,9 +120,13 @@ def grouped(device, T, E, k, bm, n, kk, dtype, sample):
             mine = mine[torch.linspace(0, mine.numel() - 1, sample, device=device).long()]
         if not mine.numel():
             continue
-        ref, mag = product(rows.view(torch.uint8)[mine], rs[mine], w[e], ws[e], 128)
+        args = rows.view(torch.uint8)[mine], rs[mine], w[e], ws[e], 128
+        ref, mag = product(*args)
         close(out.t[mine], ref, gemm_tol(ref, mag, kk, dtype), f"expert {e}")
-        gemm_norm(out.t[mine], ref, dtype)
+        if dtype == "f32":
+            gemm_norm(out.t[mine], ref, dtype)
+        else:
+            beyond_rounding(out.t[mine], ref, squares(*args))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
