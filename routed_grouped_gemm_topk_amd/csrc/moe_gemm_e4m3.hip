@@ -827,34 +827,24 @@ hipError_t launch_grouped_gemm_e4m3(const Resolved& r, int N, int K, const uint8
   g.tiles_max = (int)r.tiles_max;
   g.n_slots = (int)r.N;
   g.M = (int)r.rows_max; g.N = N; g.K = K;
-  // Stores past the last-level cache (256 MB) for an output that does not fit it (slots of 256
-  // experts to 7168 columns: 16384 in 128-row blocks 851 -> 814 us, 8192 in 64-row blocks 783 ->
-  // 704 us); a smaller output stays in reach of whoever reads it next.
-  const bool past = r.rows_max * N * (out_f32 ? 4 : 2) > (256LL << 20);
-  // 256 columns a tile while its last n-block wastes little (N = 7168: 857 us against 882 with 128;
-  // N = 2880, 7% past the end: 788 against 807; N = 1408, 9%: 152 against 128).
-  const bool wide = ((int64_t)N + 255) / 256 * 256 * 100 <= (int64_t)N * 108;
-  // Few tiles: the k-groups of the dense product (run_dense).
   const int cus = std::max(device_cu_count(), 8);
-  const bool few = r.tiles_max * ((N + 63) / 64) <= cus;
-  switch (r.BM) {
-    case 16:
-      if (few) return q8::run_grouped<16, 64, 1, 2, 4, 3>(g, out_f32, s);
-      return q8::run_grouped<16, 128, 1, 4, 1, 3>(g, out_f32, s);
-    case 32:
-      if (few) return q8::run_grouped<32, 64, 1, 4, 2, 3>(g, out_f32, s);
-      return q8::run_grouped<32, 128, 1, 4, 1, 3>(g, out_f32, s);
-    case 64:
-      if (few) return q8::run_grouped<64, 64, 2, 2, 2, 3>(g, out_f32, s);
-      if (wide && past) return q8::run_grouped<64, 256, 2, 4, 1, 3, 2, true>(g, out_f32, s);
-      if (wide) return q8::run_grouped<64, 256, 2, 4, 1, 3>(g, out_f32, s);
-      return q8::run_grouped<64, 128, 2, 4, 1, 3>(g, out_f32, s);
-    case 128:
-      if (wide && past) return q8::run_grouped<128, 256, 2, 4, 1, 3, 2, true>(g, out_f32, s);
-      if (wide) return q8::run_grouped<128, 256, 2, 4, 1, 3>(g, out_f32, s);
-      return q8::run_grouped<128, 128, 2, 4, 1, 2, 4>(g, out_f32, s);
-    default: return hipErrorInvalidValue;
+  switch (q8::choose_grouped(r.BM, r.rows_max, r.tiles_max, N, out_f32, cus)) {
+    case q8::kGrouped16x64: return q8::run_grouped<16, 64, 1, 2, 4, 3>(g, out_f32, s);
+    case q8::kGrouped16x128: return q8::run_grouped<16, 128, 1, 4, 1, 3>(g, out_f32, s);
+    case q8::kGrouped32x64: return q8::run_grouped<32, 64, 1, 4, 2, 3>(g, out_f32, s);
+    case q8::kGrouped32x128: return q8::run_grouped<32, 128, 1, 4, 1, 3>(g, out_f32, s);
+    case q8::kGrouped64x64: return q8::run_grouped<64, 64, 2, 2, 2, 3>(g, out_f32, s);
+    case q8::kGrouped64x128: return q8::run_grouped<64, 128, 2, 4, 1, 3>(g, out_f32, s);
+    case q8::kGrouped64x256: return q8::run_grouped<64, 256, 2, 4, 1, 3>(g, out_f32, s);
+    case q8::kGrouped64x256Past:
+      return q8::run_grouped<64, 256, 2, 4, 1, 3, 2, true>(g, out_f32, s);
+    case q8::kGrouped128x128: return q8::run_grouped<128, 128, 2, 4, 1, 2, 4>(g, out_f32, s);
+    case q8::kGrouped128x256: return q8::run_grouped<128, 256, 2, 4, 1, 3>(g, out_f32, s);
+    case q8::kGrouped128x256Past:
+      return q8::run_grouped<128, 256, 2, 4, 1, 3, 2, true>(g, out_f32, s);
+    case q8::kGroupedKernels: break;
   }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace moe

@@ -1,5 +1,5 @@
-// Which kernel a dense product of e4m3 codes runs on, from its sizes and the device's number of
-// compute units alone.  Host code without HIP, so that it is compiled and tested by itself.
+// Which kernel a product of e4m3 codes runs on, from its sizes and the device's number of compute
+// units alone.  Host code without HIP, so that it is compiled and tested by itself.
 #pragma once
 
 #include <stdint.h>
@@ -95,6 +95,34 @@ inline DenseKernel choose_dense(int M, int N, int K, bool brow, bool f32, int cu
   // One tile on a unit has no other's work to wait behind: a third stage, once K is long enough for
   // its longer start (2048 x 2048, K = 4096: 30.5 -> 27.6 us; 1024 x 4096, K = 2048: 15.2 -> 17.0).
   return tiles(kTile128x128) <= cus && K >= 26 * kSlice ? kTile128x128Ring3 : kTile128x128;
+}
+
+enum GroupedKernel {            // rows of an m-block, columns of a tile
+  kGrouped16x64, kGrouped16x128, kGrouped32x64, kGrouped32x128, kGrouped64x64, kGrouped64x128,
+  kGrouped64x256, kGrouped64x256Past, kGrouped128x128, kGrouped128x256, kGrouped128x256Past,
+  kGroupedKernels               // none: m-blocks of other sizes
+};
+
+inline GroupedKernel choose_grouped(int block_m, int64_t rows_max, int64_t tiles_max, int N,
+                                    bool f32, int cus) {
+  // Stores past the last-level cache (256 MB) for an output that does not fit it (slots of 256
+  // experts to 7168 columns: 16384 in 128-row blocks 851 -> 814 us, 8192 in 64-row blocks 783 ->
+  // 704 us); a smaller output stays in reach of whoever reads it next.
+  const bool past = rows_max * N * (f32 ? 4 : 2) > (256LL << 20);
+  // 256 columns a tile while its last n-block wastes little (N = 7168: 857 us against 882 with 128;
+  // N = 2880, 7% past the end: 788 against 807; N = 1408, 9%: 152 against 128).
+  const bool wide = ((int64_t)N + 255) / 256 * 256 * 100 <= (int64_t)N * 108;
+  // Few tiles: the k-groups of the dense product.
+  const bool few = tiles_max * ((N + 63) / 64) <= cus;
+  switch (block_m) {
+    case 16: return few ? kGrouped16x64 : kGrouped16x128;
+    case 32: return few ? kGrouped32x64 : kGrouped32x128;
+    case 64:
+      if (few) return kGrouped64x64;
+      return !wide ? kGrouped64x128 : past ? kGrouped64x256Past : kGrouped64x256;
+    case 128: return !wide ? kGrouped128x128 : past ? kGrouped128x256Past : kGrouped128x256;
+    default: return kGroupedKernels;
+  }
 }
 
 }  // namespace q8

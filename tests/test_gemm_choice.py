@@ -1,5 +1,5 @@
-"""The choice of a dense e4m3 product's kernel (csrc/moe_gemm_e4m3_choice.h), compiled by itself for
-the host."""
+"""The choice of an e4m3 product's kernel (csrc/moe_gemm_e4m3_choice.h), compiled by itself for the
+host."""
 import ctypes
 import os
 import subprocess
@@ -21,6 +21,10 @@ extern "C" int choose(int m, int n, int k, bool brow, bool f32, int cus) {
 }
 extern "C" int64_t tiles(int kernel, int m, int n) { return dense_tiles((DenseKernel)kernel, m, n); }
 extern "C" int threads(int kernel) { return kDenseSize[kernel].threads; }
+extern "C" int grouped_kernels() { return kGroupedKernels; }
+extern "C" int choose_grouped_(int bm, int64_t rows, int64_t tiles, int n, bool f32, int cus) {
+  return choose_grouped(bm, rows, tiles, n, f32, cus);
+}
 """
 
 
@@ -34,6 +38,8 @@ def choice(tmp_path_factory):
     lib = ctypes.CDLL(str(out))
     lib.choose.argtypes = [ctypes.c_int] * 3 + [ctypes.c_bool] * 2 + [ctypes.c_int]
     lib.tiles.restype = ctypes.c_int64
+    lib.choose_grouped_.argtypes = [ctypes.c_int] + [ctypes.c_int64] * 2 + [ctypes.c_int, ctypes.c_bool,
+                                                                           ctypes.c_int]
     assert lib.kernels() == len(KERNELS)
     return lib
 
@@ -96,3 +102,25 @@ def test_every_kernel_is_run_by_the_gpu_tests(choice):
                 continue
             for rows in ("odd", "16 bytes", "even"):
                 assert (q, brow, f32, rows) in hit, (name, brow, f32, rows)
+
+
+def test_every_grouped_kernel_is_run_by_the_gpu_tests(choice):
+    """The same for the grouped product, each kernel with both result types, more steps than stages
+    and ragged columns."""
+    import test_gpu_gemm_tiles as small
+    import test_gpu_large_outputs as large
+    names = ["16x64", "16x128", "32x64", "32x128", "64x64", "64x128", "64x256", "64x256 past",
+             "128x128", "128x256", "128x256 past"]
+    bn = [64, 128, 64, 128, 64, 128, 256, 256, 128, 256, 256]
+    groups = [4, 1, 2, 1, 2, 1, 1, 1, 1, 1, 1]
+    stages = [3, 3, 3, 3, 3, 3, 3, 3, 2, 3, 3]
+    assert choice.grouped_kernels() == len(names)
+    hit = set()
+    for T, E, k, bm, n, kk in small.GROUPED + large.PAST:
+        p = moe.make_problem(T, 128, 128, E, k, "bf16", "e4m3", bm)
+        for f32 in (False, True):
+            q = choice.choose_grouped_(bm, moe.moe_max_padded_slots(p), moe.moe_max_tiles(p), n, f32,
+                                      small.UNITS)
+            if n % bn[q] and -(-(kk // 128) // groups[q]) > stages[q] + 1:
+                hit.add((names[q], f32))
+    assert hit == {(name, f32) for name in names for f32 in (False, True)}
