@@ -421,7 +421,8 @@ int moe_quantize_cols_e4m3(int32_t m, int32_t n, const void* x, uint8_t* xq, flo
  * ceil(m/16) * ceil(n/16) <= 2^29 (MOE_ERR_SHAPE otherwise).
  * In:  a uint8 [m, k] (e4m3 codes), a_scales fp32 [m, k/128]; b uint8 [n, k], b_scales
  * Out: c c_dtype [m, n]
- * Deterministic: the order of the additions depends on the sizes alone.
+ * Deterministic on one device: the order of the additions depends on the sizes and on the
+ * device's number of compute units, which choose the kernel, and on nothing else.
  */
 int moe_gemm_e4m3(int32_t m, int32_t n, int32_t k, const uint8_t* a, const float* a_scales,
                   const uint8_t* b, const float* b_scales, int32_t b_block, void* c,
@@ -445,6 +446,7 @@ int moe_gemm_e4m3(int32_t m, int32_t n, int32_t k, const uint8_t* a, const float
  * Out: out out_dtype (MOE_F32 or MOE_BF16) [moe_max_padded_slots, n]: every row of a valid tile
  *      is written, those that hold no slot as zeros, whatever `rows` has there; rows past the
  *      last valid tile are left untouched.
+ * Deterministic as moe_gemm_e4m3 is.
  */
 int moe_grouped_gemm_e4m3(const moe_problem* p, int32_t n, int32_t k, const uint8_t* rows,
                           const float* row_scales, const uint8_t* w, const float* w_scales,
