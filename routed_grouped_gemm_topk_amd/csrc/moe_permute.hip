@@ -268,10 +268,14 @@ Args args(const Resolved& r, int row_dtype) {
   a.groups = r.H / kGroup;
   a.n_slots = r.N;
   // A workgroup's rows are cleared one after the other, and one that finds none to clear costs its
-  // launch: 4 rows where every expert may leave a block and these are as many rows as the slots
-  // (2048 tokens, top 8 of 256 in blocks of 128, 7168 codes: 51.5 us, with 8 rows 54.5, with 16
-  // 58.8), else 8 (8192 tokens, top 6 of 64 in blocks of 256, 2048 columns: 53.5 us, with 4 56.3).
-  a.pad_rows = r.rows_max - r.N >= r.N ? kPadRows / 2 : kPadRows;
+  // launch.  8 rows, but 4 where the padding may be as many rows as the slots and a row takes a
+  // workgroup more than one store.  Top 8 of 256 in blocks of 128, 4 rows against 8: 7168 codes 53.1
+  // against 55.0 us (2048 tokens), 53.1 against 57.6 (1500), 51.1 against 53.1 (1024), 2048 fp32
+  // columns 50.9 against 54.6 (1024 tokens); with rows of one store 32.0 against 28.1 (2048 tokens,
+  // 2048 bf16 columns; 26.3 against 27.8 at 512), with less padding 59.4 against 57.8 (3000 tokens,
+  // 4096 bf16 columns).
+  const bool much = r.rows_max - r.N >= r.N && a.vpr > kThreads;
+  a.pad_rows = much ? kPadRows / 2 : kPadRows;
   return a;
 }
 
