@@ -26,7 +26,8 @@
  *                          expert, a dense projection, their gradients)
  *   moe_grouped_gemm_e4m3  the same over expert-sorted rows
  *   moe_quantize_cols_e4m3 transposed quantisation, the operands of a weight gradient
- * The outputs of these must not overlap their inputs.
+ * The outputs of these must not overlap their inputs.  There is no gradient of the experts' own
+ * weights: moe_quantize_cols_e4m3 and moe_gemm_e4m3 give it for one expert's rows at a time.
  *
  * Conventions shared by every entry point
  *   - Pointers named as tensors are DEVICE pointers owned by the caller; the

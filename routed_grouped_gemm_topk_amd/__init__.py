@@ -3,7 +3,9 @@
 The computation lives in libmoe.so (hand-written HIP kernels behind the C ABI of
 include/moe.h).  This package is its Python binding: ``_lib`` mirrors the C
 entry points one to one; the helpers below only allocate buffers with torch
-and call them.
+and call them.  Nothing here records for automatic differentiation: results have
+no graph, also where an input requires a gradient; unpermute_bwd, route_bwd and
+the products of the gradients (moe_gemm_e4m3 in moe.h) are the caller's to run.
 """
 from __future__ import annotations
 

@@ -651,8 +651,10 @@ __global__ __launch_bounds__(WM * WN * KG * kWave) void tile_kernel(Args g) {
   G::template run<false>(g, dense_tile<BM, BN>(g, logical), lds);
 }
 
-// Large products (4096 x 14336 x 4096 in 231 us, 2.08 PFLOP/s, held back by the power limit: 1.4 to
-// 1.8 GHz of 2.4; the library's product with one scale per tensor takes 214 us): 256x256 tiles in
+// Large products (4096 x 14336 x 4096 in 218-232 us, 2.2-2.07 PFLOP/s; the library's product with
+// one scale per tensor takes 214): a tile of 32 slices takes 101500 cycles, 65% of them matrix work,
+// and the clock is held at 1.8-1.9 GHz while it runs (all codes 0: the same cycles at 2.38 GHz, 177
+// us).  5 of the 256 registers spill, 24 bytes a lane.  256x256 tiles in
 // rounds of one workgroup per compute unit, `full` of them whole; where the last round would fill
 // at most half of the units, its tiles run as two halves of 128 x 256 each, so that the round takes
 // about half as long.  Every element's sum is the same either way.
