@@ -104,6 +104,17 @@ def test_every_kernel_is_run_by_the_gpu_tests(choice):
                 assert (q, brow, f32, rows) in hit, (name, brow, f32, rows)
 
 
+def test_the_halves_of_a_last_round_are_run_by_the_gpu_tests(choice):
+    from test_gpu_gemm_tiles import HALVES, UNITS
+    second = set()
+    for m, n, k in HALVES:
+        assert choice.choose(m, n, k, False, False, UNITS) == KERNELS.index("256x256")
+        tiles = choice.tiles(KERNELS.index("256x256"), m, n)
+        assert tiles > UNITS and 0 < tiles % UNITS <= UNITS // 2      # run_large's rule
+        second.add(m % 256 > 128)
+    assert second == {False, True}
+
+
 def test_every_grouped_kernel_is_run_by_the_gpu_tests(choice):
     """The same for the grouped product, each kernel with both result types, more steps than stages
     and ragged columns."""

@@ -37,6 +37,8 @@ TILES = [(13, 56, 4224), (16, 60, 4224), (5, 61, 4224), (19, 56, 2176), (17, 63,
          (5208, 930, 3200), (5506, 270, 3328), (5528, 264, 3456), (5812, 267, 3328),
          (1417, 5448, 512), (1677, 4649, 512), (1059, 7402, 512), (1415, 8363, 512),
          (5818, 2062, 512), (2576, 4728, 512)]
+# 256x256 tiles whose last round runs as halves of 128 rows, the last of them with rows and without
+HALVES = [(2566, 7693, 640), (3714, 5389, 640), (2309, 8624, 640), (6019, 3338, 1152)]
 
 
 def squares(a, sa, b, sb, b_block):
@@ -61,7 +63,7 @@ def beyond_rounding(got, ref, scale):
 
 
 @pytest.mark.parametrize("b_block", [128, 1])
-@pytest.mark.parametrize("c", TILES, ids=str)
+@pytest.mark.parametrize("c", TILES + HALVES, ids=str)
 def test_dense(device, c, b_block):
     m, n, k = c
     say("dense", c, b_block)
