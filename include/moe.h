@@ -418,6 +418,10 @@ int moe_quantize_cols_e4m3(int32_t m, int32_t n, const void* x, uint8_t* xq, flo
  *   y    a = x by rows,              b = w, b_block 128
  *   d_x  a = d_y by rows,            b = w transposed (codes [k, n], scales [k/128, n/128])
  *   d_w  a = d_y by columns [n, mp], b = x by columns [k, mp], b_block 1
+ * By rows: moe_quantize_rows_e4m3 with a problem of T = m, H = k, I = 128, E = top_k = 1 (k at most
+ * 32768, m*k below 2^31; larger matrices are the caller's to quantise), by columns:
+ * moe_quantize_cols_e4m3.  The experts' weight gradient takes rows offsets[e] to offsets[e+1] of x and d_y in
+ * sorted order, whose padding rows moe_permute and moe_unpermute_bwd leave as zeros.
  * Needs m, n >= 1; k a positive multiple of 128, at most 2^22; m and n at most 2^24; and
  * ceil(m/16) * ceil(n/16) <= 2^29 (MOE_ERR_SHAPE otherwise).
  * In:  a uint8 [m, k] (e4m3 codes), a_scales fp32 [m, k/128]; b uint8 [n, k], b_scales

@@ -1,10 +1,11 @@
-"""The largest sizes that the operators' calls accept in one dimension, many experts per token, and
-dense products and the transposed quantiser in a captured graph; against 64 bits."""
+"""The largest sizes that the operators' calls accept in one dimension, many experts per token, one
+expert's weight gradient, and dense products and the transposed quantiser in a captured graph; against
+64 bits."""
 import pytest
 import torch
 
 import routed_grouped_gemm_topk_amd as moe
-from test_gpu_operators import (TD, U32, UT, Guarded, aligned, close, gemm_tol, gen, operands,
+from test_gpu_operators import (TD, U32, UBF, UT, Guarded, aligned, close, gemm_tol, gen, operands,
                                 product, say, sorted_rows)
 
 pytestmark = pytest.mark.gpu
@@ -117,6 +118,42 @@ def test_many_experts_per_token(device, T, E, k, bm, dtype):
     close(d_w, terms.sum(2), (H / 64 + 8) * U32 * terms.abs().sum(2), "d_weights")
     want = (wd * d_out.double()[:, None, :])[there[:, :, 0]]
     close(d_rows[at[there[:, :, 0]]], want, (u + 2 * U32) * want.abs() + 1e-38, "d_rows")
+
+
+def test_expert_weight_gradients(device):
+    """d_w[e] = sum over the expert's rows of d_y x, from slices of the sorted rows, padding and all:
+    the product of the codes, and within e4m3's rounding (2^-4 of each operand, and what falls below
+    the smallest code) that of the tokens themselves."""
+    T, H, n, E, k, bm = 500, 256, 136, 6, 2, 64
+    p, a, used, ss, held = aligned(device, T, H, E, k, bm, "some", 110)
+    pn = moe.make_problem(T, 192, 128, E, k, "bf16", None, bm)
+    g = gen(device, 111)
+    x = torch.randn((T, H), generator=g, device=device).bfloat16()
+    d_out = torch.randn((T, 192), generator=g, device=device).bfloat16()
+    w = torch.rand((T, k), generator=g, device=device) + 0.5
+    rows, _ = moe.permute(p, x, a)
+    y = sorted_rows(device, ss, held, 192, torch.bfloat16, 112)
+    d_rows, _ = moe.unpermute_bwd(pn, d_out, y, a, w)
+    at = a["offsets"].tolist()
+    for e in range(E):
+        mine = slice(at[e], at[e + 1])
+        if at[e] == at[e + 1]:
+            continue
+        dy = d_rows[mine, :n].contiguous()
+        q, s = moe.quantize_cols_e4m3(dy)
+        qx, sx = moe.quantize_cols_e4m3(rows[mine])
+        dw = moe.gemm_e4m3(q, s, qx, sx, out_dtype=torch.float32, b_block=1)
+        torch.cuda.synchronize()
+        ref, mag = product(q, s, qx, sx, 1)
+        close(dw, ref, gemm_tol(ref, mag, q.shape[1], "f32"), f"expert {e}")
+        slot = ss[mine][held[mine]]
+        d64 = d_out.double()[slot // k, :n] * w.double().view(-1)[slot][:, None]
+        x64 = x.double()[slot // k]
+        m = slot.numel()
+        sub = 2.0 ** -10 * m * (s.double().amax(1)[:, None] * x64.abs().amax() * 2
+                                + sx.double().amax(1)[None, :] * d64.abs().amax() * 2)
+        tol = (2 * 2.0 ** -4 + 2.0 ** -8 + UBF) * 1.01 * (d64.abs().t() @ x64.abs()) + sub
+        close(dw, d64.t() @ x64, tol, f"expert {e}, its tokens")
 
 
 def test_products_in_a_graph(device):
