@@ -26,7 +26,17 @@
  *                          expert, a dense projection, their gradients)
  *   moe_grouped_gemm_e4m3  the same over expert-sorted rows
  *   moe_quantize_cols_e4m3 transposed quantisation, the operands of a weight gradient
- * The outputs of these must not overlap their inputs.  There is no gradient of the experts' own
+ * and what stands before it and beside it in a block:
+ *   moe_route_scored       experts by softmax or sigmoid scores, with a bias for balance and
+ *                          groups of experts, renormalised and scaled weights; its gradient
+ *                          moe_route_scored_bwd
+ *   moe_rms_norm           root-mean-square norm of token rows, with the residual's addition and
+ *                          e4m3 codes as output; its gradient moe_rms_norm_bwd
+ *   moe_gemm_bf16          product of bf16 matrices with bias, activation and residual (router
+ *                          logits, dense projections) and, by its layouts, its operands'
+ *                          gradients; moe_act_bwd: the activation's and the bias'
+ * The outputs of these must not overlap their inputs, but where an entry point names an input that
+ * may be the output's own memory.  There is no gradient of the experts' own
  * weights: moe_quantize_cols_e4m3 and moe_gemm_e4m3 give it for one expert's rows at a time.
  *
  * Conventions shared by every entry point
@@ -67,7 +77,9 @@ typedef enum moe_status {
  * Pointer alignment (checked on the host before any launch; MOE_ERR_ALIGN otherwise):
  *   16 bytes: data arrays -- X and its codes, weights, act, slot rows, out, bias;
  *   4 bytes:  int32 and fp32 index, routing-weight, logit and scale arrays;
- *   256 bytes: the workspaces of moe_forward and moe_grouped_gemm_down.
+ *   256 bytes: the workspaces (moe_forward, moe_grouped_gemm_up and _down, moe_rms_norm_bwd,
+ *              moe_act_bwd).
+ * moe_rms_norm and its gradient ask for 16 bytes of every array but rstd.
  * Memory from hipMalloc or a torch allocation at offset 0 satisfies all of them.
  */
 
@@ -206,6 +218,115 @@ int moe_route_align(const moe_problem* p, const float* logits, int renormalize,
                     int32_t* topk_ids, float* topk_weights, int32_t* counts, int32_t* offsets,
                     int32_t* sorted_slots, int32_t* slot_row, int32_t* tiles, int32_t* num_tiles,
                     int32_t* n_invalid, void* stream);
+
+/*
+ * How moe_route_scored chooses and weighs experts.
+ * Limits: n_groups 1 to 64 and a divisor of E; 1 <= topk_groups <= n_groups; group_top 1 or 2;
+ *         top_k <= 64 and top_k <= topk_groups * (E / n_groups); scale finite.
+ */
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef struct moe_router {
+  int32_t score;        /* moe_score                                                        */
+  int32_t renormalize;  /* weights divided by their sum over the chosen experts             */
+  int32_t n_groups;     /* groups of E / n_groups neighbouring experts; 1: none             */
+  int32_t topk_groups;  /* groups that a token may choose from                              */
+  int32_t group_top;    /* a group's value is the sum of its group_top largest choice scores */
+  float scale;          /* factor of the weights                                            */
+} moe_router;
+
+/* Host-only validation of a router for a problem; MOE_OK or the negative status that the two
+ * entry points below would return. */
+int moe_router_validate(const moe_problem* p, const moe_router* r);
+
+/*
+ * moe_route_scored -- router producer with scores, a bias for balance and groups of experts.
+ * For every token t:
+ *   s_e = softmax(logits[t, :])_e, or 1 / (1 + exp(-logits[t, e]))
+ *   c_e = s_e + bias[e]                       the choice score; bias NULL: s_e
+ *   the topk_groups groups of the largest value are kept, ties to the lower group; the top_k
+ *   experts of the largest c among them are topk_ids[t, :], descending, ties to the lower id
+ *   topk_weights[t, j] = scale * s_e of that expert (without the bias), divided by the sum of s
+ *   over the chosen ones when renormalize != 0 (0 where that sum is 0)
+ * Scores, group values and choice are computed in 64 bits, so that the choice is that of exact
+ * arithmetic but for scores closer than about 2^-50; where no bias and no sum of scores counts
+ * (bias NULL, and n_groups == topk_groups or group_top 1) the logits are compared, which the
+ * scores keep in order.
+ * A logit of -inf or NaN takes its expert out: its score is 0 and it is never chosen; a bias of
+ * -inf or NaN keeps it from being chosen.  A group value counts the experts that can be chosen,
+ * and a group without any is not kept.  Where fewer than top_k experts can be chosen, the ids left
+ * over are -1 (excluded by moe_align) with weight 0.  +inf counts as the largest finite logit.
+ * In:  logits       logit_dtype (MOE_F32 or MOE_BF16) [T, E];  bias fp32 [E] or NULL
+ * Out: topk_ids     int32 [T, top_k];  topk_weights fp32 [T, top_k].
+ * Of the problem T, E and top_k count.  Deterministic.
+ */
+int moe_route_scored(const moe_problem* p, const moe_router* router, const void* logits,
+                     int32_t logit_dtype, const float* bias, int32_t* topk_ids,
+                     float* topk_weights, void* stream);
+
+/*
+ * moe_route_scored_bwd -- gradient of moe_route_scored's weights with respect to the logits.
+ * With s the scores, c_j = topk_ids[t, j], w_j the weights for the same router, and
+ * G = sum_j w_j d_weights[t, j]:
+ *   sigmoid:  d_logits[t, e] = sum over j with c_j = e of w_j (1 - s_e) (d_weights[t, j] - [G / scale])
+ *   softmax:  d_logits[t, e] = sum over j with c_j = e of w_j (d_weights[t, j] - [G / scale])
+ *                              - (0 with renormalize, s_e G without)
+ * where the terms in brackets are there with renormalize only; 0 elsewhere.  The choice and the
+ * bias have no gradient.  Slots whose id is outside [0,E) add nothing and their d_weights is not
+ * used; nor are experts that a logit of -inf or NaN took out.
+ * In:  logits logit_dtype [T,E]; topk_ids int32 [T,top_k]; d_weights fp32 [T,top_k]
+ * Out: d_logits logit_dtype [T,E], every element written.
+ * Sums in 32 bits or more, rounded once.  Deterministic.
+ */
+int moe_route_scored_bwd(const moe_problem* p, const moe_router* router, const void* logits,
+                         int32_t logit_dtype, const int32_t* topk_ids, const float* d_weights,
+                         void* d_logits, void* stream);
+
+/*
+ * moe_rms_norm -- root-mean-square norm of token rows, with the residual's addition before it.
+ * For every row i in [0, t):
+ *   s[i, :]      = round(x[i, :] + residual[i, :])       (x itself without residual)
+ *   rstd[i]      = 1 / sqrt(mean over h of s[i, h]^2 + eps)
+ *   n[i, h]      = s[i, h] * rstd[i] * weight[h]          (weight NULL: 1)
+ *   y[i, :]      = round(n[i, :])
+ *   scales[i, g] = amax |n[i, g-group]| / 448 over 128 columns (1 if they are all zero)
+ *   codes[i, h]  = e4m3(n[i, h] / scales[i, h/128]), nearest even
+ * The norm is taken of the rounded sum, so that it is that of the rows which go on as the residual
+ * stream; n is held in fp32 and rounded once for either output; the mean is held in 64 bits.
+ * row_dtype: MOE_F32 or MOE_BF16, of x, residual, weight, sum and y.  Needs t >= 1, 1 <= h <= 32768
+ * (a multiple of 128 with codes), eps >= 0 and finite (MOE_ERR_SHAPE otherwise).
+ * In:  x, residual row_dtype [t, h] (residual NULL: none); weight row_dtype [h] or NULL
+ * Out: sum   row_dtype [t, h], given exactly when residual is; may be x's or residual's own memory
+ *      y     row_dtype [t, h], or NULL
+ *      codes uint8 [t, h] and scales fp32 [t, h/128], or both NULL (not without y)
+ *      rstd  fp32 [t], or NULL
+ * Deterministic.
+ */
+int moe_rms_norm(int32_t t, int32_t h, int32_t row_dtype, const void* x, const void* residual,
+                 const void* weight, float eps, void* sum, void* y, uint8_t* codes, float* scales,
+                 float* rstd, void* stream);
+
+/*
+ * moe_rms_norm_bwd -- gradient of moe_rms_norm's y with respect to the rows and to the weight.
+ * With n = s[i, h] * rstd[i] and g = d_y[i, h] * weight[h]:
+ *   d_x[i, h]   = round( rstd[i] * (g - n * mean over h of (g n)) + d_sum[i, h] )
+ *   d_weight[h] = sum over i of d_y[i, h] * n              (fp32, a fixed order of additions)
+ * d_sum is the gradient that reaches the sum past the norm (the residual stream's), NULL: none; the
+ * gradient of x and that of the residual are both d_x.  s: the sum of moe_rms_norm, or x.
+ * In:  d_y, d_sum, s row_dtype [t, h]; weight row_dtype [h] or NULL; rstd fp32 [t]
+ * Out: d_x row_dtype [t, h], may be d_y's or d_sum's own memory; d_weight fp32 [h], or NULL
+ * workspace: moe_rms_norm_bwd_workspace_bytes bytes of device memory, 256-byte aligned, with
+ *      d_weight only (NULL without it).  It needs no initial contents; calls that share one must
+ *      not overlap.
+ * Sizes and row_dtype as moe_rms_norm.  Deterministic on one device: the order of additions
+ * depends on the sizes and on the device's number of compute units.
+ */
+int moe_rms_norm_bwd(int32_t t, int32_t h, int32_t row_dtype, const void* d_y, const void* d_sum,
+                     const void* s, const void* weight, const float* rstd, void* d_x,
+                     float* d_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of moe_rms_norm_bwd's workspace; negative moe_status for sizes that it refuses.  An upper
+ * bound that holds on every device. */
+int64_t moe_rms_norm_bwd_workspace_bytes(int32_t t, int32_t h);
 
 /*
  * moe_quantize_rows_e4m3 -- fp8 workload only (dtype BF16, w_dtype E4M3).
@@ -458,6 +579,61 @@ int moe_grouped_gemm_e4m3(const moe_problem* p, int32_t n, int32_t k, const uint
                           const int32_t* sorted_slots, const int32_t* offsets,
                           const int32_t* tiles, const int32_t* num_tiles, void* out,
                           int32_t out_dtype, void* stream);
+
+typedef enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_SILU = 1,       /* z / (1 + exp(-z))                                       */
+  MOE_ACT_GELU = 2,       /* z (1 + erf(z / sqrt 2)) / 2                             */
+  MOE_ACT_GELU_TANH = 3   /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2         */
+} moe_act;
+
+typedef enum moe_layout {
+  MOE_NT = 0,  /* a [m, k], b [n, k]:  z = a b^T    a projection's weight as it is stored */
+  MOE_NN = 1,  /* a [m, k], b [k, n]:  z = a b      the gradient of the projection's rows  */
+  MOE_TN = 2   /* a [k, m], b [k, n]:  z = a^T b    the gradient of its weight             */
+} moe_layout;
+
+/*
+ * moe_gemm_bf16 -- product of bf16 matrices with bias, activation and residual in its epilogue.
+ *   z[i, j]   = sum over k of a[., .] b[., .] + bias[j]      (bias NULL: 0)
+ *   pre[i, j] = round(z[i, j])
+ *   c[i, j]   = round( act(z[i, j]) + residual[i, j] )       (residual NULL: 0)
+ * accumulated in fp32; the epilogue is fp32 and rounds once.  pre is what moe_act_bwd takes.
+ * The products of a projection y = act(x w^T + bias) + r of x [m, k] by w [n, k]:
+ *   y     MOE_NT  a = x,    b = w        moe_gemm_bf16(m, n, k)
+ *   d_z, d_bias   moe_act_bwd of d_y; the gradient of r is d_y
+ *   d_x   MOE_NN  a = d_z,  b = w        moe_gemm_bf16(m, k, n)
+ *   d_w   MOE_TN  a = d_z,  b = x        moe_gemm_bf16(n, k, m)
+ * Needs m, n, k >= 1 and at most 2^24, ceil(m/16) * ceil(n/16) <= 2^29, and a layout and an act of
+ * those above (MOE_ERR_SHAPE otherwise).  Rows of a and b that are no multiple of 16 bytes (8 values) run on a slower kernel.
+ * In:  a, b bf16; bias fp32 [n] or NULL; residual c_dtype [m, n] or NULL
+ * Out: c c_dtype (MOE_F32 or MOE_BF16) [m, n], may be residual's own memory; pre bf16 [m, n] or NULL
+ * Deterministic on one device: the order of the additions depends on the sizes, the layout and
+ * the device's number of compute units, which choose the kernel, and on nothing else.
+ */
+int moe_gemm_bf16(int32_t m, int32_t n, int32_t k, int32_t layout, const void* a, const void* b,
+                  const float* bias, int32_t act, const void* residual, void* pre, void* c,
+                  int32_t c_dtype, void* stream);
+
+/*
+ * moe_act_bwd -- gradient of moe_gemm_bf16's epilogue: of the activation and of the bias.
+ *   v[i, j]   = d_c[i, j] * act'(pre[i, j])       (d_c itself for MOE_ACT_NONE)
+ *   d_z[i, j] = round(v[i, j])
+ *   d_bias[j] = sum over i of v[i, j]             (fp32, before the rounding; a fixed order)
+ * In:  d_c bf16 [m, n]; pre bf16 [m, n] (NULL exactly with MOE_ACT_NONE)
+ * Out: d_z bf16 [m, n], may be d_c's or pre's own memory (NULL exactly with MOE_ACT_NONE: it is
+ *      d_c); d_bias fp32 [n] or NULL (not with MOE_ACT_NONE)
+ * workspace: moe_act_bwd_workspace_bytes bytes of device memory, 256-byte aligned, with d_bias only
+ *      (NULL without it).  It needs no initial contents; calls that share one must not overlap.
+ * Needs m, n >= 1 and at most 2^24, and an act of those above (MOE_ERR_SHAPE otherwise).
+ * Deterministic as moe_rms_norm_bwd is.
+ */
+int moe_act_bwd(int32_t m, int32_t n, int32_t act, const void* d_c, const void* pre, void* d_z,
+                float* d_bias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of moe_act_bwd's workspace; negative moe_status for sizes that it refuses.  An upper bound
+ * that holds on every device. */
+int64_t moe_act_bwd_workspace_bytes(int32_t m, int32_t n);
 
 /*
  * moe_forward -- the whole layer: align, [quantise X], up, down, combine.

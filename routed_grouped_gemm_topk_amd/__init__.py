@@ -4,18 +4,23 @@ The computation lives in libmoe.so (hand-written HIP kernels behind the C ABI of
 include/moe.h).  This package is its Python binding: ``_lib`` mirrors the C
 entry points one to one; the helpers below only allocate buffers with torch
 and call them.  Nothing here records for automatic differentiation: results have
-no graph, also where an input requires a gradient; unpermute_bwd, route_bwd and
-the products of the gradients (moe_gemm_e4m3 in moe.h) are the caller's to run.
+no graph, also where an input requires a gradient; the gradients (unpermute_bwd,
+route_bwd, route_scored_bwd, rms_norm_bwd, act_bwd, the products of moe_gemm_bf16
+and moe_gemm_e4m3 in moe.h) are the caller's to run.
 """
 from __future__ import annotations
 
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
 from ._lib import (  # noqa: F401
     EXPORTS,
     LIB_PATH,
+    MOE_ACT_GELU,
+    MOE_ACT_GELU_TANH,
+    MOE_ACT_NONE,
+    MOE_ACT_SILU,
     MOE_BF16,
     MOE_E4M3,
     MOE_ERR_ALIGN,
@@ -27,17 +32,27 @@ from ._lib import (  # noqa: F401
     MOE_ERR_WORKSPACE,
     MOE_F32,
     MOE_MXFP4,
+    MOE_NN,
+    MOE_NT,
     MOE_OK,
+    MOE_SCORE_SIGMOID,
+    MOE_SCORE_SOFTMAX,
+    MOE_TN,
     MoeError,
     Problem,
+    Router,
     load,
     make_problem,
+    make_router,
+    moe_act_bwd,
+    moe_act_bwd_workspace_bytes,
     moe_align,
     moe_block_m_for,
     moe_combine,
     moe_gemm_workspace_bytes,
     moe_forward,
     moe_forward_scratch,
+    moe_gemm_bf16,
     moe_gemm_e4m3,
     moe_grouped_gemm_down,
     moe_grouped_gemm_e4m3,
@@ -49,9 +64,15 @@ from ._lib import (  # noqa: F401
     moe_pick_block_m,
     moe_quantize_cols_e4m3,
     moe_quantize_rows_e4m3,
+    moe_rms_norm,
+    moe_rms_norm_bwd,
+    moe_rms_norm_bwd_workspace_bytes,
     moe_route,
     moe_route_align,
     moe_route_bwd,
+    moe_route_scored,
+    moe_route_scored_bwd,
+    moe_router_validate,
     moe_scratch_max_bytes,
     moe_unpermute,
     moe_unpermute_bwd,
@@ -223,3 +244,115 @@ def grouped_gemm_e4m3(p: Problem, rows: torch.Tensor, row_scales: torch.Tensor, 
     moe_grouped_gemm_e4m3(p, rows, row_scales, w, w_scales, a["sorted_slots"], a["offsets"],
                           a["tiles"], a["num_tiles"], out, stream)
     return out
+
+
+# ---------------------------------------------------------------------------------------------
+# before the layer and beside it: router with scores, norm, bf16 products with an epilogue
+# ---------------------------------------------------------------------------------------------
+def route_scored(p: Problem, r: Router, logits: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                 stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Experts and weights by scores (fp32 or bf16 logits), with a bias for balance and groups,
+    through moe_route_scored; returns (topk_ids int32 [T,k], topk_weights fp32 [T,k])."""
+    ids = _new(logits, (p.T, p.top_k), torch.int32, stream)
+    w = _new(logits, (p.T, p.top_k), torch.float32, stream)
+    moe_route_scored(p, r, logits, bias, ids, w, stream)
+    return ids, w
+
+
+def route_scored_bwd(p: Problem, r: Router, logits: torch.Tensor, topk_ids: torch.Tensor,
+                     d_weights: torch.Tensor, d_logits: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Gradient of route_scored's weights with respect to the logits through
+    moe_route_scored_bwd."""
+    if d_logits is None:
+        d_logits = _new(logits, (p.T, p.E), logits.dtype, stream)
+    moe_route_scored_bwd(p, r, logits, topk_ids, d_weights, d_logits, stream)
+    return d_logits
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+             residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             want: Sequence[str] = ("y",), sum: Optional[torch.Tensor] = None,
+             stream=None) -> dict:
+    """Root-mean-square norm of the rows of x (plus residual) through moe_rms_norm.  `want` names
+    the outputs: "y" (rows), "codes" (e4m3 codes, with "scales" per 128 columns) and "rstd" (for
+    rms_norm_bwd); with a residual "sum" comes too, in `sum` if given (residual or x, say)."""
+    for name in want:
+        if name not in ("y", "codes", "rstd"):
+            raise ValueError(f"want: {name!r}, expected 'y', 'codes' or 'rstd'")
+    t, h = x.shape
+    out = {}
+    if residual is not None:
+        out["sum"] = sum if sum is not None else _new(x, (t, h), x.dtype, stream)
+    elif sum is not None:
+        raise ValueError("sum: given without a residual")
+    if "y" in want:
+        out["y"] = _new(x, (t, h), x.dtype, stream)
+    if "codes" in want:
+        out["codes"] = _new(x, (t, h), torch.float8_e4m3fn, stream)
+        out["scales"] = _new(x, (t, h // 128), torch.float32, stream)
+    if "rstd" in want:
+        out["rstd"] = _new(x, (1, t), torch.float32, stream).view(t)
+    get = out.get
+    moe_rms_norm(x, residual, weight, eps, get("sum"), get("y"), get("codes"), get("scales"),
+                 get("rstd"), stream)
+    return out
+
+
+def rms_norm_bwd(d_y: torch.Tensor, s: torch.Tensor, weight: Optional[torch.Tensor],
+                 rstd: torch.Tensor, d_sum: Optional[torch.Tensor] = None, d_weight: bool = True,
+                 d_x: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gradient of rms_norm's y through moe_rms_norm_bwd, from the rows s that it was taken of
+    ("sum", or x without a residual), its rstd, and d_sum, the gradient that reaches s otherwise;
+    returns (d_x, the gradient of the rows and of the residual; d_weight fp32, None if not asked
+    for)."""
+    t, h = d_y.shape
+    if d_x is None:
+        d_x = _new(d_y, (t, h), d_y.dtype, stream)
+    dw = None
+    if d_weight:
+        dw = _new(d_y, (1, h), torch.float32, stream).view(h)
+        if workspace is None:
+            workspace = _new(d_y, (1, moe_rms_norm_bwd_workspace_bytes(t, h)), torch.uint8, stream)
+    moe_rms_norm_bwd(d_y, d_sum, s, weight, rstd, d_x, dw, workspace if d_weight else None, stream)
+    return d_x, dw
+
+
+def gemm_bf16(a: torch.Tensor, b: torch.Tensor, layout: str = "nt",
+              bias: Optional[torch.Tensor] = None, act: str = "none",
+              residual: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+              with_pre: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+    """act(a b + bias) + residual through moe_gemm_bf16; layout "nt": a [m,k], b [n,k]; "nn":
+    a [m,k], b [k,n]; "tn": a [k,m], b [k,n].  bias fp32 [n]; residual as the output.  with_pre:
+    returns (out, pre), pre the bf16 values before the activation, for act_bwd."""
+    shape = (a.shape[1] if layout in ("tn", MOE_TN) else a.shape[0],
+             b.shape[0] if layout in ("nt", MOE_NT) else b.shape[1])
+    if out is None:
+        out = _new(a, shape, out_dtype, stream)
+    pre = _new(a, shape, torch.bfloat16, stream) if with_pre else None
+    moe_gemm_bf16(layout, a, b, bias, act, residual, pre, out, stream)
+    return (out, pre) if with_pre else out
+
+
+def act_bwd(d_c: torch.Tensor, pre: Optional[torch.Tensor] = None, act: str = "none",
+            d_bias: bool = False, d_z: Optional[torch.Tensor] = None,
+            workspace: Optional[torch.Tensor] = None,
+            stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gradient of gemm_bf16's epilogue through moe_act_bwd; returns (d_z, which is d_c itself
+    without an activation; the bias' gradient fp32 [n], None if not asked for)."""
+    m, n = d_c.shape
+    none = act in ("none", MOE_ACT_NONE)
+    if none and not d_bias:
+        return d_c, None
+    if none:                    # nothing to multiply with: d_z is d_c
+        pre = d_z = None
+    elif d_z is None:
+        d_z = _new(d_c, (m, n), torch.bfloat16, stream)
+    db = None
+    if d_bias:
+        db = _new(d_c, (1, n), torch.float32, stream).view(n)
+        if workspace is None:
+            workspace = _new(d_c, (1, moe_act_bwd_workspace_bytes(m, n)), torch.uint8, stream)
+    moe_act_bwd(act, d_c, pre, d_z, db, workspace if d_bias else None, stream)
+    return (d_c if none else d_z), db

@@ -31,13 +31,24 @@ MOE_F32, MOE_BF16, MOE_E4M3, MOE_MXFP4 = 0, 1, 2, 3
 _DT_NAME = {"f32": MOE_F32, "bf16": MOE_BF16, "e4m3": MOE_E4M3, "mxfp4": MOE_MXFP4}
 _TORCH_DT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_E4M3: torch.float8_e4m3fn}
 
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+_SCORE = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = 0, 1, 2, 3
+_ACT = {"none": MOE_ACT_NONE, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU,
+        "gelu_tanh": MOE_ACT_GELU_TANH}
+MOE_NT, MOE_NN, MOE_TN = 0, 1, 2
+_LAYOUT = {"nt": MOE_NT, "nn": MOE_NN, "tn": MOE_TN}
+
 EXPORTS = ["moe_status_str", "moe_validate", "moe_pick_block_m", "moe_block_m_for", "moe_max_padded_slots",
            "moe_max_tiles", "moe_workspace_bytes", "moe_route", "moe_route_align", "moe_align",
            "moe_quantize_rows_e4m3", "moe_grouped_gemm_up", "moe_grouped_gemm_up_mxfp4",
            "moe_grouped_gemm_down", "moe_gemm_workspace_bytes",
            "moe_combine", "moe_forward", "moe_scratch_max_bytes", "moe_forward_scratch",
            "moe_permute", "moe_unpermute", "moe_unpermute_bwd", "moe_route_bwd",
-           "moe_quantize_cols_e4m3", "moe_gemm_e4m3", "moe_grouped_gemm_e4m3"]
+           "moe_quantize_cols_e4m3", "moe_gemm_e4m3", "moe_grouped_gemm_e4m3",
+           "moe_router_validate", "moe_route_scored", "moe_route_scored_bwd", "moe_rms_norm",
+           "moe_rms_norm_bwd", "moe_rms_norm_bwd_workspace_bytes", "moe_gemm_bf16", "moe_act_bwd",
+           "moe_act_bwd_workspace_bytes"]
 
 
 class MoeError(RuntimeError):
@@ -63,6 +74,27 @@ def make_problem(T, H, I, E, top_k, dtype="bf16", w_dtype=None, block_m=0) -> Pr
     return Problem(int(T), int(H), int(I), int(E), int(top_k), int(block_m), dt, wdt)
 
 
+class Router(ctypes.Structure):
+    """Mirror of ``moe_router``."""
+    _fields_ = [("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+    def __repr__(self):
+        return ("Router(score=%d, renormalize=%d, n_groups=%d, topk_groups=%d, group_top=%d, scale=%g)"
+                % (self.score, self.renormalize, self.n_groups, self.topk_groups, self.group_top,
+                   self.scale))
+
+
+def make_router(score="softmax", renormalize=True, n_groups=1, topk_groups=None, group_top=1,
+                scale=1.0) -> Router:
+    """How route_scored chooses and weighs experts; topk_groups None: all groups."""
+    sc = _SCORE[score] if isinstance(score, str) else int(score)
+    kept = n_groups if topk_groups is None else topk_groups
+    return Router(sc, 1 if renormalize else 0, int(n_groups), int(kept), int(group_top),
+                  float(scale))
+
+
 _lib = None
 
 
@@ -77,8 +109,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                           "`python -m routed_grouped_gemm_topk_amd.build` (needs hipcc)")
     lib = ctypes.CDLL(p)
     P = ctypes.POINTER(Problem)
+    Q = ctypes.POINTER(Router)
     vp = ctypes.c_void_p
     i32 = ctypes.c_int32
+    f32 = ctypes.c_float
+    size = ctypes.c_size_t
     sig = {
         "moe_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "moe_validate": (ctypes.c_int, [P]),
@@ -107,6 +142,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_quantize_cols_e4m3": (ctypes.c_int, [i32] * 2 + [vp] * 3 + [vp]),
         "moe_gemm_e4m3": (ctypes.c_int, [i32] * 3 + [vp] * 4 + [i32, vp, i32, vp]),
         "moe_grouped_gemm_e4m3": (ctypes.c_int, [P, i32, i32] + [vp] * 9 + [i32, vp]),
+        "moe_router_validate": (ctypes.c_int, [P, Q]),
+        "moe_route_scored": (ctypes.c_int, [P, Q, vp, i32] + [vp] * 3 + [vp]),
+        "moe_route_scored_bwd": (ctypes.c_int, [P, Q, vp, i32] + [vp] * 3 + [vp]),
+        "moe_rms_norm": (ctypes.c_int, [i32] * 3 + [vp] * 3 + [f32] + [vp] * 5 + [vp]),
+        "moe_rms_norm_bwd": (ctypes.c_int, [i32] * 3 + [vp] * 8 + [size, vp]),
+        "moe_rms_norm_bwd_workspace_bytes": (ctypes.c_int64, [i32, i32]),
+        "moe_gemm_bf16": (ctypes.c_int, [i32] * 4 + [vp] * 3 + [i32] + [vp] * 3 + [i32, vp]),
+        "moe_act_bwd": (ctypes.c_int, [i32] * 3 + [vp] * 5 + [size, vp]),
+        "moe_act_bwd_workspace_bytes": (ctypes.c_int64, [i32, i32]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -351,7 +395,7 @@ def moe_forward_scratch(p: Problem, x, topk_ids, topk_weights, w13, w13_scales, 
 
 
 # ---------------------------------------------------------------------------------------------
-# rows in expert-sorted order, gradients, products of e4m3 codes.  Every tensor of a call must be
+# rows in expert-sorted order, router, norm, products, gradients.  Every tensor of a call must be
 # on the current device: the launch goes to that device's stream.  A call's host time is that of
 # these checks next to 3.5 us of launch, so the common case of each is one expression (0.3 us a
 # tensor) and only a tensor that fails it is looked at again, for the reason.
@@ -518,3 +562,127 @@ def moe_grouped_gemm_e4m3(p: Problem, rows, row_scales, w, w_scales, sorted_slot
         _arg(tiles, "tiles", _I32, 2 * moe_max_tiles(p), dev),
         _arg(num_tiles, "num_tiles", _I32, 1, dev), _mat(out, "out", _OUT, (rm, n), dev),
         _row_dtype(out, "out"), _where(stream, dev)), "moe_grouped_gemm_e4m3")
+
+
+# ---------------------------------------------------------------------------------------------
+# router with scores, norm, bf16 products with an epilogue
+# ---------------------------------------------------------------------------------------------
+_LOGITS = (torch.float32, torch.bfloat16)
+
+
+def moe_router_validate(p: Problem, r: Router) -> int:
+    return load().moe_router_validate(ctypes.byref(p), ctypes.byref(r))
+
+
+def moe_route_scored(p: Problem, r: Router, logits, bias, topk_ids, topk_weights,
+                     stream=None) -> None:
+    dt = _row_dtype(logits, "logits")
+    dev = _device()
+    T, N = p.T, p.T * p.top_k
+    _checked(load().moe_route_scored(
+        ctypes.byref(p), ctypes.byref(r), _arg(logits, "logits", _LOGITS, T * p.E, dev), dt,
+        _arg(bias, "bias", _F32, p.E, dev), _arg(topk_ids, "topk_ids", _I32, N, dev),
+        _arg(topk_weights, "topk_weights", _F32, N, dev), _where(stream, dev)),
+        "moe_route_scored")
+
+
+def moe_route_scored_bwd(p: Problem, r: Router, logits, topk_ids, d_weights, d_logits,
+                         stream=None) -> None:
+    dt = _row_dtype(logits, "logits")
+    dev = _device()
+    L, N = p.T * p.E, p.T * p.top_k
+    _checked(load().moe_route_scored_bwd(
+        ctypes.byref(p), ctypes.byref(r), _arg(logits, "logits", _LOGITS, L, dev), dt,
+        _arg(topk_ids, "topk_ids", _I32, N, dev), _arg(d_weights, "d_weights", _F32, N, dev),
+        _arg(d_logits, "d_logits", (logits.dtype,), L, dev), _where(stream, dev)),
+        "moe_route_scored_bwd")
+
+
+def _rows(x, name: str, where: str):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix")
+    _refuse_past_int32(where, *x.shape)
+    return x.shape
+
+
+def moe_rms_norm(x, residual, weight, eps: float, sum, y, codes, scales, rstd,
+                 stream=None) -> None:
+    t, h = shape = _rows(x, "x", "moe_rms_norm")
+    dt = _row_dtype(x, "x")
+    same = (x.dtype,)
+    dev = _device()
+    _checked(load().moe_rms_norm(
+        t, h, dt, _arg(x, "x", same, t * h, dev), _mat(residual, "residual", same, shape, dev),
+        _arg(weight, "weight", same, h, dev), eps, _mat(sum, "sum", same, shape, dev),
+        _mat(y, "y", same, shape, dev), _mat(codes, "codes", _CODES, shape, dev),
+        _mat(scales, "scales", _F32, (t, h // 128), dev), _arg(rstd, "rstd", _F32, t, dev),
+        _where(stream, dev)), "moe_rms_norm")
+
+
+def moe_rms_norm_bwd_workspace_bytes(t: int, h: int) -> int:
+    _refuse_past_int32("moe_rms_norm_bwd_workspace_bytes", t, h)
+    return _checked(load().moe_rms_norm_bwd_workspace_bytes(t, h),
+                    "moe_rms_norm_bwd_workspace_bytes")
+
+
+def _space(workspace, dev: int):
+    """Pointer and size of an optional workspace."""
+    if workspace is None:
+        return None, 0
+    return (_arg(workspace, "workspace", (torch.uint8,), workspace.numel(), dev),
+            workspace.numel())
+
+
+def moe_rms_norm_bwd(d_y, d_sum, s, weight, rstd, d_x, d_weight, workspace, stream=None) -> None:
+    t, h = shape = _rows(d_y, "d_y", "moe_rms_norm_bwd")
+    dt = _row_dtype(d_y, "d_y")
+    same = (d_y.dtype,)
+    dev = _device()
+    _checked(load().moe_rms_norm_bwd(
+        t, h, dt, _arg(d_y, "d_y", same, t * h, dev), _mat(d_sum, "d_sum", same, shape, dev),
+        _mat(s, "s", same, shape, dev), _arg(weight, "weight", same, h, dev),
+        _arg(rstd, "rstd", _F32, t, dev), _mat(d_x, "d_x", same, shape, dev),
+        _arg(d_weight, "d_weight", _F32, h, dev), *_space(workspace, dev), _where(stream, dev)),
+        "moe_rms_norm_bwd")
+
+
+def _named(value, names: dict, what: str) -> int:
+    got = names.get(value, value) if isinstance(value, str) else value
+    if isinstance(got, str):
+        raise ValueError(f"{what}: {value!r}, expected one of {', '.join(names)}")
+    return int(got)
+
+
+def moe_gemm_bf16(layout, a, b, bias, act, residual, pre, c, stream=None) -> None:
+    layout, act = _named(layout, _LAYOUT, "layout"), _named(act, _ACT, "act")
+    if layout not in _LAYOUT.values():
+        raise MoeError(MOE_ERR_SHAPE, "moe_gemm_bf16")
+    a0, a1 = _rows(a, "a", "moe_gemm_bf16")
+    b0, b1 = _rows(b, "b", "moe_gemm_bf16")
+    m, k = (a1, a0) if layout == MOE_TN else (a0, a1)
+    n, kb = (b0, b1) if layout == MOE_NT else (b1, b0)
+    if k != kb:
+        raise ValueError(f"b: shape {tuple(b.shape)}, its k is {kb}, that of a is {k}")
+    dev = _device()
+    shape = (m, n)
+    dt = _row_dtype(c, "c")
+    _checked(load().moe_gemm_bf16(
+        m, n, k, layout, _arg(a, "a", _BF16, m * k, dev), _arg(b, "b", _BF16, n * k, dev),
+        _arg(bias, "bias", _F32, n, dev), act, _mat(residual, "residual", (c.dtype,), shape, dev),
+        _mat(pre, "pre", _BF16, shape, dev), _mat(c, "c", _OUT, shape, dev), dt,
+        _where(stream, dev)), "moe_gemm_bf16")
+
+
+def moe_act_bwd_workspace_bytes(m: int, n: int) -> int:
+    _refuse_past_int32("moe_act_bwd_workspace_bytes", m, n)
+    return _checked(load().moe_act_bwd_workspace_bytes(m, n), "moe_act_bwd_workspace_bytes")
+
+
+def moe_act_bwd(act, d_c, pre, d_z, d_bias, workspace, stream=None) -> None:
+    m, n = shape = _rows(d_c, "d_c", "moe_act_bwd")
+    dev = _device()
+    _checked(load().moe_act_bwd(
+        m, n, _named(act, _ACT, "act"), _arg(d_c, "d_c", _BF16, m * n, dev),
+        _mat(pre, "pre", _BF16, shape, dev), _mat(d_z, "d_z", _BF16, shape, dev),
+        _arg(d_bias, "d_bias", _F32, n, dev), *_space(workspace, dev), _where(stream, dev)),
+        "moe_act_bwd")

@@ -109,6 +109,38 @@ int validate_gemm(int32_t m, int32_t n, int32_t k) {
   return MOE_OK;
 }
 
+int validate_router(const moe_problem* p, const moe_router* q) {
+  const int v = validate(p);
+  if (v) return v;
+  if (!q) return MOE_ERR_NULL;
+  if (q->score != MOE_SCORE_SOFTMAX && q->score != MOE_SCORE_SIGMOID) return MOE_ERR_SHAPE;
+  if (q->n_groups < 1 || q->n_groups > kWave || p->E % q->n_groups) return MOE_ERR_SHAPE;
+  if (q->topk_groups < 1 || q->topk_groups > q->n_groups) return MOE_ERR_SHAPE;
+  if (q->group_top != 1 && q->group_top != 2) return MOE_ERR_SHAPE;
+  if (p->top_k > kRouteMaxK || p->top_k > q->topk_groups * (p->E / q->n_groups))
+    return MOE_ERR_SHAPE;
+  if (!(q->scale - q->scale == 0.0f)) return MOE_ERR_SHAPE;      // infinite or NaN
+  return MOE_OK;
+}
+
+int validate_norm(int32_t t, int32_t h) {
+  return t < 1 || h < 1 || h > kMaxDim ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+int validate_act(int32_t m, int32_t n, int32_t act) {
+  if (m < 1 || n < 1 || m > kGemmMaxDim || n > kGemmMaxDim) return MOE_ERR_SHAPE;
+  return act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+// Workspaces of moe_rms_norm_bwd and moe_act_bwd: rows of partial sums, at most as many as the
+// launches make on any device.
+int64_t norm_partial_bytes(int64_t t, int64_t h) {
+  return align_up((t < kPartialRows ? t : kPartialRows) * h * 4, 256);
+}
+int64_t act_partial_bytes(int32_t m, int32_t n) {
+  return align_up((int64_t)act_partial_rows(m, n, kMaxUnits) * n * 4, 256);
+}
+
 // Workspace pieces of moe_forward, in order, each 256-byte aligned.
 struct Layout {
   int64_t status, counts, offsets, sorted_slots, slot_row, tiles, num_tiles;
@@ -549,6 +581,110 @@ int moe_grouped_gemm_e4m3(const moe_problem* p, int32_t n, int32_t k, const uint
   return status_of(launch_grouped_gemm_e4m3(r, n, k, rows, row_scales, w, w_scales,
                                             sorted_slots, offsets, tiles, num_tiles, out,
                                             out_dtype == MOE_F32, (hipStream_t)stream));
+}
+
+int moe_router_validate(const moe_problem* p, const moe_router* r) { return validate_router(p, r); }
+
+int moe_route_scored(const moe_problem* p, const moe_router* router, const void* logits,
+                     int32_t logit_dtype, const float* bias, int32_t* topk_ids,
+                     float* topk_weights, void* stream) {
+  int v = validate_router(p, router);
+  if (v) return v;
+  if (logit_dtype != MOE_F32 && logit_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (!logits || !topk_ids || !topk_weights) return MOE_ERR_NULL;
+  if ((v = check_align({{logits, 4}, {bias, 4}, {topk_ids, 4}, {topk_weights, 4}}))) return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_route_scored(resolve(p), *router, logits, logit_dtype == MOE_BF16, bias,
+                                       topk_ids, topk_weights, (hipStream_t)stream));
+}
+
+int moe_route_scored_bwd(const moe_problem* p, const moe_router* router, const void* logits,
+                         int32_t logit_dtype, const int32_t* topk_ids, const float* d_weights,
+                         void* d_logits, void* stream) {
+  int v = validate_router(p, router);
+  if (v) return v;
+  if (logit_dtype != MOE_F32 && logit_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (!logits || !topk_ids || !d_weights || !d_logits) return MOE_ERR_NULL;
+  if ((v = check_align({{logits, 4}, {topk_ids, 4}, {d_weights, 4}, {d_logits, 4}}))) return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_route_scored_bwd(resolve(p), *router, logits, logit_dtype == MOE_BF16,
+                                           topk_ids, d_weights, d_logits, (hipStream_t)stream));
+}
+
+int moe_rms_norm(int32_t t, int32_t h, int32_t row_dtype, const void* x, const void* residual,
+                 const void* weight, float eps, void* sum, void* y, uint8_t* codes, float* scales,
+                 float* rstd, void* stream) {
+  int v = validate_norm(t, h);
+  if (v) return v;
+  if (row_dtype != MOE_F32 && row_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (!(eps >= 0.0f) || !(eps - eps == 0.0f) || ((codes || scales) && h % kGroup))
+    return MOE_ERR_SHAPE;
+  if (!x || !residual != !sum || !codes != !scales || (!y && !codes)) return MOE_ERR_NULL;
+  if ((v = check_align({{x, 16}, {residual, 16}, {weight, 16}, {sum, 16}, {y, 16}, {codes, 16},
+                        {scales, 16}, {rstd, 4}})))
+    return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_rms_norm(t, h, row_dtype == MOE_BF16, x, residual, weight, eps, sum, y,
+                                   codes, scales, rstd, (hipStream_t)stream));
+}
+
+int64_t moe_rms_norm_bwd_workspace_bytes(int32_t t, int32_t h) {
+  const int v = validate_norm(t, h);
+  return v ? v : norm_partial_bytes(t, h);
+}
+
+int moe_rms_norm_bwd(int32_t t, int32_t h, int32_t row_dtype, const void* d_y, const void* d_sum,
+                     const void* s, const void* weight, const float* rstd, void* d_x,
+                     float* d_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  int v = validate_norm(t, h);
+  if (v) return v;
+  if (row_dtype != MOE_F32 && row_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (!d_y || !s || !rstd || !d_x || (d_weight && !workspace)) return MOE_ERR_NULL;
+  if (d_weight && workspace_bytes < (size_t)norm_partial_bytes(t, h)) return MOE_ERR_WORKSPACE;
+  if ((v = check_align({{d_y, 16}, {d_sum, 16}, {s, 16}, {weight, 16}, {rstd, 4}, {d_x, 16},
+                        {d_weight, 16}, {workspace, 256}})))
+    return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_rms_norm_bwd(t, h, row_dtype == MOE_BF16, d_y, d_sum, s, weight, rstd,
+                                       d_x, d_weight, (float*)workspace, (hipStream_t)stream));
+}
+
+int moe_gemm_bf16(int32_t m, int32_t n, int32_t k, int32_t layout, const void* a, const void* b,
+                  const float* bias, int32_t act, const void* residual, void* pre, void* c,
+                  int32_t c_dtype, void* stream) {
+  int v = validate_act(m, n, act);
+  if (v) return v;
+  if (k < 1 || k > kGemmMaxDim ||
+      ((int64_t)m + 15) / 16 * (((int64_t)n + 15) / 16) > kMaxGemmTiles)
+    return MOE_ERR_SHAPE;
+  if (layout < MOE_NT || layout > MOE_TN) return MOE_ERR_SHAPE;
+  if (c_dtype != MOE_F32 && c_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (!a || !b || !c) return MOE_ERR_NULL;
+  if ((v = check_align({{a, 16}, {b, 16}, {bias, 4}, {residual, 16}, {pre, 16}, {c, 16}})))
+    return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_gemm_bf16({m, n, k, layout, act, a, b, bias, residual, pre, c,
+                                     c_dtype == MOE_F32}, (hipStream_t)stream));
+}
+
+int64_t moe_act_bwd_workspace_bytes(int32_t m, int32_t n) {
+  const int v = validate_act(m, n, MOE_ACT_NONE);
+  return v ? v : act_partial_bytes(m, n);
+}
+
+int moe_act_bwd(int32_t m, int32_t n, int32_t act, const void* d_c, const void* pre, void* d_z,
+                float* d_bias, void* workspace, size_t workspace_bytes, void* stream) {
+  int v = validate_act(m, n, act);
+  if (v) return v;
+  const bool none = act == MOE_ACT_NONE;
+  if (!d_c || none != !pre || none != !d_z || (none && !d_bias) || (d_bias && !workspace))
+    return MOE_ERR_NULL;
+  if (d_bias && workspace_bytes < (size_t)act_partial_bytes(m, n))
+    return MOE_ERR_WORKSPACE;
+  if ((v = check_align({{d_c, 16}, {pre, 16}, {d_z, 16}, {d_bias, 4}, {workspace, 256}}))) return v;
+  if ((v = check_device())) return v;
+  return status_of(launch_act_bwd(m, n, act, d_c, pre, d_z, d_bias, (float*)workspace,
+                                  (hipStream_t)stream));
 }
 
 int moe_forward(const moe_problem* p, const void* x, const int32_t* topk_ids,

@@ -36,6 +36,16 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
   return u >> 16;
 }
 
+// The same by gfx950's own conversion: nearest even, NaN stays NaN.
+__device__ __forceinline__ uint32_t f32_to_bf16(float f) {
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+__device__ __forceinline__ uint32_t f32_to_bf16x2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
 }
@@ -306,6 +316,46 @@ hipError_t launch_grouped_gemm_e4m3(const Resolved& r, int N, int K, const uint8
                                     const int32_t* offsets, const int32_t* tiles,
                                     const int32_t* num_tiles, void* out, bool out_f32,
                                     hipStream_t s);
+// Router with scores, bias and groups (moe_route_scored.hip).
+hipError_t launch_route_scored(const Resolved& r, const moe_router& q, const void* logits,
+                               bool bf16, const float* bias, int32_t* topk_ids, float* topk_w,
+                               hipStream_t s);
+hipError_t launch_route_scored_bwd(const Resolved& r, const moe_router& q, const void* logits,
+                                   bool bf16, const int32_t* topk_ids, const float* d_w,
+                                   void* d_logits, hipStream_t s);
+// Root-mean-square norm (moe_norm.hip) and its gradient, whose weight part leaves rows of partial
+// sums in `partials`.
+constexpr int kPartialRows = 512;   // of moe_rms_norm_bwd and moe_act_bwd, at most
+hipError_t launch_rms_norm(int T, int H, bool bf16, const void* x, const void* residual,
+                           const void* weight, float eps, void* sum, void* y, uint8_t* codes,
+                           float* scales, float* rstd, hipStream_t s);
+hipError_t launch_rms_norm_bwd(int T, int H, bool bf16, const void* d_y, const void* d_sum,
+                               const void* sum, const void* weight, const float* rstd, void* d_x,
+                               float* d_weight, float* partials, hipStream_t s);
+// out[c] = sum over r < rows, ascending, of partials[r, c].
+hipError_t launch_sum_rows(int rows, int cols, const float* partials, float* out, hipStream_t s);
+// bf16 products with an epilogue and the epilogue's gradient (moe_gemm_bf16.hip).
+constexpr int kMaxUnits = 1024;     // compute units that a launch counts on, at most
+constexpr int kActCols = 256;       // columns of a workgroup of the epilogue's gradient
+// Its rows of workgroups, and of partial sums: as many as fill the units eight times.
+inline int act_partial_rows(int M, int N, int cus) {
+  const int per_unit = (cus < kMaxUnits ? cus : kMaxUnits) * 8 / ((N + kActCols - 1) / kActCols);
+  int rows = (M + 3) / 4;
+  rows = rows < kPartialRows ? rows : kPartialRows;
+  rows = rows < per_unit ? rows : per_unit;
+  return rows > 1 ? rows : 1;
+}
+struct GemmBf16 {
+  int M, N, K, layout, act;
+  const void *a, *b;
+  const float* bias;
+  const void* residual;
+  void *pre, *c;
+  bool c_f32;
+};
+hipError_t launch_gemm_bf16(const GemmBf16& g, hipStream_t s);
+hipError_t launch_act_bwd(int M, int N, int act, const void* d_c, const void* pre, void* d_z,
+                          float* d_bias, float* partials, hipStream_t s);
 hipError_t launch_combine(const Resolved& r, const void* slot_out, const int32_t* slot_row,
                           void* out, hipStream_t s);
 

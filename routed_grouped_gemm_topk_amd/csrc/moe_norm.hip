@@ -1,0 +1,398 @@
+// Root-mean-square norm of token rows, with the residual's addition before it and rows and e4m3
+// codes as its outputs, and its gradient.
+//
+//   s = round(x + residual),  r = 1 / sqrt(mean s^2 + eps),  n = s r w
+//   y = round(n);  codes = e4m3(n / scale), scale = amax |n| / 448 over 128 columns
+//   d_x = r (g - n' mean(g n')) + d_sum,  d_w = sum over rows of d_y n',   n' = s r, g = d_y w
+//
+// HBM bounds both: every row is read once and stays in registers.  TPR threads share a row, each
+// with NV chunks of 8 neighbouring columns: chunk v of thread i begins at column (v TPR + i) 8, so
+// that 16 neighbouring lanes hold one scale group.
+#include <algorithm>
+#include <type_traits>
+
+#include "moe_internal.h"
+#include "moe_route.h"
+
+namespace moe {
+
+namespace nm {
+
+constexpr int kThreads = 256;     // of a workgroup, at least
+
+struct Args {
+  const void *x, *residual, *weight;
+  void *sum, *y;
+  uint8_t* codes;
+  float *scales, *rstd;
+  int T, H;
+  float eps;
+};
+
+// Eight neighbouring values of a row as they lie in memory, and as fp32.  VEC: rows are whole
+// 16-byte blocks; n: values of the chunk that the row has.
+template <bool BF16, bool VEC>
+struct Chunk {
+  static constexpr int W = BF16 ? 4 : 8;
+  uint32_t w[W];
+
+  __device__ __forceinline__ void load(const void* base, int64_t at, int n) {
+    #pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0;
+    if constexpr (VEC) {
+      if (n <= 0) return;
+      const i32x4* p = (const i32x4*)((const char*)base + at * (BF16 ? 2 : 4));
+      #pragma unroll
+      for (int q = 0; q < W / 4; ++q) {
+        const i32x4 v = p[q];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 * q + i] = (uint32_t)v[i];
+      }
+    } else if constexpr (BF16) {
+      const uint16_t* p = (const uint16_t*)base + at;
+      #pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+    } else {
+      const uint32_t* p = (const uint32_t*)base + at;
+      #pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) w[i] = p[i];
+    }
+  }
+  __device__ __forceinline__ void store(void* base, int64_t at, int n) const {
+    if constexpr (VEC) {
+      if (n <= 0) return;
+      i32x4* p = (i32x4*)((char*)base + at * (BF16 ? 2 : 4));
+      #pragma unroll
+      for (int q = 0; q < W / 4; ++q)
+        p[q] = i32x4{(int)w[4 * q], (int)w[4 * q + 1], (int)w[4 * q + 2], (int)w[4 * q + 3]};
+    } else if constexpr (BF16) {
+      uint16_t* p = (uint16_t*)base + at;
+      #pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    } else {
+      uint32_t* p = (uint32_t*)base + at;
+      #pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = w[i];
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (BF16)
+      return i & 1 ? __uint_as_float(w[i / 2] & 0xFFFF0000u) : __uint_as_float(w[i / 2] << 16);
+    else
+      return __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ void set(const float* v) {
+    #pragma unroll
+    for (int i = 0; i < W; ++i)
+      w[i] = BF16 ? f32_to_bf16x2(v[BF16 ? 2 * i : i], v[BF16 ? 2 * i + 1 : i])
+                  : __float_as_uint(v[i]);
+  }
+};
+
+// Sum over the TPR threads of a row, the same on each: lanes first, then waves in their order.
+// Every wave of the workgroup calls it as often; `turn` picks one of two sets of LDS words, so that
+// one barrier per call is enough.
+template <int TPR, class V>
+__device__ __forceinline__ V row_sum(V v, V (*words)[TPR / kWave], int turn) {
+  #pragma unroll
+  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d, kWave);
+  if constexpr (TPR > kWave) {
+    const int wave = threadIdx.x / kWave;
+    if ((threadIdx.x & (kWave - 1)) == 0) words[turn][wave] = v;
+    __syncthreads();
+    v = words[turn][0];
+    #pragma unroll
+    for (int i = 1; i < TPR / kWave; ++i) v += words[turn][i];
+  }
+  return v;
+}
+
+template <int TPR, int NV, bool BF16, bool VEC>
+__global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kernel(Args g) {
+  constexpr int ROWS = TPR < kThreads ? kThreads / TPR : 1;      // of a workgroup
+  using Row = Chunk<BF16, VEC>;
+  __shared__ double words[2][TPR / kWave];
+  const int i = ROWS > 1 ? threadIdx.x % TPR : threadIdx.x;
+  const int in_row = ROWS > 1 ? threadIdx.x / TPR : 0;
+  Row w[NV];
+  int n[NV];
+  #pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    n[v] = g.H - (v * TPR + i) * 8;
+    if (g.weight) w[v].load(g.weight, (v * TPR + i) * 8, n[v]);
+  }
+  int turn = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < g.T; row0 += (int64_t)gridDim.x * ROWS) {
+    const int64_t row = row0 + in_row;
+    const bool live = row < g.T;                       // the same for a whole wave
+    const int64_t at = row * g.H + i * 8;
+    Row x[NV];
+    if (live) {
+      #pragma unroll
+      for (int v = 0; v < NV; ++v) x[v].load(g.x, at + v * TPR * 8, n[v]);
+      if (g.residual) {
+        Row r[NV];
+        #pragma unroll
+        for (int v = 0; v < NV; ++v) r[v].load(g.residual, at + v * TPR * 8, n[v]);
+        #pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          float s[8];
+          #pragma unroll
+          for (int k = 0; k < 8; ++k) s[k] = x[v].get(k) + r[v].get(k);
+          x[v].set(s);
+          x[v].store(g.sum, at + v * TPR * 8, n[v]);
+        }
+      }
+    } else {
+      #pragma unroll
+      for (int v = 0; v < NV; ++v) x[v] = Row{};
+    }
+    // squares of fp32 values neither overflow nor vanish in 64 bits
+    double sq = 0.0;
+    #pragma unroll
+    for (int v = 0; v < NV; ++v)
+      #pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const double s = x[v].get(k);
+        sq = __builtin_fma(s, s, sq);
+      }
+    sq = row_sum<TPR>(sq, words, turn);
+    turn ^= 1;
+    if (!live) continue;
+    const float rstd = (float)rsqrt(sq / (double)g.H + (double)g.eps);
+    if (g.rstd && i == 0) g.rstd[row] = rstd;
+    #pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float y[8];
+      #pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        y[k] = x[v].get(k) * rstd;
+        if (g.weight) y[k] *= w[v].get(k);
+      }
+      if (g.y) {
+        Row o;
+        o.set(y);
+        o.store(g.y, at + v * TPR * 8, n[v]);
+      }
+      if (VEC && g.codes) {
+        float m = 0.0f;
+        #pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(y[k]));
+        // 16 lanes hold a group
+        m = fmaxf(m, dpp_xchg<0xB1>(m));
+        m = fmaxf(m, dpp_xchg<0x4E>(m));
+        m = fmaxf(m, dpp_xchg<0x141>(m));
+        m = fmaxf(m, dpp_xchg<0x140>(m));
+        const float s = m == 0.0f ? 1.0f : m / kE4M3Max;
+        if (n[v] > 0) {
+          // quotients are at most 448 up to their rounding, below the 464 from which e4m3 would
+          // overflow, so the convert (nearest even, NaN kept) needs no clamp
+          uint32_t q[2];
+          #pragma unroll
+          for (int h = 0; h < 2; ++h)
+            q[h] = __builtin_amdgcn_cvt_pk_fp8_f32(
+                y[4 * h + 2] / s, y[4 * h + 3] / s,
+                __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h] / s, y[4 * h + 1] / s, 0, false), true);
+          *(uint2*)(g.codes + at + v * TPR * 8) = make_uint2(q[0], q[1]);
+          if ((i & 15) == 0) g.scales[row * (g.H / kGroup) + (v * TPR + i) / 16] = s;
+        }
+      }
+    }
+  }
+}
+
+struct BwdArgs {
+  const void *d_y, *d_sum, *sum, *weight;
+  const float* rstd;
+  void* d_x;
+  float* partials;              // [gridDim.x, H], or null: no gradient of the weight
+  int T, H;
+};
+
+// A workgroup takes every gridDim.x-th set of rows and keeps its part of d_w in registers; its rows
+// (one per wave where TPR is a wave) are added through LDS at the end, then one row of partials.
+template <int TPR, int NV, bool BF16, bool VEC>
+__global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_bwd_kernel(BwdArgs g) {
+  constexpr int ROWS = TPR < kThreads ? kThreads / TPR : 1;
+  using Row = Chunk<BF16, VEC>;
+  __shared__ float words[2][TPR / kWave];
+  __shared__ float part[ROWS > 1 ? ROWS * TPR * 8 : 1];
+  const int i = ROWS > 1 ? threadIdx.x % TPR : threadIdx.x;
+  const int in_row = ROWS > 1 ? threadIdx.x / TPR : 0;
+  Row w[NV];
+  int n[NV];
+  float dw[NV][8];
+  #pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    n[v] = g.H - (v * TPR + i) * 8;
+    if (g.weight) w[v].load(g.weight, (v * TPR + i) * 8, n[v]);
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) dw[v][k] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < g.T; row0 += (int64_t)gridDim.x * ROWS) {
+    const int64_t row = row0 + in_row;
+    const bool live = row < g.T;
+    const int64_t at = row * g.H + i * 8;
+    Row dy[NV], s[NV], ds[NV];
+    float r = 0.0f;
+    if (live) {
+      r = g.rstd[row];
+      #pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        dy[v].load(g.d_y, at + v * TPR * 8, n[v]);
+        s[v].load(g.sum, at + v * TPR * 8, n[v]);
+        if (g.d_sum) ds[v].load(g.d_sum, at + v * TPR * 8, n[v]);
+      }
+    } else {
+      #pragma unroll
+      for (int v = 0; v < NV; ++v) dy[v] = s[v] = Row{};
+    }
+    float dot = 0.0f;
+    #pragma unroll
+    for (int v = 0; v < NV; ++v)
+      #pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float d = dy[v].get(k), norm = s[v].get(k) * r;
+        dw[v][k] = __builtin_fmaf(d, norm, dw[v][k]);
+        dot = __builtin_fmaf(g.weight ? d * w[v].get(k) : d, norm, dot);
+      }
+    dot = row_sum<TPR>(dot, words, turn) / (float)g.H;
+    turn ^= 1;
+    if (!live) continue;
+    #pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float d[8];
+      #pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float gk = g.weight ? dy[v].get(k) * w[v].get(k) : dy[v].get(k);
+        d[k] = r * (gk - s[v].get(k) * r * dot);
+        if (g.d_sum) d[k] += ds[v].get(k);
+      }
+      Row o;
+      o.set(d);
+      o.store(g.d_x, at + v * TPR * 8, n[v]);
+    }
+  }
+  if (!g.partials) return;
+  float* out = g.partials + (int64_t)blockIdx.x * g.H;
+  #pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if constexpr (ROWS > 1) {
+      __syncthreads();
+      #pragma unroll
+      for (int k = 0; k < 8; ++k) part[(in_row * TPR + i) * 8 + k] = dw[v][k];
+      __syncthreads();
+      for (int c = threadIdx.x; c < TPR * 8; c += kThreads) {
+        float t = part[c];
+        #pragma unroll
+        for (int q = 1; q < ROWS; ++q) t += part[q * TPR * 8 + c];
+        if (v * TPR * 8 + c < g.H) out[v * TPR * 8 + c] = t;
+      }
+    } else {
+      #pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n[v]) out[(v * TPR + i) * 8 + k] = dw[v][k];
+    }
+  }
+}
+
+// 64 columns a workgroup; its 16 waves take 16 neighbouring stretches of the rows.
+constexpr int kSumWaves = 16;
+
+__global__ __launch_bounds__(kSumWaves * kWave) void sum_rows_kernel(
+    const float* __restrict__ partials, float* __restrict__ out, int rows, int cols) {
+  __shared__ float part[kSumWaves][kWave];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int64_t c = (int64_t)blockIdx.x * kWave + lane;
+  const int per = (rows + kSumWaves - 1) / kSumWaves;
+  float t = 0.0f;
+  if (c < cols)
+    for (int r = wave * per; r < min(rows, (wave + 1) * per); ++r) t += partials[(int64_t)r * cols + c];
+  part[wave][lane] = t;
+  __syncthreads();
+  if (wave > 0 || c >= cols) return;
+  #pragma unroll
+  for (int w = 1; w < kSumWaves; ++w) t += part[w][lane];
+  out[c] = t;
+}
+
+// Calls f(TPR, NV, VEC) as compile-time constants for rows of H values.
+template <class F>
+hipError_t by_width(int T, int H, F f) {
+  using std::integral_constant;
+  const bool vec = H % 8 == 0;
+  auto with = [&](auto tpr, auto nv) {
+    return vec ? f(tpr, nv, std::true_type{}) : f(tpr, nv, std::false_type{});
+  };
+  const integral_constant<int, 1> one{};
+  const integral_constant<int, 2> two{};
+  const integral_constant<int, 4> four{};
+  const integral_constant<int, 64> wave{};
+  const integral_constant<int, 256> four_waves{};
+  const integral_constant<int, 1024> all{};
+  if (H <= 512) return with(wave, one);
+  if (H <= 1024) return with(wave, two);
+  if (H <= 2048) return with(four_waves, one);
+  if (H <= 4096) return with(four_waves, two);
+  if (H <= 8192) return with(all, one);
+  if (H <= 16384) return with(all, two);
+  return with(all, four);
+}
+
+}  // namespace nm
+
+hipError_t launch_rms_norm(int T, int H, bool bf16, const void* x, const void* residual,
+                           const void* weight, float eps, void* sum, void* y, uint8_t* codes,
+                           float* scales, float* rstd, hipStream_t s) {
+  nm::Args a{x, residual, weight, sum, y, codes, scales, rstd, T, H, eps};
+  const int cus = std::max(device_cu_count(), 8);
+  return nm::by_width(T, H, [&](auto tpr, auto nv, auto vec) {
+    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    constexpr bool VEC = decltype(vec)::value;
+    constexpr int TH = std::max(TPR, nm::kThreads), ROWS = TH / TPR;
+    const int64_t sets = ((int64_t)T + ROWS - 1) / ROWS;
+    const unsigned grid = (unsigned)std::min<int64_t>(sets, (int64_t)cus * (2048 / TH) * 2);
+    if (bf16)
+      hipLaunchKernelGGL((nm::rms_norm_kernel<TPR, NV, true, VEC>), dim3(grid), dim3(TH), 0, s, a);
+    else
+      hipLaunchKernelGGL((nm::rms_norm_kernel<TPR, NV, false, VEC>), dim3(grid), dim3(TH), 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_sum_rows(int rows, int cols, const float* partials, float* out, hipStream_t s) {
+  hipLaunchKernelGGL(nm::sum_rows_kernel, dim3((unsigned)((cols + kWave - 1) / kWave)),
+                     dim3(nm::kSumWaves * kWave), 0, s, partials, out, rows, cols);
+  return hipGetLastError();
+}
+
+hipError_t launch_rms_norm_bwd(int T, int H, bool bf16, const void* d_y, const void* d_sum,
+                               const void* sum, const void* weight, const float* rstd, void* d_x,
+                               float* d_weight, float* partials, hipStream_t s) {
+  nm::BwdArgs a{d_y, d_sum, sum, weight, rstd, d_x, d_weight ? partials : nullptr, T, H};
+  const int cus = std::max(device_cu_count(), 8);
+  unsigned grid = 0;
+  const hipError_t e = nm::by_width(T, H, [&](auto tpr, auto nv, auto vec) {
+    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    constexpr bool VEC = decltype(vec)::value;
+    constexpr int TH = std::max(TPR, nm::kThreads), ROWS = TH / TPR;
+    const int64_t sets = ((int64_t)T + ROWS - 1) / ROWS;
+    grid = (unsigned)std::min<int64_t>(std::min<int64_t>(sets, 2 * cus), kPartialRows);
+    if (bf16)
+      hipLaunchKernelGGL((nm::rms_norm_bwd_kernel<TPR, NV, true, VEC>), dim3(grid), dim3(TH), 0, s,
+                         a);
+    else
+      hipLaunchKernelGGL((nm::rms_norm_bwd_kernel<TPR, NV, false, VEC>), dim3(grid), dim3(TH), 0, s,
+                         a);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || !d_weight) return e;
+  return launch_sum_rows((int)grid, H, partials, d_weight, s);
+}
+
+}  // namespace moe
