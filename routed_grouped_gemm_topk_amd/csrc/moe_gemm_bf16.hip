@@ -7,7 +7,9 @@
 // Accumulated in fp32 by the bf16 matrix instructions.  The operand order puts b on a result's rows
 // and a on its columns, so a lane holds 4 neighbouring columns of ONE row of c.
 #include <algorithm>
+#include <type_traits>
 
+#include "moe_gemm_bf16_choice.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -122,6 +124,498 @@ hipError_t run_any(const Args& g, int layout, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------------------------
+// Rows of whole 16-byte blocks
+// ---------------------------------------------------------------------------------------------
+constexpr int ROWB = 128;       // bytes of a row of LDS
+constexpr int kGroupM = 8;      // m-blocks that sweep the n-blocks together
+
+// One tile of c: rows [m0, m0 + rows) x columns [n0, n0 + cols).
+struct Tile {
+  int64_t m0;
+  int n0, rows, cols;
+};
+
+// Tile `logical` of the product: groups of kGroupM m-blocks sweep the n-blocks.
+template <int BM, int BN>
+__device__ __forceinline__ Tile tile_at(const Args& g, int logical) {
+  const int mblk = (g.M + BM - 1) / BM, nblk = (g.N + BN - 1) / BN;
+  const int grp = logical / (kGroupM * nblk);
+  const int gm = min(kGroupM, mblk - grp * kGroupM);
+  const int w = logical - grp * kGroupM * nblk;
+  Tile t;
+  t.m0 = (int64_t)(grp * kGroupM + w % gm) * BM;
+  t.n0 = w / gm * BN;
+  t.rows = (int)min((int64_t)BM, (int64_t)g.M - t.m0);
+  t.cols = min(BN, g.N - t.n0);
+  return t;
+}
+
+// Eight values of a row of c, rows being whole 16-byte blocks.
+struct Eight {
+  i32x4 lo, hi;                 // hi: fp32 only
+  __device__ __forceinline__ float get(int i, bool f32) const {
+    if (f32) return __int_as_float(i < 4 ? lo[i] : hi[i - 4]);
+    const uint32_t w = (uint32_t)lo[i / 2];
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+};
+__device__ __forceinline__ Eight load8(const void* p, int64_t at, bool f32) {
+  Eight e;
+  if (f32) {
+    e.lo = *(const i32x4*)((const float*)p + at);
+    e.hi = *(const i32x4*)((const float*)p + at + 4);
+  } else {
+    e.lo = *(const i32x4*)((const uint16_t*)p + at);
+    e.hi = i32x4{0, 0, 0, 0};
+  }
+  return e;
+}
+__device__ __forceinline__ i32x4 pack8(const float* v) {
+  return i32x4{(int)f32_to_bf16x2(v[0], v[1]), (int)f32_to_bf16x2(v[2], v[3]),
+               (int)f32_to_bf16x2(v[4], v[5]), (int)f32_to_bf16x2(v[6], v[7])};
+}
+__device__ __forceinline__ void finish8(const Args& g, const f32x4& z0, const f32x4& z1, int64_t at,
+                                        int n, const Eight& res) {
+  float z[8] = {z0[0], z0[1], z0[2], z0[3], z1[0], z1[1], z1[2], z1[3]};
+  if (g.bias) {
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += g.bias[n + i];
+  }
+  if (g.pre) *(i32x4*)(g.pre + at) = pack8(z);
+  if (g.act != MOE_ACT_NONE) {
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = activate(z[i], g.act);
+  }
+  if (g.residual) {
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += res.get(i, g.c_f32);
+  }
+  if (g.c_f32) {
+    f32x4* to = (f32x4*)((float*)g.c + at);
+    to[0] = f32x4{z[0], z[1], z[2], z[3]};
+    to[1] = f32x4{z[4], z[5], z[6], z[7]};
+  } else {
+    *(i32x4*)((uint16_t*)g.c + at) = pack8(z);
+  }
+}
+
+// BM x BN tile by WM x WN waves; slices of 64 values of k of both operands in a ring of NS LDS
+// stages, copied by direct-to-LDS loads NS-1 steps ahead.  KG groups of WM x WN waves take every
+// KG-th slice each and their sums are added at the end in the order of the groups.
+//
+// KA, KB: k is the contiguous dimension of the operand.  Then a stage holds its rows, 128 bytes of k
+// each, chunk c of row r at c ^ swz(r).  Otherwise it holds panels of 64 columns, each 64 rows of k
+// of 128 bytes, and the fragments are read with the transposing LDS load: 16 lanes name 4 rows of
+// k times 16 columns, and each receives one column's 4 values.  Half a wave reads rows k of
+// {0-3, 16-19} (+ 4, 8, 12, 32 ...), whose pairs of chunks lie at c ^ 2 f with f = bit 1 of k and twice
+// bit 4 of k: all on different banks.  A lane's values of k are those of the other form: matrix
+// instruction t of a slice takes k = 16 (lane / 16) + 8 t + 0..7 of every lane.
+template <int BM, int BN, int WM, int WN, int KG, int NS, bool KA, bool KB>
+struct TileGemm {
+  static constexpr int NW = WM * WN;
+  static constexpr int WTM = BM / WM, WTN = BN / WN;        // a wave's part of the tile
+  static constexpr int FM = WTM / 16, FN = WTN / 16;
+  static constexpr int NQ_REAL = (BM + BN) / 8;             // 1 KB copies per slice
+  static constexpr int NQ = (NQ_REAL + NW - 1) / NW * NW;
+  static constexpr int NQW = NQ / NW;
+  static constexpr int STAGE = NQ * 1024;
+  static constexpr int RING = NS * KG * STAGE;
+  static constexpr int SUMS = (KG - 1) * NW * FM * FN * kWave * 16;
+  static constexpr int PITCH = WTN * 4 + 16;
+  static constexpr int OUTF = FM < 4 ? FM : 4;              // fragments turned around at a time
+  static constexpr int OUT_OFF = KG > 1 ? SUMS : 0;
+  static constexpr int OUT = OUT_OFF + NW * OUTF * 16 * PITCH;
+  static constexpr int LDS = RING > OUT ? RING : OUT;
+  // A slice's copies go out in parts: PART of each wave right after the barrier that frees the
+  // stage, PART more before each of the next slice's fragments.
+  static constexpr int PART = NS == 2 && FM >= 4 ? std::max(2, (NQW + FM - 1) / FM) : NQW;
+  static_assert(WTM % 16 == 0 && WTN % 16 == 0 && FM % OUTF == 0, "whole fragments");
+  static_assert(KA || (BM % 64 == 0 && (WTM % 64 == 0 || 64 % WTM == 0)), "whole panels");
+  static_assert(KB || (BN % 64 == 0 && (WTN % 64 == 0 || 64 % WTN == 0)), "whole panels");
+  static_assert(BM % 8 == 0 && (KA || BM / 8 % 8 == 0), "whole copies");
+  static_assert(NS >= 2 && (NS - 1) * NQW <= 63, "vmcnt range");
+  static_assert(LDS <= 160 * 1024, "LDS");
+  static_assert((NQW + PART - 1) / PART <= FM, "every part goes out within its slice");
+
+  // Where a lane finds a wave's fragments of an operand in a stage.
+  template <bool KC, int WT, int F>
+  struct Where {
+    static constexpr int NADDR = KC ? 2 : (F < 4 ? F : 4);
+    uint32_t at[NADDR];
+    __device__ __forceinline__ void init(uint32_t base, int w, int lane) {
+      const int fr = lane & 15, fq = lane >> 4;
+      if constexpr (KC) {
+        #pragma unroll
+        for (int t = 0; t < 2; ++t)
+          at[t] = base + (w * WT + fr) * ROWB + (((2 * fq + t) ^ swz(fr)) << 4);
+      } else {
+        const int k = fq * 16 + (fr >> 2);
+        const int f = ((k >> 1) & 1) | ((k >> 4) & 1) << 1;
+        const int c0 = w * WT / 16;                    // the wave's first 16 columns
+        #pragma unroll
+        for (int v = 0; v < NADDR; ++v) {
+          const int pair = ((c0 + v) & 3) ^ f;
+          at[v] = base + (c0 / 4) * 64 * ROWB + k * ROWB +
+                  ((2 * pair + ((fr >> 1) & 1)) << 4) + (fr & 1) * 8;
+        }
+      }
+    }
+    __device__ __forceinline__ void step(uint32_t d) {
+      #pragma unroll
+      for (int v = 0; v < NADDR; ++v) at[v] += d;
+    }
+    __device__ __forceinline__ bf16x8 read(const char* lds, int i, int t) const {
+      if constexpr (KC) {
+        return *reinterpret_cast<const bf16x8*>(lds + at[t] + i * 16 * ROWB);
+      } else {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        using Shared = __attribute__((address_space(3))) bf16x4;
+        const char* p = lds + at[i % NADDR] + (i / 4) * 64 * ROWB + t * 8 * ROWB;
+        const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Shared*)p);
+        const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Shared*)(p + 4 * ROWB));
+        return bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      }
+    }
+  };
+
+  __device__ static __forceinline__ void run(const Args& g, const Tile& t, char* lds) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int kg = all / NW, wave = all % NW;                // group, and wave of the group
+    const int wn = wave % WN, wm = wave / WN;
+    const int K = g.K, KT = (K + kSlice - 1) / kSlice, steps = (KT + KG - 1) / KG;
+
+    // ---- this wave's copies.  Offsets past a descriptor's end read as zeros: rows past the
+    // operand's last, k past K (in the last slice, and in slices past it, which the ring and the
+    // k-groups run into) ------------------------------------------------------------------------
+    const i32x4 ra = buf_rsrc(g.a + (size_t)t.m0 * K, (uint32_t)t.rows * (uint32_t)K * 2);
+    const i32x4 rb = buf_rsrc(g.b + (size_t)t.n0 * K, (uint32_t)t.cols * (uint32_t)K * 2);
+    // the descriptor of 64 rows of k of an operand whose rows are k
+    auto rows_of_k = [&](const uint16_t* p, int ld, int64_t first, int kt) {
+      const int left = min(max(K - kt * kSlice, 0), kSlice);
+      return buf_rsrc(p + (size_t)min(kt, KT) * kSlice * ld + first,
+                      left > 0 ? (uint32_t)(left * (int64_t)ld - first) * 2 : 0u);
+    };
+    const int kc = ((lane & 7) ^ (lane >> 3)) * 8;           // k of the lane's chunk, even copies
+    uint32_t voff[NQW];
+    #pragma unroll
+    for (int i = 0; i < NQW; ++i) {
+      const int q = wave * NQW + i;
+      const bool is_a = q < BM / 8;
+      const int qo = is_a ? q : q - BM / 8;
+      uint32_t v;
+      if (is_a ? KA : KB) {
+        v = (uint32_t)(qo * 8 + (lane >> 3)) * (uint32_t)K * 2 + (uint32_t)(kc ^ ((q & 1) * 8)) * 2;
+      } else {
+        const int k = (qo & 7) * 8 + (lane >> 3);
+        const int f = ((k >> 1) & 1) | ((k >> 4) & 1) << 1;
+        v = (uint32_t)k * (uint32_t)(is_a ? g.M : g.N) * 2 + (qo >> 3) * ROWB +
+            (((lane & 7) ^ (2 * f)) << 4);
+      }
+      voff[i] = q < NQ_REAL ? v : kPastEnd;
+    }
+    const uint32_t lds_base = lds_u32(lds);
+    // part p of the group's slice of `step` into stage buf
+    auto issue = [&](int buf, int step, int p) {
+      const int kt = step * KG + kg;
+      const uint32_t st = __builtin_amdgcn_readfirstlane(lds_base + (buf * KG + kg) * STAGE);
+      const int left = K - kt * kSlice;
+      i32x4 sa = ra, sb = rb;
+      if constexpr (!KA) sa = rows_of_k(g.a, g.M, t.m0, kt);
+      if constexpr (!KB) sb = rows_of_k(g.b, g.N, t.n0, kt);
+      auto copies = [&](auto tail) {
+        #pragma unroll
+        for (int i = 0; i < NQW; ++i) {
+          if (i / PART != p) continue;
+          const int q = wave * NQW + i;
+          const bool is_a = q < BM / 8;
+          uint32_t v = voff[i];
+          const bool contiguous = is_a ? KA : KB;
+          if (decltype(tail)::value && contiguous && (kc ^ ((q & 1) * 8)) >= left) v = kPastEnd;
+          buf_dma16(is_a ? sa : sb, v, contiguous ? (uint32_t)kt * ROWB : 0u, st + q * 1024);
+        }
+      };
+      if ((KA || KB) && left < kSlice) copies(std::true_type{});
+      else copies(std::false_type{});
+    };
+
+    Where<KA, WTM, FM> wa;
+    Where<KB, WTN, FN> wb;
+    wa.init(kg * STAGE, wm, lane);
+    wb.init(kg * STAGE + BM * ROWB, wn, lane);
+
+    f32x4 acc[FM][FN];
+    #pragma unroll
+    for (int i = 0; i < FM; ++i)
+      #pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // Software pipeline over a's fragments: while the products of fragment i run, fragment i+1 is
+    // read.  The barrier of a slice sits before its last fragment's products: every wave has read
+    // all of the slice by then, so its stage is refilled (slice kt + NS) and those products cover
+    // the first reads of slice kt+1.
+    bf16x8 bf[FN][2], af[2][2];
+    auto read_a = [&](int i, bf16x8* f) {
+      #pragma unroll
+      for (int h = 0; h < 2; ++h) f[h] = wa.read(lds, i, h);
+    };
+    auto read_b = [&](int j) {
+      #pragma unroll
+      for (int h = 0; h < 2; ++h) bf[j][h] = wb.read(lds, j, h);
+    };
+    int buf = 0;
+    auto slice = [&](auto par, int step) {
+      constexpr int P = decltype(par)::value * FM;     // fragments of the slices before, mod 2
+      const int nbuf = (buf + 1 == NS) ? 0 : buf + 1;
+      const int pbuf = (buf == 0) ? NS - 1 : buf - 1;
+      #pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int c = (P + i) & 1;                     // this fragment's set
+        if (i + 1 < FM) {
+          read_a(i + 1, af[c ^ 1]);
+          if ((i + 1) * PART < NQW) issue(pbuf, step - 1 + NS, i + 1);
+        } else {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          wait_vmcnt<(NS - 2) * NQW>();                // this wave's copies of the next slice
+          __builtin_amdgcn_s_barrier();
+          issue(buf, step + NS, 0);
+          const uint32_t d = (uint32_t)((nbuf - buf) * KG * STAGE);
+          wa.step(d);
+          wb.step(d);
+          read_a(0, af[c ^ 1]);
+        }
+        #pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          #pragma unroll
+          for (int h = 0; h < 2; ++h) acc[i][j] = OpBf16::mma(bf[j][h], af[c][h], acc[i][j]);
+          if (i + 1 == FM) read_b(j);
+        }
+      }
+      buf = nbuf;
+    };
+    // slices 0..NS-2 whole and the first part of slice NS-1; slice 0 has to have landed
+    #pragma unroll
+    for (int s = 0; s < NS - 1; ++s)
+      #pragma unroll
+      for (int p = 0; p * PART < NQW; ++p) issue(s, s, p);
+    issue(NS - 1, NS - 1, 0);
+    wait_vmcnt<(NS - 2) * NQW + (PART < NQW ? PART : NQW)>();
+    __syncthreads();
+    read_a(0, af[0]);
+    #pragma unroll
+    for (int j = 0; j < FN; ++j) read_b(j);
+    using Even = std::integral_constant<int, 0>;
+    using Odd = std::integral_constant<int, 1>;
+    int step = 0;
+    for (; step + 1 < steps; step += 2) {
+      slice(Even{}, step);
+      slice(Odd{}, step + 1);
+    }
+    if (step < steps) slice(Even{}, step);
+    wait_vmcnt<0>();
+
+    __syncthreads();              // the ring is done with
+    if constexpr (KG > 1) {
+      f32x4* sums = reinterpret_cast<f32x4*>(lds);
+      auto at = [&](int g_, int i, int j) {
+        return (((g_ - 1) * NW + wave) * FM * FN + i * FN + j) * kWave + lane;
+      };
+      if (kg > 0) {
+        #pragma unroll
+        for (int i = 0; i < FM; ++i)
+          #pragma unroll
+          for (int j = 0; j < FN; ++j) sums[at(kg, i, j)] = acc[i][j];
+      }
+      __syncthreads();
+      if (kg > 0) return;
+      #pragma unroll
+      for (int g_ = 1; g_ < KG; ++g_)
+        #pragma unroll
+        for (int i = 0; i < FM; ++i)
+          #pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] += sums[at(g_, i, j)];
+    }
+
+    // ---- c: lane holds row lane & 15 of a, columns (lane >> 4) * 4 + v.  Each wave turns its
+    // fragments around in its part of LDS, OUTF of them at a time, in fp32, and finishes 8
+    // neighbouring columns of a row a lane, or, where rows of c are no whole 16-byte blocks, one
+    // column a lane -----------------------------------------------------------------------------
+    const int fr = lane & 15, fq = lane >> 4;
+    char* mine = lds + OUT_OFF + wave * OUTF * 16 * PITCH;
+    const int m_w = wm * WTM, n_w = wn * WTN;
+    #pragma unroll
+    for (int i0 = 0; i0 < FM; i0 += OUTF) {
+      #pragma unroll
+      for (int i = 0; i < OUTF; ++i)
+        #pragma unroll
+        for (int j = 0; j < FN; ++j)
+          *reinterpret_cast<f32x4*>(mine + (i * 16 + fr) * PITCH + (j * 16 + fq * 4) * 4) =
+              acc[i0 + i][j];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (g.N % 8 == 0) {
+        constexpr int VPR = WTN / 8, RPP = kWave / VPR < 16 ? kWave / VPR : 16;
+        constexpr int TURNS = OUTF * 16 / RPP;
+        const int c = lane % VPR * 8, n = n_w + c;
+        const bool in_n = lane < RPP * VPR && n < t.cols;
+        #pragma unroll 2
+        for (int u = 0; u < TURNS; ++u) {
+          const int r = u * RPP + lane / VPR, m = m_w + i0 * 16 + r;
+          if (!in_n || m >= t.rows) continue;
+          const int64_t at = (t.m0 + m) * (int64_t)g.N + t.n0 + n;
+          Eight res{};
+          if (g.residual) res = load8(g.residual, at, g.c_f32);
+          const f32x4* z = reinterpret_cast<const f32x4*>(mine + r * PITCH + c * 4);
+          finish8(g, z[0], z[1], at, t.n0 + n, res);
+        }
+      } else {
+        constexpr int VPR = WTN < kWave ? WTN : kWave, RPP = kWave / VPR;
+        #pragma unroll 2
+        for (int u = 0; u < OUTF * 16 / RPP; ++u) {
+          const int r = u * RPP + lane / VPR, m = m_w + i0 * 16 + r;
+          #pragma unroll
+          for (int c0 = 0; c0 < WTN; c0 += VPR) {
+            const int c = c0 + lane % VPR, n = n_w + c;
+            if (m >= t.rows || n >= t.cols) continue;
+            const float z = *reinterpret_cast<const float*>(mine + r * PITCH + c * 4);
+            finish<1>(g, &z, t.m0 + m, t.n0 + n, 1);
+          }
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+  }
+};
+
+template <int BM, int BN, int WM, int WN, int KG, int NS, int WPS, bool KA, bool KB>
+__global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void tile_kernel(Args g) {
+  using G = TileGemm<BM, BN, WM, WN, KG, NS, KA, KB>;
+  __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
+  const int mblk = (g.M + BM - 1) / BM, nblk = (g.N + BN - 1) / BN;
+  const int logical = xcd_chunked<kChunk>(blockIdx.x, mblk * nblk);
+  if (logical < 0) return;
+  G::run(g, tile_at<BM, BN>(g, logical), lds);
+}
+
+// Few rows of a (up to 16), a b^T: what counts is how fast b streams from HBM.  A workgroup takes
+// 16 * FN rows of b and its NW waves take every NW-th slice, straight from memory into the matrix
+// instructions' registers: no value of b is used twice, so LDS would only add a stop, and cutting K
+// over the waves keeps the workgroups as many as N / (16 * FN) with the bytes in flight of NW waves
+// each.  The waves' sums are added through LDS in the order of the waves.
+template <int FN, int NW, int U>
+__global__ __launch_bounds__(NW * kWave) void stream_kernel(Args g) {
+  constexpr int BN = 16 * FN;
+  __shared__ __attribute__((aligned(16))) f32x4 sums[NW * FN * kWave];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int K = g.K, KT = (K + kSlice - 1) / kSlice;
+  const int fr = lane & 15, fq = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * BN;
+  // rows past the operands' ends read the last row, their products are not stored
+  const uint16_t *pa = g.a + (size_t)min(fr, g.M - 1) * K + fq * 8, *pb[FN];
+  #pragma unroll
+  for (int j = 0; j < FN; ++j)
+    pb[j] = g.b + (size_t)min(n0 + j * 16 + fr, (int64_t)g.N - 1) * K + fq * 8;
+  struct Slice {                // one slice in registers
+    bf16x8 a[2], b[FN][2];
+  };
+  auto load = [&](Slice& s, int kt) {
+    #pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = kt * kSlice + h * 32;
+      const bf16x8 none = {};
+      const bool in = k + fq * 8 < K;
+      s.a[h] = in ? *reinterpret_cast<const bf16x8*>(pa + k) : none;
+      #pragma unroll
+      for (int j = 0; j < FN; ++j)
+        s.b[j][h] = in ? *reinterpret_cast<const bf16x8*>(pb[j] + k) : none;
+    }
+  };
+  f32x4 acc[FN] = {};
+  // U slices are in flight while the U before them are multiplied
+  Slice cur[U], nxt[U];
+  int kt = wave;
+  #pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (kt + u * NW < KT) load(cur[u], kt + u * NW);
+  for (; kt < KT; kt += U * NW) {
+    #pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (kt + (U + u) * NW < KT) load(nxt[u], kt + (U + u) * NW);
+    #pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (kt + u * NW < KT) {
+        #pragma unroll
+        for (int h = 0; h < 2; ++h)
+          #pragma unroll
+          for (int j = 0; j < FN; ++j) acc[j] = OpBf16::mma(cur[u].b[j][h], cur[u].a[h], acc[j]);
+      }
+    #pragma unroll
+    for (int u = 0; u < U; ++u) cur[u] = nxt[u];
+  }
+  #pragma unroll
+  for (int j = 0; j < FN; ++j) sums[(wave * FN + j) * kWave + lane] = acc[j];
+  __syncthreads();
+  for (int j = wave; j < FN; j += NW) {
+    f32x4 c = sums[j * kWave + lane];
+    #pragma unroll
+    for (int w = 1; w < NW; ++w) c += sums[(w * FN + j) * kWave + lane];
+    const int64_t n = n0 + j * 16 + fq * 4;
+    const float v[4] = {c[0], c[1], c[2], c[3]};
+    if (fr < g.M && n < g.N) finish<4>(g, v, fr, (int)n, g.N - (int)n);
+  }
+}
+
+// The kernels of these tiles, as moe_gemm_bf16_choice.h knows them.
+template <int BM, int BN, int THREADS>
+constexpr bool listed() {
+  for (const TileSize& d : kTileSize)
+    if (d.bm == BM && d.bn == BN && d.threads == THREADS) return true;
+  return false;
+}
+
+template <int FN, int NW, int U>
+hipError_t run_stream(const Args& a, hipStream_t s) {
+  static_assert(listed<16, 16 * FN, NW * kWave>(), "the choice counts these tiles and threads");
+  const unsigned grid = (unsigned)(((int64_t)a.N + 16 * FN - 1) / (16 * FN));
+  hipLaunchKernelGGL((stream_kernel<FN, NW, U>), dim3(grid), dim3(NW * kWave), 0, s, a);
+  return hipGetLastError();
+}
+
+template <bool KA, bool KB>
+struct Run {
+  template <int BM, int BN, int WM, int WN, int KG, int NS, int WPS>
+  static hipError_t tile(const Args& a, hipStream_t s) {
+    static_assert(listed<BM, BN, WM * WN * KG * kWave>(), "the choice counts these tiles and threads");
+    const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
+    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, KG, NS, WPS, KA, KB>),
+                       dim3((unsigned)xcd_chunked_grid<kChunk>(tiles)), dim3(WM * WN * KG * kWave),
+                       0, s, a);
+    return hipGetLastError();
+  }
+  static hipError_t dense(const Args& a, int layout, int cus, hipStream_t s) {
+    switch (choose(a.M, a.N, a.K, KA, KB, cus)) {
+      case kAny: return run_any(a, layout, s);
+      case kStream16x16:
+        if constexpr (KA && KB) return run_stream<1, 8, 2>(a, s);
+        break;
+      case kStream16x32:
+        if constexpr (KA && KB) return run_stream<2, 8, 2>(a, s);
+        break;
+      case kTile32x64:
+        if constexpr (KA) return tile<32, 64, 1, 4, 2, 3, 2>(a, s);
+        break;
+      case kTile64x64: return tile<64, 64, 2, 2, 2, 3, 2>(a, s);
+      case kTile64x128: return tile<64, 128, 2, 4, 1, 3, 2>(a, s);
+      case kTile128x128: return tile<128, 128, 2, 4, 1, 2, 4>(a, s);
+      case kTile128x256: return tile<128, 256, 2, 4, 1, 3, 2>(a, s);
+      case kTile256x256: return tile<256, 256, 2, 4, 1, 2, 2>(a, s);
+      case kKernels: break;
+    }
+    return hipErrorInvalidValue;
+  }
+};
+
+// ---------------------------------------------------------------------------------------------
 // Gradient of the epilogue
 // ---------------------------------------------------------------------------------------------
 // Beyond 200 every slope is 0 or 1 in fp32, and its formula would multiply 0 by infinity.
@@ -189,7 +683,10 @@ __global__ __launch_bounds__(kActThreads) void act_bwd_kernel(ActArgs g) {
 hipError_t launch_gemm_bf16(const GemmBf16& p, hipStream_t s) {
   gb::Args g{(const uint16_t*)p.a, (const uint16_t*)p.b, p.bias, p.residual, (uint16_t*)p.pre, p.c,
              p.M, p.N, p.K, p.act, p.c_f32};
-  return gb::run_any(g, p.layout, s);
+  const int cus = std::max(device_cu_count(), 8);
+  if (p.layout == MOE_NT) return gb::Run<true, true>::dense(g, p.layout, cus, s);
+  if (p.layout == MOE_NN) return gb::Run<true, false>::dense(g, p.layout, cus, s);
+  return gb::Run<false, false>::dense(g, p.layout, cus, s);
 }
 
 hipError_t launch_act_bwd(int M, int N, int act, const void* d_c, const void* pre, void* d_z,

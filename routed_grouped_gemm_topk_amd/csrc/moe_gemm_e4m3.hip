@@ -37,38 +37,6 @@ struct Args {
   int M, N, K;
 };
 
-__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-
-// Raw buffer descriptor of [base, base + bytes): a lane whose offset is past `bytes` reads zeros
-// without touching memory.
-__device__ __forceinline__ i32x4 buf_rsrc(const void* base, uint32_t bytes) {
-  const unsigned long long a = (unsigned long long)base;
-  i32x4 r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));   // stride 0
-  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);                 // num_records (bytes)
-  r[3] = 0x00020000;                                                 // raw 32-bit data
-  return r;
-}
-
-// 64 lanes x 16 (4) bytes from the buffer at voff + soff straight to LDS at M0 (s_nop: lds_dma16).
-__device__ __forceinline__ void buf_dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               ::"v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
-}
-// The same for memory that is read once: it does not push others out of the caches.
-__device__ __forceinline__ void buf_dma16_once(i32x4 rsrc, uint32_t voff, uint32_t soff,
-                                               uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
-               ::"v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
-}
-__device__ __forceinline__ void buf_dma4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
-               ::"v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
-}
-
-constexpr uint32_t kPastEnd = 0x80000000u;   // past every descriptor below (all < 2^31 bytes)
-
 // Four neighbouring n of one row of c.
 template <bool F32>
 __device__ __forceinline__ void store4(void* c, int64_t at, const f32x4& v, int n_left, bool vec) {

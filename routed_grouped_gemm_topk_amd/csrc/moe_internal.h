@@ -213,6 +213,40 @@ __device__ __forceinline__ uint32_t lds_u32(T* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)p;
 }
 
+// Where the 16-byte chunks of a row of 128 bytes lie in LDS: chunk c of row r at c ^ swz(r), so that 16
+// rows read at one offset fall on different banks.
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// Raw buffer descriptor of [base, base + bytes): a lane whose offset is past `bytes` reads zeros
+// without touching memory.
+__device__ __forceinline__ i32x4 buf_rsrc(const void* base, uint32_t bytes) {
+  const unsigned long long a = (unsigned long long)base;
+  i32x4 r;
+  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));   // stride 0
+  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);                 // num_records (bytes)
+  r[3] = 0x00020000;                                                 // raw 32-bit data
+  return r;
+}
+
+// 64 lanes x 16 (4) bytes from the buffer at voff + soff straight to LDS at M0 (s_nop: lds_dma16).
+__device__ __forceinline__ void buf_dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               ::"v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
+}
+// The same for memory that is read once: it does not push others out of the caches.
+__device__ __forceinline__ void buf_dma16_once(i32x4 rsrc, uint32_t voff, uint32_t soff,
+                                               uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+               ::"v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void buf_dma4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+               ::"v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
+}
+
+constexpr uint32_t kPastEnd = 0x80000000u;   // past every descriptor (all < 2^31 bytes)
+
 // ---------------------------------------------------------------------------------------------
 // Launchers (host side), one per translation unit
 // ---------------------------------------------------------------------------------------------
