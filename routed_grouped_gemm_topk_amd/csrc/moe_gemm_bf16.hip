@@ -199,9 +199,9 @@ __device__ __forceinline__ void finish8(const Args& g, const f32x4& z0, const f3
   }
 }
 
-// BM x BN tile by WM x WN waves; slices of 64 values of k of both operands in a ring of NS LDS
-// stages, copied by direct-to-LDS loads NS-1 steps ahead.  KG groups of WM x WN waves take every
-// KG-th slice each and their sums are added at the end in the order of the groups.
+// BM x BN tile by WM x WN waves; slices of 64 values of k of both operands in rings of LDS stages,
+// NSA of a and NSB of b, copied by direct-to-LDS loads.  KG groups of WM x WN waves take every KG-th
+// slice each and their sums are added at the end in the order of the groups.
 //
 // KA, KB: k is the contiguous dimension of the operand.  Then a stage holds its rows, 128 bytes of k
 // each, chunk c of row r at c ^ swz(r).  Otherwise it holds panels of 64 columns, each 64 rows of k
@@ -210,32 +210,51 @@ __device__ __forceinline__ void finish8(const Args& g, const f32x4& z0, const f3
 // {0-3, 16-19} (+ 4, 8, 12, 32 ...), whose pairs of chunks lie at c ^ 2 f with f = bit 1 of k and twice
 // bit 4 of k: all on different banks.  A lane's values of k are those of the other form: matrix
 // instruction t of a slice takes k = 16 (lane / 16) + 8 t + 0..7 of every lane.
-template <int BM, int BN, int WM, int WN, int KG, int NS, bool KA, bool KB>
+template <int BM, int BN, int WM, int WN, int KG, int NSA, int NSB, bool KA, bool KB>
 struct TileGemm {
   static constexpr int NW = WM * WN;
   static constexpr int WTM = BM / WM, WTN = BN / WN;        // a wave's part of the tile
   static constexpr int FM = WTM / 16, FN = WTN / 16;
-  static constexpr int NQ_REAL = (BM + BN) / 8;             // 1 KB copies per slice
-  static constexpr int NQ = (NQ_REAL + NW - 1) / NW * NW;
-  static constexpr int NQW = NQ / NW;
-  static constexpr int STAGE = NQ * 1024;
-  static constexpr int RING = NS * KG * STAGE;
+  static constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // a wave's 1 KB copies per slice
+  static constexpr int STAGE_A = BM * ROWB, STAGE_B = BN * ROWB;
+  static constexpr int RING_B = NSA * KG * STAGE_A;         // where b's ring begins
+  static constexpr int RING = RING_B + NSB * KG * STAGE_B;
   static constexpr int SUMS = (KG - 1) * NW * FM * FN * kWave * 16;
   static constexpr int PITCH = WTN * 4 + 16;
   static constexpr int OUTF = FM < 4 ? FM : 4;              // fragments turned around at a time
   static constexpr int OUT_OFF = KG > 1 ? SUMS : 0;
   static constexpr int OUT = OUT_OFF + NW * OUTF * 16 * PITCH;
   static constexpr int LDS = RING > OUT ? RING : OUT;
-  // A slice's copies go out in parts: PART of each wave right after the barrier that frees the
-  // stage, PART more before each of the next slice's fragments.
-  static constexpr int PART = NS == 2 && FM >= 4 ? std::max(2, (NQW + FM - 1) / FM) : NQW;
+  // A slice is multiplied in STEPS: both matrix instructions' halves of k, one after the other, and
+  // in each the fragments of a.  A fragment of a is read AHEAD steps before its products.
+  static constexpr int STEPS = 2 * FM, AHEAD = 3;
+  static constexpr int LAST = STEPS - 1 - AHEAD;            // the step that reads the slice's last
+  static constexpr int BSTEPS = std::min({LAST + 1, FM, FN});           // that read b's second half
+  static constexpr int BNEXT = LAST + 1 > FM ? LAST + 1 : FM;          // where its first half is free
+  // The fragments of b of a slice are in registers before half of its steps are done, those of a
+  // only towards its end.  With SOON a barrier of its own after step BFREE gives b's stage up there,
+  // so that two stages of b reach as far ahead as three of a.
+  static constexpr bool SOON = NSA != NSB;
+  static constexpr int BFREE = BSTEPS + 1;
+  // Copies go out one a step: b's (SOON) from step BFREE + 1 on, the others from step LAST + 1 on into
+  // the next slice's first steps.
+  static constexpr int TAIL = SOON ? CA : CA + CB;
+  static constexpr int EARLY = AHEAD < TAIL ? AHEAD : TAIL;   // of them before the next slice begins
+  // copies that may still be on their way when the next slice has to have landed: those that went out
+  // after its own
+  static constexpr int PENDING = !SOON ? (NSA - 2) * (CA + CB)
+                                 : NSB < NSA ? (NSB - 1) * (CA + CB)
+                                             : (NSA - 2) * CA + (NSA - 1) * CB;
   static_assert(WTM % 16 == 0 && WTN % 16 == 0 && FM % OUTF == 0, "whole fragments");
   static_assert(KA || (BM % 64 == 0 && (WTM % 64 == 0 || 64 % WTM == 0)), "whole panels");
   static_assert(KB || (BN % 64 == 0 && (WTN % 64 == 0 || 64 % WTN == 0)), "whole panels");
-  static_assert(BM % 8 == 0 && (KA || BM / 8 % 8 == 0), "whole copies");
-  static_assert(NS >= 2 && (NS - 1) * NQW <= 63, "vmcnt range");
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole copies");
+  static_assert(NSA >= 2 && NSB >= 2 && PENDING + TAIL <= 63, "vmcnt range");
   static_assert(LDS <= 160 * 1024, "LDS");
-  static_assert((NQW + PART - 1) / PART <= FM, "every part goes out within its slice");
+  static_assert(STEPS % (AHEAD + 1) == 0, "a fragment's registers are known");
+  static_assert(BNEXT + 2 <= STEPS, "b is read by then");
+  static_assert(TAIL - EARLY <= (SOON ? BFREE : LAST) + 1, "every copy goes out within its slice");
+  static_assert(!SOON || BFREE + CB <= LAST, "every copy goes out within its slice");
 
   // Where a lane finds a wave's fragments of an operand in a stage.
   template <bool KC, int WT, int F>
@@ -297,52 +316,54 @@ struct TileGemm {
                       left > 0 ? (uint32_t)(left * (int64_t)ld - first) * 2 : 0u);
     };
     const int kc = ((lane & 7) ^ (lane >> 3)) * 8;           // k of the lane's chunk, even copies
-    uint32_t voff[NQW];
+    // where copy q of an operand's slice (8 of its rows, or 8 rows of k of a panel) lies
+    auto offset = [&](auto contiguous, int q, int ld) {
+      if constexpr (decltype(contiguous)::value)
+        return (uint32_t)(q * 8 + (lane >> 3)) * (uint32_t)K * 2 +
+               (uint32_t)(kc ^ ((q & 1) * 8)) * 2;
+      const int k = (q & 7) * 8 + (lane >> 3);
+      const int f = ((k >> 1) & 1) | ((k >> 4) & 1) << 1;
+      return (uint32_t)k * (uint32_t)ld * 2 + (uint32_t)((q >> 3) * ROWB) +
+             (uint32_t)(((lane & 7) ^ (2 * f)) << 4);
+    };
+    using ContA = std::bool_constant<KA>;
+    using ContB = std::bool_constant<KB>;
+    uint32_t va[CA], vb[CB];
     #pragma unroll
-    for (int i = 0; i < NQW; ++i) {
-      const int q = wave * NQW + i;
-      const bool is_a = q < BM / 8;
-      const int qo = is_a ? q : q - BM / 8;
-      uint32_t v;
-      if (is_a ? KA : KB) {
-        v = (uint32_t)(qo * 8 + (lane >> 3)) * (uint32_t)K * 2 + (uint32_t)(kc ^ ((q & 1) * 8)) * 2;
-      } else {
-        const int k = (qo & 7) * 8 + (lane >> 3);
-        const int f = ((k >> 1) & 1) | ((k >> 4) & 1) << 1;
-        v = (uint32_t)k * (uint32_t)(is_a ? g.M : g.N) * 2 + (qo >> 3) * ROWB +
-            (((lane & 7) ^ (2 * f)) << 4);
-      }
-      voff[i] = q < NQ_REAL ? v : kPastEnd;
-    }
-    const uint32_t lds_base = lds_u32(lds);
-    // part p of the group's slice of `step` into stage buf
-    auto issue = [&](int buf, int step, int p) {
+    for (int i = 0; i < CA; ++i) va[i] = offset(ContA{}, wave * CA + i, g.M);
+    #pragma unroll
+    for (int i = 0; i < CB; ++i) vb[i] = offset(ContB{}, wave * CB + i, g.N);
+    const uint32_t lds_base = __builtin_amdgcn_readfirstlane(lds_u32(lds));
+    // copy q (the wave's) of an operand's slice of `step` into its stage; `ends`: k may pass K in it
+    auto copy = [&](auto ends, auto contiguous, i32x4 r, uint32_t v, int q, int step, uint32_t stage) {
       const int kt = step * KG + kg;
-      const uint32_t st = __builtin_amdgcn_readfirstlane(lds_base + (buf * KG + kg) * STAGE);
-      const int left = K - kt * kSlice;
-      i32x4 sa = ra, sb = rb;
-      if constexpr (!KA) sa = rows_of_k(g.a, g.M, t.m0, kt);
-      if constexpr (!KB) sb = rows_of_k(g.b, g.N, t.n0, kt);
-      auto copies = [&](auto tail) {
-        #pragma unroll
-        for (int i = 0; i < NQW; ++i) {
-          if (i / PART != p) continue;
-          const int q = wave * NQW + i;
-          const bool is_a = q < BM / 8;
-          uint32_t v = voff[i];
-          const bool contiguous = is_a ? KA : KB;
-          if (decltype(tail)::value && contiguous && (kc ^ ((q & 1) * 8)) >= left) v = kPastEnd;
-          buf_dma16(is_a ? sa : sb, v, contiguous ? (uint32_t)kt * ROWB : 0u, st + q * 1024);
-        }
-      };
-      if ((KA || KB) && left < kSlice) copies(std::true_type{});
-      else copies(std::false_type{});
+      constexpr bool C = decltype(contiguous)::value;
+      if (decltype(ends)::value && C && (kc ^ ((q & 1) * 8)) >= K - kt * kSlice) v = kPastEnd;
+      buf_dma16(r, v, C ? (uint32_t)kt * ROWB : 0u, lds_base + stage + (uint32_t)q * 1024);
+    };
+    auto copy_a = [&](auto ends, int buf, int step, int i) {
+      i32x4 r = ra;
+      if constexpr (!KA) r = rows_of_k(g.a, g.M, t.m0, step * KG + kg);
+      copy(ends, ContA{}, r, va[i], wave * CA + i, step, (uint32_t)((buf * KG + kg) * STAGE_A));
+    };
+    auto copy_b = [&](auto ends, int buf, int step, int i) {
+      i32x4 r = rb;
+      if constexpr (!KB) r = rows_of_k(g.b, g.N, t.n0, step * KG + kg);
+      copy(ends, ContB{}, r, vb[i], wave * CB + i, step,
+           (uint32_t)(RING_B + (buf * KG + kg) * STAGE_B));
+    };
+    // copy i of the tail's: b's first, where they are in it
+    auto copy_tail = [&](auto ends, int buf_a, int buf_b, int step_a, int step_b, int i) {
+      if (i < 0 || i >= TAIL) return;
+      if (SOON) copy_a(ends, buf_a, step_a, i);
+      else if (i < CB) copy_b(ends, buf_b, step_b, i);
+      else copy_a(ends, buf_a, step_a, i - CB);
     };
 
     Where<KA, WTM, FM> wa;
     Where<KB, WTN, FN> wb;
-    wa.init(kg * STAGE, wm, lane);
-    wb.init(kg * STAGE + BM * ROWB, wn, lane);
+    wa.init(kg * STAGE_A, wm, lane);
+    wb.init(RING_B + kg * STAGE_B, wn, lane);
 
     f32x4 acc[FM][FN];
     #pragma unroll
@@ -350,68 +371,76 @@ struct TileGemm {
       #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // Software pipeline over a's fragments: while the products of fragment i run, fragment i+1 is
-    // read.  The barrier of a slice sits before its last fragment's products: every wave has read
-    // all of the slice by then, so its stage is refilled (slice kt + NS) and those products cover
-    // the first reads of slice kt+1.
-    bf16x8 bf[FN][2], af[2][2];
-    auto read_a = [&](int i, bf16x8* f) {
+    // Software pipeline.  The barrier of a slice sits AHEAD steps before its end: every wave has read
+    // all of the slice by then, so its stages are refilled, and the steps left cover the first reads
+    // of the next slice.  Fragments of b are read half a slice ahead, a few a step.
+    bf16x8 bf[2][FN], af[AHEAD + 1];
+    auto read_b = [&](int h, int step, int steps_for_it) {
+      const int per = (FN + steps_for_it - 1) / steps_for_it;
       #pragma unroll
-      for (int h = 0; h < 2; ++h) f[h] = wa.read(lds, i, h);
+      for (int j = 0; j < FN; ++j)
+        if (j / per == step) bf[h][j] = wb.read(lds, j, h);
     };
-    auto read_b = [&](int j) {
+    int ba = 0, bb = 0;           // the slice's stages
+    auto after = [](int buf, int n) { return buf + 1 == n ? 0 : buf + 1; };
+    auto slice = [&](auto ends, int step) {
+      const int na = after(ba, NSA), nb = after(bb, NSB);
+      const int pa = ba == 0 ? NSA - 1 : ba - 1, pb = bb == 0 ? NSB - 1 : bb - 1;
       #pragma unroll
-      for (int h = 0; h < 2; ++h) bf[j][h] = wb.read(lds, j, h);
-    };
-    int buf = 0;
-    auto slice = [&](auto par, int step) {
-      constexpr int P = decltype(par)::value * FM;     // fragments of the slices before, mod 2
-      const int nbuf = (buf + 1 == NS) ? 0 : buf + 1;
-      const int pbuf = (buf == 0) ? NS - 1 : buf - 1;
-      #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int c = (P + i) & 1;                     // this fragment's set
-        if (i + 1 < FM) {
-          read_a(i + 1, af[c ^ 1]);
-          if ((i + 1) * PART < NQW) issue(pbuf, step - 1 + NS, i + 1);
-        } else {
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          wait_vmcnt<(NS - 2) * NQW>();                // this wave's copies of the next slice
-          __builtin_amdgcn_s_barrier();
-          issue(buf, step + NS, 0);
-          const uint32_t d = (uint32_t)((nbuf - buf) * KG * STAGE);
-          wa.step(d);
-          wb.step(d);
-          read_a(0, af[c ^ 1]);
-        }
+      for (int u = 0; u < STEPS; ++u) {
+        const int next = (u + AHEAD) % STEPS;
+        af[next % (AHEAD + 1)] = wa.read(lds, next % FM, next / FM);
+        if (u <= LAST) read_b(1, u, BSTEPS);
+        if (u >= BNEXT) read_b(0, u - BNEXT, 2);       // the next slice's
+        if (u <= LAST) copy_tail(ends, pa, pb, step - 1 + NSA, step - 1 + NSB, EARLY + u);
+        else copy_tail(ends, ba, bb, step + NSA, step + NSB, u - LAST - 1);
+        if (SOON && u > BFREE && u - BFREE <= CB) copy_b(ends, bb, step + NSB, u - BFREE - 1);
         #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          #pragma unroll
-          for (int h = 0; h < 2; ++h) acc[i][j] = OpBf16::mma(bf[j][h], af[c][h], acc[i][j]);
-          if (i + 1 == FM) read_b(j);
+        for (int j = 0; j < FN; ++j)
+          acc[u % FM][j] = OpBf16::mma(bf[u / FM][j], af[u % (AHEAD + 1)], acc[u % FM][j]);
+        if (SOON && u == BFREE) {
+          __builtin_amdgcn_sched_barrier(0);           // the waits come after these products
+          // b was read two steps before and earlier; since then only a, once a step
+          asm volatile("s_waitcnt lgkmcnt(2)" ::: "memory");
+          __builtin_amdgcn_s_barrier();
         }
+        if (u == LAST) {
+          __builtin_amdgcn_sched_barrier(0);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          wait_vmcnt<PENDING>();                       // this wave's copies of the next slice
+          __builtin_amdgcn_s_barrier();
+          wa.step((uint32_t)((na - ba) * KG * STAGE_A));
+          wb.step((uint32_t)((nb - bb) * KG * STAGE_B));
+        }
+        // the scheduler would move the reads down to their products
+        __builtin_amdgcn_sched_barrier(0);
       }
-      buf = nbuf;
+      ba = na;
+      bb = nb;
     };
-    // slices 0..NS-2 whole and the first part of slice NS-1; slice 0 has to have landed
+    // what the slices before the first would have copied, in their order
     #pragma unroll
-    for (int s = 0; s < NS - 1; ++s)
+    for (int e = -(NSA > NSB ? NSA : NSB); e < 0; ++e) {
+      const std::true_type ends{};
+      if (SOON && e + NSB >= 0)
+        #pragma unroll
+        for (int i = 0; i < CB; ++i) copy_b(ends, e + NSB, e + NSB, i);
+      if (e + NSA < 0) continue;
       #pragma unroll
-      for (int p = 0; p * PART < NQW; ++p) issue(s, s, p);
-    issue(NS - 1, NS - 1, 0);
-    wait_vmcnt<(NS - 2) * NQW + (PART < NQW ? PART : NQW)>();
-    __syncthreads();
-    read_a(0, af[0]);
-    #pragma unroll
-    for (int j = 0; j < FN; ++j) read_b(j);
-    using Even = std::integral_constant<int, 0>;
-    using Odd = std::integral_constant<int, 1>;
-    int step = 0;
-    for (; step + 1 < steps; step += 2) {
-      slice(Even{}, step);
-      slice(Odd{}, step + 1);
+      for (int i = 0; i < (e == -1 ? EARLY : TAIL); ++i)
+        copy_tail(ends, e + NSA, e + NSB, e + NSA, e + NSB, i);
     }
-    if (step < steps) slice(Even{}, step);
+    // slice 0 has to have landed
+    wait_vmcnt<!SOON ? (NSA - 2) * TAIL + EARLY : 0>();
+    __syncthreads();
+    #pragma unroll
+    for (int u = 0; u < AHEAD; ++u) af[u] = wa.read(lds, u % FM, u / FM);
+    read_b(0, 0, 1);
+    // steps that copy whole slices only, and those that come to the end of k
+    const int whole = min(steps, max(K / kSlice / KG - std::max(NSA, NSB), 0));
+    int step = 0;
+    for (; step < whole; ++step) slice(std::false_type{}, step);
+    for (; step < steps; ++step) slice(std::true_type{}, step);
     wait_vmcnt<0>();
 
     __syncthreads();              // the ring is done with
@@ -486,9 +515,9 @@ struct TileGemm {
   }
 };
 
-template <int BM, int BN, int WM, int WN, int KG, int NS, int WPS, bool KA, bool KB>
+template <int BM, int BN, int WM, int WN, int KG, int NSA, int NSB, int WPS, bool KA, bool KB>
 __global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void tile_kernel(Args g) {
-  using G = TileGemm<BM, BN, WM, WN, KG, NS, KA, KB>;
+  using G = TileGemm<BM, BN, WM, WN, KG, NSA, NSB, KA, KB>;
   __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
   const int mblk = (g.M + BM - 1) / BM, nblk = (g.N + BN - 1) / BN;
   const int logical = xcd_chunked<kChunk>(blockIdx.x, mblk * nblk);
@@ -583,11 +612,11 @@ hipError_t run_stream(const Args& a, hipStream_t s) {
 
 template <bool KA, bool KB>
 struct Run {
-  template <int BM, int BN, int WM, int WN, int KG, int NS, int WPS>
+  template <int BM, int BN, int WM, int WN, int KG, int NSA, int NSB, int WPS>
   static hipError_t tile(const Args& a, hipStream_t s) {
     static_assert(listed<BM, BN, WM * WN * KG * kWave>(), "the choice counts these tiles and threads");
     const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
-    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, KG, NS, WPS, KA, KB>),
+    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, KG, NSA, NSB, WPS, KA, KB>),
                        dim3((unsigned)xcd_chunked_grid<kChunk>(tiles)), dim3(WM * WN * KG * kWave),
                        0, s, a);
     return hipGetLastError();
@@ -602,13 +631,13 @@ struct Run {
         if constexpr (KA && KB) return run_stream<2, 8, 2>(a, s);
         break;
       case kTile32x64:
-        if constexpr (KA) return tile<32, 64, 1, 4, 2, 3, 2>(a, s);
+        if constexpr (KA) return tile<32, 64, 1, 4, 2, 3, 3, 2>(a, s);
         break;
-      case kTile64x64: return tile<64, 64, 2, 2, 2, 3, 2>(a, s);
-      case kTile64x128: return tile<64, 128, 2, 4, 1, 3, 2>(a, s);
-      case kTile128x128: return tile<128, 128, 2, 4, 1, 2, 4>(a, s);
-      case kTile128x256: return tile<128, 256, 2, 4, 1, 3, 2>(a, s);
-      case kTile256x256: return tile<256, 256, 2, 4, 1, 2, 2>(a, s);
+      case kTile64x64: return tile<64, 64, 2, 2, 2, 3, 3, 2>(a, s);
+      case kTile64x128: return tile<64, 128, 2, 4, 1, 3, 3, 2>(a, s);
+      case kTile128x128: return tile<128, 128, 2, 4, 1, 2, 2, 4>(a, s);
+      case kTile128x256: return tile<128, 256, 2, 4, 1, 3, 3, 2>(a, s);
+      case kTile256x256: return tile<256, 256, 2, 4, 1, 3, 2, 2>(a, s);
       case kKernels: break;
     }
     return hipErrorInvalidValue;
