@@ -221,7 +221,7 @@ struct TileGemm {
   static constexpr int RING = RING_B + NSB * KG * STAGE_B;
   static constexpr int SUMS = (KG - 1) * NW * FM * FN * kWave * 16;
   static constexpr int PITCH = WTN * 4 + 16;
-  static constexpr int OUTF = FM < 4 ? FM : 4;              // fragments turned around at a time
+  static constexpr int OUTF = FM <= 4 ? FM : FM % 4 ? 3 : 4;              // fragments turned around at a time
   static constexpr int OUT_OFF = KG > 1 ? SUMS : 0;
   static constexpr int OUT = OUT_OFF + NW * OUTF * 16 * PITCH;
   static constexpr int LDS = RING > OUT ? RING : OUT;
@@ -236,7 +236,7 @@ struct TileGemm {
   // so that two stages of b reach as far ahead as three of a.
   static constexpr bool SOON = NSA != NSB;
   static constexpr int BFREE = BSTEPS + 1;
-  // Copies go out one a step: b's (SOON) from step BFREE + 1 on, the others from step LAST + 1 on into
+  // Copies go out one a step, b's (SOON) two a step from step BFREE + 1 on, the others from step LAST + 1 on into
   // the next slice's first steps.
   static constexpr int TAIL = SOON ? CA : CA + CB;
   static constexpr int EARLY = AHEAD < TAIL ? AHEAD : TAIL;   // of them before the next slice begins
@@ -246,15 +246,14 @@ struct TileGemm {
                                  : NSB < NSA ? (NSB - 1) * (CA + CB)
                                              : (NSA - 2) * CA + (NSA - 1) * CB;
   static_assert(WTM % 16 == 0 && WTN % 16 == 0 && FM % OUTF == 0, "whole fragments");
-  static_assert(KA || (BM % 64 == 0 && (WTM % 64 == 0 || 64 % WTM == 0)), "whole panels");
-  static_assert(KB || (BN % 64 == 0 && (WTN % 64 == 0 || 64 % WTN == 0)), "whole panels");
+  static_assert((KA || BM % 64 == 0) && (KB || BN % 64 == 0), "whole panels");
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole copies");
   static_assert(NSA >= 2 && NSB >= 2 && PENDING + TAIL <= 63, "vmcnt range");
   static_assert(LDS <= 160 * 1024, "LDS");
   static_assert(STEPS % (AHEAD + 1) == 0, "a fragment's registers are known");
   static_assert(BNEXT + 2 <= STEPS, "b is read by then");
   static_assert(TAIL - EARLY <= (SOON ? BFREE : LAST) + 1, "every copy goes out within its slice");
-  static_assert(!SOON || BFREE + CB <= LAST, "every copy goes out within its slice");
+  static_assert(!SOON || BFREE + (CB + 1) / 2 <= LAST, "every copy goes out within its slice");
 
   // Where a lane finds a wave's fragments of an operand in a stage.
   template <bool KC, int WT, int F>
@@ -270,11 +269,11 @@ struct TileGemm {
       } else {
         const int k = fq * 16 + (fr >> 2);
         const int f = ((k >> 1) & 1) | ((k >> 4) & 1) << 1;
-        const int c0 = w * WT / 16;                    // the wave's first 16 columns
         #pragma unroll
         for (int v = 0; v < NADDR; ++v) {
-          const int pair = ((c0 + v) & 3) ^ f;
-          at[v] = base + (c0 / 4) * 64 * ROWB + k * ROWB +
+          const int c = w * WT / 16 + v;               // 16 columns of the operand
+          const int pair = (c & 3) ^ f;
+          at[v] = base + (c / 4) * 64 * ROWB + k * ROWB +
                   ((2 * pair + ((fr >> 1) & 1)) << 4) + (fr & 1) * 8;
         }
       }
@@ -394,7 +393,10 @@ struct TileGemm {
         if (u >= BNEXT) read_b(0, u - BNEXT, 2);       // the next slice's
         if (u <= LAST) copy_tail(ends, pa, pb, step - 1 + NSA, step - 1 + NSB, EARLY + u);
         else copy_tail(ends, ba, bb, step + NSA, step + NSB, u - LAST - 1);
-        if (SOON && u > BFREE && u - BFREE <= CB) copy_b(ends, bb, step + NSB, u - BFREE - 1);
+        if (SOON && u > BFREE)
+          #pragma unroll
+          for (int i = 2 * (u - BFREE - 1); i < std::min(CB, 2 * (u - BFREE)); ++i)
+            copy_b(ends, bb, step + NSB, i);
         #pragma unroll
         for (int j = 0; j < FN; ++j)
           acc[u % FM][j] = OpBf16::mma(bf[u / FM][j], af[u % (AHEAD + 1)], acc[u % FM][j]);
@@ -482,7 +484,8 @@ struct TileGemm {
               acc[i0 + i][j];
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (g.N % 8 == 0) {
-        constexpr int VPR = WTN / 8, RPP = kWave / VPR < 16 ? kWave / VPR : 16;
+        constexpr int VPR = WTN / 8, RPP = VPR <= 4 ? 16 : 8;    // lanes of a row, rows a turn
+        static_assert(VPR <= 8 && OUTF * 16 % RPP == 0, "whole turns");
         constexpr int TURNS = OUTF * 16 / RPP;
         const int c = lane % VPR * 8, n = n_w + c;
         const bool in_n = lane < RPP * VPR && n < t.cols;
@@ -497,17 +500,16 @@ struct TileGemm {
           finish8(g, z[0], z[1], at, t.n0 + n, res);
         }
       } else {
-        constexpr int VPR = WTN < kWave ? WTN : kWave, RPP = kWave / VPR;
+        constexpr int VPR = WTN, RPP = kWave / VPR;
+        static_assert(VPR <= kWave, "a column a lane");
         #pragma unroll 2
-        for (int u = 0; u < OUTF * 16 / RPP; ++u) {
+        for (int u = 0; u < OUTF * 16 / RPP; ++u) {        // OUTF * 16 is a multiple of 4
+          if (lane >= RPP * VPR) break;
           const int r = u * RPP + lane / VPR, m = m_w + i0 * 16 + r;
-          #pragma unroll
-          for (int c0 = 0; c0 < WTN; c0 += VPR) {
-            const int c = c0 + lane % VPR, n = n_w + c;
-            if (m >= t.rows || n >= t.cols) continue;
-            const float z = *reinterpret_cast<const float*>(mine + r * PITCH + c * 4);
-            finish<1>(g, &z, t.m0 + m, t.n0 + n, 1);
-          }
+          const int c = lane % VPR, n = n_w + c;
+          if (m >= t.rows || n >= t.cols) continue;
+          const float z = *reinterpret_cast<const float*>(mine + r * PITCH + c * 4);
+          finish<1>(g, &z, t.m0 + m, t.n0 + n, 1);
         }
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -520,77 +522,114 @@ __global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void tile_kernel(Args g)
   using G = TileGemm<BM, BN, WM, WN, KG, NSA, NSB, KA, KB>;
   __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
   const int mblk = (g.M + BM - 1) / BM, nblk = (g.N + BN - 1) / BN;
-  const int logical = xcd_chunked<kChunk>(blockIdx.x, mblk * nblk);
+  const int logical = xcd_logical(blockIdx.x, mblk * nblk);
   if (logical < 0) return;
   G::run(g, tile_at<BM, BN>(g, logical), lds);
 }
 
-// Few rows of a (up to 16), a b^T: what counts is how fast b streams from HBM.  A workgroup takes
-// 16 * FN rows of b and its NW waves take every NW-th slice, straight from memory into the matrix
-// instructions' registers: no value of b is used twice, so LDS would only add a stop, and cutting K
-// over the waves keeps the workgroups as many as N / (16 * FN) with the bytes in flight of NW waves
-// each.  The waves' sums are added through LDS in the order of the waves.
-template <int FN, int NW, int U>
+// 256x256 tiles in rounds of one workgroup per compute unit, the first `whole` of them whole, the others
+// as two halves (whole_tiles).
+template <bool KA, bool KB>
+__global__ __launch_bounds__(512, 2) void large_kernel(Args g, int whole, int whole_grid) {
+  using G = TileGemm<256, 256, 2, 4, 1, 3, 2, KA, KB>;
+  using H = TileGemm<128, 256, 2, 4, 1, 3, 3, KA, KB>;
+  __shared__ __attribute__((aligned(1024))) char lds[G::LDS > H::LDS ? G::LDS : H::LDS];
+  if ((int)blockIdx.x < whole_grid) {
+    const int logical = xcd_logical(blockIdx.x, whole);
+    if (logical >= 0) G::run(g, tile_at<256, 256>(g, logical), lds);
+    return;
+  }
+  const int tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
+  const int h = xcd_logical((int)blockIdx.x - whole_grid, (tiles - whole) * 2);
+  if (h < 0) return;
+  Tile t = tile_at<256, 256>(g, whole + h / 2);
+  t.m0 += (h & 1) * 128;
+  t.rows = min(128, t.rows - (h & 1) * 128);
+  if (t.rows > 0) H::run(g, t, lds);
+}
+
+// Few rows, a b^T: what counts is how fast the operands stream into the compute units that there are
+// tiles for, 64 bytes a cycle each at most.  A workgroup takes 16 * FM rows of a and 16 * FN of b, and
+// its NW waves every NW-th slice, each through a ring of its own in LDS, NS stages deep: whole lines
+// of memory in every copy, and no barrier until the waves' sums are added, in the order of the waves.
+template <int FM, int FN, int NW, int NS>
 __global__ __launch_bounds__(NW * kWave) void stream_kernel(Args g) {
-  constexpr int BN = 16 * FN;
-  __shared__ __attribute__((aligned(16))) f32x4 sums[NW * FN * kWave];
+  constexpr int BM = 16 * FM, BN = 16 * FN;
+  constexpr int CA = BM / 8, CB = BN / 8;              // 1 KB copies of a slice
+  constexpr int STAGE = (CA + CB) * 1024;
+  constexpr int RING = NW * NS * STAGE, SUMS = NW * FM * FN * kWave * 16;
+  static_assert(RING <= 160 * 1024 && SUMS <= RING && (NS - 1) * (CA + CB) <= 63, "LDS, vmcnt");
+  __shared__ __attribute__((aligned(1024))) char lds[RING];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int K = g.K, KT = (K + kSlice - 1) / kSlice;
   const int fr = lane & 15, fq = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * BN;
-  // rows past the operands' ends read the last row, their products are not stored
-  const uint16_t *pa = g.a + (size_t)min(fr, g.M - 1) * K + fq * 8, *pb[FN];
+  const int nblk = (g.N + BN - 1) / BN;
+  const int m0 = (int)blockIdx.x / nblk * BM, n0 = (int)blockIdx.x % nblk * BN;
+  // rows and values of k past the operands' ends read as zeros
+  const i32x4 ra = buf_rsrc(g.a + (size_t)m0 * K, (uint32_t)min(BM, g.M - m0) * (uint32_t)K * 2);
+  const i32x4 rb = buf_rsrc(g.b + (size_t)n0 * K, (uint32_t)min(BN, g.N - n0) * (uint32_t)K * 2);
+  const int kc = ((lane & 7) ^ (lane >> 3)) * 8;       // k of the lane's chunk, even copies
+  uint32_t v[2];                                       // copies 2 i and 2 i + 1 of an operand
   #pragma unroll
-  for (int j = 0; j < FN; ++j)
-    pb[j] = g.b + (size_t)min(n0 + j * 16 + fr, (int64_t)g.N - 1) * K + fq * 8;
-  struct Slice {                // one slice in registers
-    bf16x8 a[2], b[FN][2];
-  };
-  auto load = [&](Slice& s, int kt) {
+  for (int o = 0; o < 2; ++o)
+    v[o] = (uint32_t)(o * 8 + (lane >> 3)) * (uint32_t)K * 2 + (uint32_t)(kc ^ (o * 8)) * 2;
+  const uint32_t mine = __builtin_amdgcn_readfirstlane(lds_u32(lds) + wave * NS * STAGE);
+  auto copy = [&](int slot, int i) {                   // the wave's i-th slice
+    const int kt = i * NW + wave, left = K - kt * kSlice;
     #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = kt * kSlice + h * 32;
-      const bf16x8 none = {};
-      const bool in = k + fq * 8 < K;
-      s.a[h] = in ? *reinterpret_cast<const bf16x8*>(pa + k) : none;
-      #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        s.b[j][h] = in ? *reinterpret_cast<const bf16x8*>(pb[j] + k) : none;
+    for (int q = 0; q < CA + CB; ++q) {
+      const bool is_a = q < CA;
+      const int o = q & 1, row16 = (is_a ? q : q - CA) / 2;
+      uint32_t at = v[o] + (uint32_t)row16 * 32u * (uint32_t)K;
+      if ((kc ^ (o * 8)) >= left) at = kPastEnd;
+      buf_dma16(is_a ? ra : rb, at, (uint32_t)kt * ROWB, mine + slot * STAGE + q * 1024);
     }
   };
-  f32x4 acc[FN] = {};
-  // U slices are in flight while the U before them are multiplied
-  Slice cur[U], nxt[U];
-  int kt = wave;
+  f32x4 acc[FM][FN] = {};
+  const int slices = (KT + NW - 1) / NW;               // the same for every wave
   #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (kt + u * NW < KT) load(cur[u], kt + u * NW);
-  for (; kt < KT; kt += U * NW) {
+  for (int i = 0; i < NS - 1; ++i) copy(i, i);
+  const char* stages = lds + wave * NS * STAGE;
+  int slot = 0;
+  for (int i = 0; i < slices; ++i) {
+    // the slice before has been read: its stage takes the one NS - 1 further on
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    copy(slot == 0 ? NS - 1 : slot - 1, i + NS - 1);
+    wait_vmcnt<(NS - 1) * (CA + CB)>();
+    const char* st = stages + slot * STAGE;
     #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (kt + (U + u) * NW < KT) load(nxt[u], kt + (U + u) * NW);
-    #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (kt + u * NW < KT) {
+    for (int h = 0; h < 2; ++h) {
+      const int chunk = ((2 * fq + h) ^ swz(fr)) << 4;
+      bf16x8 a[FM], b[FN];
+      #pragma unroll
+      for (int r = 0; r < FM; ++r)
+        a[r] = *reinterpret_cast<const bf16x8*>(st + (r * 16 + fr) * ROWB + chunk);
+      #pragma unroll
+      for (int c = 0; c < FN; ++c)
+        b[c] = *reinterpret_cast<const bf16x8*>(st + (BM + c * 16 + fr) * ROWB + chunk);
+      #pragma unroll
+      for (int r = 0; r < FM; ++r)
         #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          #pragma unroll
-          for (int j = 0; j < FN; ++j) acc[j] = OpBf16::mma(cur[u].b[j][h], cur[u].a[h], acc[j]);
-      }
-    #pragma unroll
-    for (int u = 0; u < U; ++u) cur[u] = nxt[u];
+        for (int c = 0; c < FN; ++c) acc[r][c] = OpBf16::mma(b[c], a[r], acc[r][c]);
+    }
+    slot = slot + 1 == NS ? 0 : slot + 1;
   }
-  #pragma unroll
-  for (int j = 0; j < FN; ++j) sums[(wave * FN + j) * kWave + lane] = acc[j];
+  wait_vmcnt<0>();
   __syncthreads();
-  for (int j = wave; j < FN; j += NW) {
-    f32x4 c = sums[j * kWave + lane];
+  f32x4* sums = reinterpret_cast<f32x4*>(lds);
+  #pragma unroll
+  for (int r = 0; r < FM; ++r)
     #pragma unroll
-    for (int w = 1; w < NW; ++w) c += sums[(w * FN + j) * kWave + lane];
-    const int64_t n = n0 + j * 16 + fq * 4;
-    const float v[4] = {c[0], c[1], c[2], c[3]};
-    if (fr < g.M && n < g.N) finish<4>(g, v, fr, (int)n, g.N - (int)n);
+    for (int c = 0; c < FN; ++c) sums[(wave * FM * FN + r * FN + c) * kWave + lane] = acc[r][c];
+  __syncthreads();
+  for (int f = wave; f < FM * FN; f += NW) {
+    f32x4 c = sums[f * kWave + lane];
+    #pragma unroll
+    for (int w = 1; w < NW; ++w) c += sums[(w * FM * FN + f) * kWave + lane];
+    const int m = m0 + f / FN * 16 + fr, n = n0 + f % FN * 16 + fq * 4;
+    const float z[4] = {c[0], c[1], c[2], c[3]};
+    if (m < g.M && n < g.N) finish<4>(g, z, m, n, g.N - n);
   }
 }
 
@@ -602,11 +641,13 @@ constexpr bool listed() {
   return false;
 }
 
-template <int FN, int NW, int U>
+template <int FM, int FN, int NW, int NS>
 hipError_t run_stream(const Args& a, hipStream_t s) {
-  static_assert(listed<16, 16 * FN, NW * kWave>(), "the choice counts these tiles and threads");
-  const unsigned grid = (unsigned)(((int64_t)a.N + 16 * FN - 1) / (16 * FN));
-  hipLaunchKernelGGL((stream_kernel<FN, NW, U>), dim3(grid), dim3(NW * kWave), 0, s, a);
+  static_assert(listed<16 * FM, 16 * FN, NW * kWave>(), "the choice counts these tiles and threads");
+  const int64_t tiles = (((int64_t)a.M + 16 * FM - 1) / (16 * FM)) *
+                        (((int64_t)a.N + 16 * FN - 1) / (16 * FN));
+  hipLaunchKernelGGL((stream_kernel<FM, FN, NW, NS>), dim3((unsigned)tiles), dim3(NW * kWave), 0, s,
+                     a);
   return hipGetLastError();
 }
 
@@ -617,27 +658,35 @@ struct Run {
     static_assert(listed<BM, BN, WM * WN * KG * kWave>(), "the choice counts these tiles and threads");
     const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
     hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, KG, NSA, NSB, WPS, KA, KB>),
-                       dim3((unsigned)xcd_chunked_grid<kChunk>(tiles)), dim3(WM * WN * KG * kWave),
-                       0, s, a);
+                       dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(WM * WN * KG * kWave), 0, s, a);
+    return hipGetLastError();
+  }
+  static hipError_t large(const Args& a, int cus, hipStream_t s) {
+    const int64_t tiles = tiles_of(kTile256x256, a.M, a.N), whole = whole_tiles(tiles, cus);
+    const int64_t whole_grid = (whole + 7) / 8 * 8, halves = ((tiles - whole) * 2 + 7) / 8 * 8;
+    hipLaunchKernelGGL((large_kernel<KA, KB>), dim3((unsigned)(whole_grid + halves)), dim3(512), 0,
+                       s, a, (int)whole, (int)whole_grid);
     return hipGetLastError();
   }
   static hipError_t dense(const Args& a, int layout, int cus, hipStream_t s) {
     switch (choose(a.M, a.N, a.K, KA, KB, cus)) {
       case kAny: return run_any(a, layout, s);
       case kStream16x16:
-        if constexpr (KA && KB) return run_stream<1, 8, 2>(a, s);
+        if constexpr (KA && KB) return run_stream<1, 1, 8, 4>(a, s);
         break;
       case kStream16x32:
-        if constexpr (KA && KB) return run_stream<2, 8, 2>(a, s);
+        if constexpr (KA && KB) return run_stream<1, 2, 8, 3>(a, s);
         break;
       case kTile32x64:
-        if constexpr (KA) return tile<32, 64, 1, 4, 2, 3, 3, 2>(a, s);
+        if constexpr (KA) return tile<32, 64, 1, 4, 2, 4, 4, 2>(a, s);
         break;
       case kTile64x64: return tile<64, 64, 2, 2, 2, 3, 3, 2>(a, s);
       case kTile64x128: return tile<64, 128, 2, 4, 1, 3, 3, 2>(a, s);
-      case kTile128x128: return tile<128, 128, 2, 4, 1, 2, 2, 4>(a, s);
+      case kTile128x128: return tile<128, 128, 2, 4, 1, 3, 3, 2>(a, s);
       case kTile128x256: return tile<128, 256, 2, 4, 1, 3, 3, 2>(a, s);
-      case kTile256x256: return tile<256, 256, 2, 4, 1, 3, 2, 2>(a, s);
+      case kTile192x192: return tile<192, 192, 2, 4, 1, 3, 3, 2>(a, s);
+      case kTile192x256: return tile<192, 256, 2, 4, 1, 4, 2, 2>(a, s);
+      case kTile256x256: return large(a, cus, s);
       case kKernels: break;
     }
     return hipErrorInvalidValue;
