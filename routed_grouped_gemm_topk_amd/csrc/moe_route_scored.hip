@@ -8,6 +8,8 @@
 // rounded up to a power of two) neighbouring lanes: expert g * GS + sub + LG * i (GS = E / n_groups)
 // is item i of lane g * LG + sub, so that a group's value is a butterfly over its lanes, and without
 // groups item i of lane l is expert l + 64 i.
+#include <type_traits>
+
 #include "moe_route.h"
 
 namespace moe {
@@ -59,24 +61,157 @@ __device__ __forceinline__ float wave_max(float v) {
   return wave_allreduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// LPL: items per lane.  C: the type that choices are compared in: double for sums of scores and
-// biases; float where the logits are compared.
-template <int LPL, class C>
-__global__ __launch_bounds__(kThreads) void route_scored_kernel(Args g) {
-  constexpr bool SCORES = sizeof(C) == 8;
-  constexpr C NONE = -INFINITY;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int t = blockIdx.x * kTokens + threadIdx.x / kWave;
-  if (t >= g.T) return;
-  const int grp = lane >> g.lg, sub = lane & ((1 << g.lg) - 1);
-  const int e0 = grp * g.gs + sub;
-  float l[LPL];
+// exp(l - m) in fp32 for l <= m: what the subtraction rounds off is put back (relative error 3 u,
+// u = 2^-24, whatever l - m is).
+__device__ __forceinline__ float exp_diff(float l, float m) {
+  const float d = l - m, back = d - l;
+  const float rest = (l - (d - back)) - (m + back);
+  const float e = expf(d);
+  return d > -104.0f ? __builtin_fmaf(e, rest, e) : 0.0f;      // below it e is 0, and rest may be NaN
+}
+
+struct Token {
+  int64_t t;
+  int lane, grp, sub, e0;       // lane, its group, its place in it, its first expert
+};
+
+// The choice and the weights in fp32; returns false, having stored nothing, where fp32 does not tell
+// two experts or groups apart that the choice depends on.  Every lane of the wave must be active.
+//
+// Errors (u = 2^-24): a sigmoid score is at most 1 and 5 u of itself off; a softmax score p is 3 u
+// of itself off for its exponential, 3 u and an addition's u for each of LPL + 6 for the sum, 1 u for
+// the quotient, and at most 1 / total; a choice score c another u |c| for the addition of the bias, a
+// sum of two the errors of both and its own.  Two that differ by more than both errors are in the
+// right order.  Where the logits themselves are compared, only equal ones are uncertain.
+template <int LPL, bool SCORES>
+__device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const float (&l)[LPL]) {
+  constexpr float U = 0x1p-24f;
+  float m = 0.0f, total = 1.0f, sure = 0.0f;   // sure: error of the scores of two experts
+  float s[LPL], c[LPL];
+  if (!g.sigmoid) {
+    m = -INFINITY;
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) m = fmaxf(m, l[i]);
+    m = wave_max(m);
+    if (m == -INFINITY) m = 0.0f;
+    float sum = 0.0f;
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) {
+      s[i] = exp_diff(l[i], m);
+      sum += s[i];
+    }
+    if (SCORES || !g.renorm) total = wave_allreduce(sum, [](float a, float b) { return a + b; });
+    if (SCORES) sure = 2 * (LPL + 13) * U / total;
+  } else {
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) s[i] = 1.0f / (1.0f + expf(-l[i]));
+    sure = 2 * 5 * U;
+  }
   #pragma unroll
   for (int i = 0; i < LPL; ++i) {
-    const int in = sub + (i << g.lg);
-    l[i] = grp < g.groups && in < g.gs
-               ? load_logit(g.logits, (int64_t)t * g.E + e0 + (i << g.lg), g.bf16) : -INFINITY;
+    c[i] = l[i];
+    if (SCORES && l[i] > -INFINITY) {
+      const float b = g.bias ? g.bias[at.e0 + (i << g.lg)] : 0.0f;
+      c[i] = b > -INFINITY ? (g.sigmoid ? s[i] : s[i] / total) + b : -INFINITY;
+    }
   }
+  auto apart = [&](float hi, float lo, float err) {
+    return hi - lo > (SCORES ? err + 4 * U * (fabsf(hi) + fabsf(lo)) : 0.0f);
+  };
+  bool ok = true;
+  if (g.kept < g.groups) {
+    float v1 = -INFINITY, v2 = -INFINITY;
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) {
+      v2 = fmaxf(v2, fminf(v1, c[i]));
+      v1 = fmaxf(v1, c[i]);
+    }
+    for (int d = 1; d < (1 << g.lg); d *= 2) {
+      const float o1 = __shfl_xor(v1, d, kWave), o2 = __shfl_xor(v2, d, kWave);
+      v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
+      v1 = fmaxf(v1, o1);
+    }
+    const float value = g.top == 2 && v2 > -INFINITY ? v1 + v2 : v1;
+    // a sum's error is at most that of its two scores, each off by u |c|, |c| <= |v1| + |v2|
+    const float size = fabsf(v1) + (v2 > -INFINITY ? fabsf(v2) : 0.0f);
+    int before = 0;             // groups that come before this lane's
+    bool close = false;
+    for (int o = 0; o < g.groups; ++o) {
+      const float ov = bcast(value, o << g.lg), os = bcast(size, o << g.lg);
+      before += ov > value;
+      close |= o != at.grp && !(fabsf(ov - value) > (SCORES ? 2 * sure + 4 * U * (os + size) : 0.0f));
+    }
+    ok = __ballot(close && at.grp < g.groups) == 0;
+    if (before >= g.kept) {
+      #pragma unroll
+      for (int i = 0; i < LPL; ++i) c[i] = -INFINITY;
+    }
+  }
+  int round[LPL];               // the round in which the item was chosen
+  #pragma unroll
+  for (int i = 0; i < LPL; ++i) round[i] = -1;
+  float prev = INFINITY;
+  int found = 0;
+  for (int j = 0; j <= g.K; ++j) {       // one more than are chosen, for the last one's margin
+    float best = c[0];
+    #pragma unroll
+    for (int i = 1; i < LPL; ++i) best = fmaxf(best, c[i]);
+    best = wave_max(best);
+    if (best == -INFINITY) break;
+    ok = ok && (j == 0 || apart(prev, best, sure));
+    if (j == g.K) break;
+    int n = 0;
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) {
+      const bool is = c[i] == best;
+      n += __popcll(__ballot(is));
+      round[i] = is ? j : round[i];
+      c[i] = is ? -INFINITY : c[i];
+    }
+    ok = ok && n == 1;
+    prev = best;
+    found = j + 1;
+  }
+  if (!ok) return false;
+  if (g.renorm) {
+    float sum = 0.0f;
+    if (!g.sigmoid) {           // relative to the largest chosen, which may be far below m
+      float top = -INFINITY;
+      #pragma unroll
+      for (int i = 0; i < LPL; ++i) top = fmaxf(top, round[i] >= 0 ? l[i] : -INFINITY);
+      top = fmaxf(wave_max(top), -3.40282347e38f);
+      if (top != m) {
+        #pragma unroll
+        for (int i = 0; i < LPL; ++i) s[i] = exp_diff(l[i], fmaxf(top, l[i]));
+      }
+    }
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) sum += round[i] >= 0 ? s[i] : 0.0f;
+    total = wave_allreduce(sum, [](float a, float b) { return a + b; });
+    if (g.sigmoid && total < 0x1p-100f) return false;    // their ratios need 64 bits
+  }
+  const bool divide = g.renorm || !g.sigmoid;
+  #pragma unroll
+  for (int i = 0; i < LPL; ++i) {
+    if (round[i] < 0) continue;
+    const float w = divide ? (total > 0.0f ? s[i] / total : 0.0f) : s[i];
+    g.ids[at.t * g.K + round[i]] = at.e0 + (i << g.lg);
+    g.w[at.t * g.K + round[i]] = w * g.scale;
+  }
+  if (at.lane >= found && at.lane < g.K) {
+    g.ids[at.t * g.K + at.lane] = -1;
+    g.w[at.t * g.K + at.lane] = 0.0f;
+  }
+  return true;
+}
+
+// The same with scores, group values and weights in 64 bits (SCORES) and ties to the lowest ids.
+template <int LPL, bool SCORES>
+__device__ __forceinline__ void route_exact(const Args& g, const Token& at_, const float (&l)[LPL]) {
+  using C = typename std::conditional<SCORES, double, float>::type;
+  constexpr C NONE = -INFINITY;
+  const int lane = at_.lane, grp = at_.grp, e0 = at_.e0;
+  const int64_t t = at_.t;
   float m = 0.0f;               // softmax: the largest logit, 0 without any
   double total = 0.0;           // softmax: the sum of exp(l - m)
   if (!g.sigmoid && (SCORES || !g.renorm)) {
@@ -205,9 +340,27 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(Args g) {
   if (g.renorm) total = wave_sum(s);
   if (g.renorm || !g.sigmoid) s = total > 0.0 ? s / total : 0.0;
   if (lane < g.K) {
-    g.ids[(int64_t)t * g.K + lane] = my_id;
-    g.w[(int64_t)t * g.K + lane] = (float)(s * (double)g.scale);
+    g.ids[t * g.K + lane] = my_id;
+    g.w[t * g.K + lane] = (float)(s * (double)g.scale);
   }
+}
+
+// LPL: items per lane.  SCORES: scores and their sums are compared, not the logits.
+template <int LPL, bool SCORES>
+__global__ __launch_bounds__(kThreads) void route_scored_kernel(Args g) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t t = (int64_t)blockIdx.x * kTokens + threadIdx.x / kWave;
+  if (t >= g.T) return;
+  const int grp = lane >> g.lg, sub = lane & ((1 << g.lg) - 1);
+  const Token at{t, lane, grp, sub, grp * g.gs + sub};
+  float l[LPL];
+  #pragma unroll
+  for (int i = 0; i < LPL; ++i) {
+    const int in = sub + (i << g.lg);
+    l[i] = grp < g.groups && in < g.gs
+               ? load_logit(g.logits, t * g.E + at.e0 + (i << g.lg), g.bf16) : -INFINITY;
+  }
+  if (!route_fast<LPL, SCORES>(g, at, l)) route_exact<LPL, SCORES>(g, at, l);
 }
 
 struct BwdArgs {
@@ -302,16 +455,16 @@ __global__ __launch_bounds__(kThreads) void route_scored_bwd_kernel(BwdArgs g) {
   }
 }
 
-template <class C>
+template <bool SCORES>
 hipError_t run_route(const Args& a, hipStream_t s) {
   const dim3 grid((unsigned)(((int64_t)a.T + kTokens - 1) / kTokens)), block(kThreads);
   const int items = (a.gs + (1 << a.lg) - 1) >> a.lg;    // at most 32 (E <= 1024)
-  if (items <= 1) hipLaunchKernelGGL((route_scored_kernel<1, C>), grid, block, 0, s, a);
-  else if (items <= 2) hipLaunchKernelGGL((route_scored_kernel<2, C>), grid, block, 0, s, a);
-  else if (items <= 4) hipLaunchKernelGGL((route_scored_kernel<4, C>), grid, block, 0, s, a);
-  else if (items <= 8) hipLaunchKernelGGL((route_scored_kernel<8, C>), grid, block, 0, s, a);
-  else if (items <= 16) hipLaunchKernelGGL((route_scored_kernel<16, C>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((route_scored_kernel<32, C>), grid, block, 0, s, a);
+  if (items <= 1) hipLaunchKernelGGL((route_scored_kernel<1, SCORES>), grid, block, 0, s, a);
+  else if (items <= 2) hipLaunchKernelGGL((route_scored_kernel<2, SCORES>), grid, block, 0, s, a);
+  else if (items <= 4) hipLaunchKernelGGL((route_scored_kernel<4, SCORES>), grid, block, 0, s, a);
+  else if (items <= 8) hipLaunchKernelGGL((route_scored_kernel<8, SCORES>), grid, block, 0, s, a);
+  else if (items <= 16) hipLaunchKernelGGL((route_scored_kernel<16, SCORES>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((route_scored_kernel<32, SCORES>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -330,7 +483,7 @@ hipError_t launch_route_scored(const Resolved& r, const moe_router& q, const voi
   a.lg = 6;
   while ((kWave >> a.lg) < q.n_groups) --a.lg;
   const bool sums = bias || (q.topk_groups < q.n_groups && q.group_top == 2);
-  return sums ? rs::run_route<double>(a, s) : rs::run_route<float>(a, s);
+  return sums ? rs::run_route<true>(a, s) : rs::run_route<false>(a, s);
 }
 
 hipError_t launch_route_scored_bwd(const Resolved& r, const moe_router& q, const void* logits,
