@@ -75,132 +75,184 @@ struct Token {
   int lane, grp, sub, e0;       // lane, its group, its place in it, its first expert
 };
 
+// Floats as integers of the same order (the function is its own inverse): their maxima need no
+// quieting of NaN and take a lane exchange as an operand.  kNoKey is below all of them.
+constexpr int kNoKey = INT32_MIN;
+__device__ __forceinline__ int ordered(int b) { return b ^ ((b >> 31) & 0x7fffffff); }
+__device__ __forceinline__ int key_of(float f) { return ordered(__builtin_bit_cast(int, f)); }
+__device__ __forceinline__ float of_key(int k) { return __builtin_bit_cast(float, ordered(k)); }
+
+__device__ __forceinline__ int wave_max(int v) {
+  return wave_allreduce(v, [](int a, int b) { return max(a, b); });
+}
+
+// A lane exchange after which groups of 2d lanes agree, if groups of d lanes did before.
+template <class F>
+__device__ __forceinline__ void exchange(int lg, F step) {
+  if (lg > 0) step([](int v) { return dpp_xchg<0xB1>(v); });      // quad_perm 1,0,3,2
+  if (lg > 1) step([](int v) { return dpp_xchg<0x4E>(v); });      // quad_perm 2,3,0,1
+  if (lg > 2) step([](int v) { return dpp_xchg<0x141>(v); });     // row_half_mirror
+  if (lg > 3) step([](int v) { return dpp_xchg<0x140>(v); });     // row_mirror
+  if (lg > 4) step([](int v) { return __shfl_xor(v, 16, kWave); });
+  if (lg > 5) step([](int v) { return __shfl_xor(v, 32, kWave); });
+}
+
 // The choice and the weights in fp32; returns false, having stored nothing, where fp32 does not tell
 // two experts or groups apart that the choice depends on.  Every lane of the wave must be active.
 //
-// Errors (u = 2^-24): a sigmoid score is at most 1 and 5 u of itself off; a softmax score p is 3 u
-// of itself off for its exponential, 3 u and an addition's u for each of LPL + 6 for the sum, 1 u for
-// the quotient, and at most 1 / total; a choice score c another u |c| for the addition of the bias, a
-// sum of two the errors of both and its own.  Two that differ by more than both errors are in the
-// right order.  Where the logits themselves are compared, only equal ones are uncertain.
+// An expert's key is its choice score's (its logit's) ordered integer, whose last bits hold the item's
+// place in the lane, so that a lane's keys differ and the largest one names its item.  A bf16 logit
+// leaves 16 bits, which hold the whole id, the lowest largest: its order, ties included, is exact.
+//
+// Errors otherwise (u = 2^-24): a sigmoid score is at most 1 and 5 u of itself off (2 u exponential,
+// 1 u addition, 2 u reciprocal); a softmax score p is 3 u of itself off for its exponential, 3 u and
+// an addition's u for each of LPL + 6 for the sum, 3 u for the quotient, and at most 1 / total; a choice
+// score c another u |c| for the addition of the bias and 2 LPL u |c| for the bits given up; a sum of
+// two the errors of both and its own.  Two that differ by more than both errors are in the right
+// order.
 template <int LPL, bool SCORES>
-__device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const float (&l)[LPL]) {
+__device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const float (&l)[LPL],
+                                           const float (&bias)[LPL]) {
   constexpr float U = 0x1p-24f;
-  float m = 0.0f, total = 1.0f, sure = 0.0f;   // sure: error of the scores of two experts
-  float s[LPL], c[LPL];
-  if (!g.sigmoid) {
+  const bool whole_ids = !SCORES && g.bf16;
+  float m = 0.0f, inv = 1.0f, sure = 0.0f;     // sure: error of the scores of two experts
+  if (!g.sigmoid && (SCORES || !g.renorm)) {
     m = -INFINITY;
     #pragma unroll
     for (int i = 0; i < LPL; ++i) m = fmaxf(m, l[i]);
     m = wave_max(m);
     if (m == -INFINITY) m = 0.0f;
-    float sum = 0.0f;
+  }
+  int key[LPL], group1 = kNoKey, group2 = kNoKey;      // the group's two largest
+  if (SCORES || (!g.sigmoid && !g.renorm)) {
+    float s[LPL];
+    if (!g.sigmoid) {
+      float sum = 0.0f;
+      #pragma unroll
+      for (int i = 0; i < LPL; ++i) {
+        s[i] = exp_diff(l[i], m);
+        sum += s[i];
+      }
+      sum = wave_allreduce(sum, [](float a, float b) { return a + b; });
+      inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+      sure = 2 * (LPL + 15) * U * inv;
+    } else {
+      #pragma unroll
+      for (int i = 0; i < LPL; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + expf(-l[i]));
+      sure = 2 * 5 * U;
+    }
+    if constexpr (SCORES) {
+      #pragma unroll
+      for (int i = 0; i < LPL; ++i) {
+        const float c = s[i] * inv + bias[i];
+        key[i] = l[i] > -INFINITY && bias[i] > -INFINITY ? key_of(c) : kNoKey;
+      }
+    }
+  }
+  if constexpr (!SCORES) {
     #pragma unroll
     for (int i = 0; i < LPL; ++i) {
-      s[i] = exp_diff(l[i], m);
-      sum += s[i];
-    }
-    if (SCORES || !g.renorm) total = wave_allreduce(sum, [](float a, float b) { return a + b; });
-    if (SCORES) sure = 2 * (LPL + 13) * U / total;
-  } else {
-    #pragma unroll
-    for (int i = 0; i < LPL; ++i) s[i] = 1.0f / (1.0f + expf(-l[i]));
-    sure = 2 * 5 * U;
-  }
-  #pragma unroll
-  for (int i = 0; i < LPL; ++i) {
-    c[i] = l[i];
-    if (SCORES && l[i] > -INFINITY) {
-      const float b = g.bias ? g.bias[at.e0 + (i << g.lg)] : 0.0f;
-      c[i] = b > -INFINITY ? (g.sigmoid ? s[i] : s[i] / total) + b : -INFINITY;
+      const int k = key_of(l[i]);
+      key[i] = l[i] == -INFINITY ? kNoKey
+               : whole_ids ? (k & ~0xffff) | (0xffff - (at.e0 + (i << g.lg))) : k;
     }
   }
-  auto apart = [&](float hi, float lo, float err) {
-    return hi - lo > (SCORES ? err + 4 * U * (fabsf(hi) + fabsf(lo)) : 0.0f);
+  // two values of the same kind that are further apart than their errors
+  auto apart = [&](float hi, float lo, float err, float parts) {
+    return hi - lo > (SCORES ? err : 0.0f) + parts * U * (fabsf(hi) + fabsf(lo));
   };
   bool ok = true;
   if (g.kept < g.groups) {
-    float v1 = -INFINITY, v2 = -INFINITY;
     #pragma unroll
     for (int i = 0; i < LPL; ++i) {
-      v2 = fmaxf(v2, fminf(v1, c[i]));
-      v1 = fmaxf(v1, c[i]);
+      group2 = max(group2, min(group1, key[i]));
+      group1 = max(group1, key[i]);
     }
-    for (int d = 1; d < (1 << g.lg); d *= 2) {
-      const float o1 = __shfl_xor(v1, d, kWave), o2 = __shfl_xor(v2, d, kWave);
-      v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
-      v1 = fmaxf(v1, o1);
-    }
-    const float value = g.top == 2 && v2 > -INFINITY ? v1 + v2 : v1;
-    // a sum's error is at most that of its two scores, each off by u |c|, |c| <= |v1| + |v2|
-    const float size = fabsf(v1) + (v2 > -INFINITY ? fabsf(v2) : 0.0f);
+    exchange(g.lg, [&](auto from) {
+      const int o1 = from(group1), o2 = from(group2);
+      group2 = max(min(group1, o1), max(group2, o2));
+      group1 = max(group1, o1);
+    });
+    const bool two = SCORES && g.top == 2 && group2 != kNoKey;
+    const float v1 = of_key(group1), v2 = of_key(group2);
+    const int value = two ? key_of(v1 + v2) : group1;
     int before = 0;             // groups that come before this lane's
-    bool close = false;
-    for (int o = 0; o < g.groups; ++o) {
-      const float ov = bcast(value, o << g.lg), os = bcast(size, o << g.lg);
-      before += ov > value;
-      close |= o != at.grp && !(fabsf(ov - value) > (SCORES ? 2 * sure + 4 * U * (os + size) : 0.0f));
-    }
-    ok = __ballot(close && at.grp < g.groups) == 0;
+    for (int o = 0; o < g.groups; ++o)
+      before += __builtin_amdgcn_readlane(value, o << g.lg) > value;
+    // the last group kept and the first that is not: one each unless two values are the same
+    const bool first = at.sub == 0 && at.grp < g.groups;
+    const uint64_t in = __ballot(first && before == g.kept - 1);
+    const uint64_t out = __ballot(first && before == g.kept);
+    if (__popcll(in) != 1 || __popcll(out) != 1) return false;
+    const int a = __builtin_ctzll(in), b = __builtin_ctzll(out);
+    const float size = two ? fabsf(v1) + fabsf(v2) : 0.0f;
+    const int va = __builtin_amdgcn_readlane(value, a), vb = __builtin_amdgcn_readlane(value, b);
+    if (!whole_ids && vb != kNoKey)
+      ok = apart(of_key(va), of_key(vb), 2 * sure + 4 * U * (bcast(size, a) + bcast(size, b)), 2);
     if (before >= g.kept) {
       #pragma unroll
-      for (int i = 0; i < LPL; ++i) c[i] = -INFINITY;
+      for (int i = 0; i < LPL; ++i) key[i] = kNoKey;
     }
   }
-  int round[LPL];               // the round in which the item was chosen
-  #pragma unroll
-  for (int i = 0; i < LPL; ++i) round[i] = -1;
-  float prev = INFINITY;
-  int found = 0;
-  for (int j = 0; j <= g.K; ++j) {       // one more than are chosen, for the last one's margin
-    float best = c[0];
+  if (!whole_ids) {
     #pragma unroll
-    for (int i = 1; i < LPL; ++i) best = fmaxf(best, c[i]);
-    best = wave_max(best);
-    if (best == -INFINITY) break;
-    ok = ok && (j == 0 || apart(prev, best, sure));
-    if (j == g.K) break;
-    int n = 0;
+    for (int i = 0; i < LPL; ++i)
+      key[i] = key[i] == kNoKey ? kNoKey : (key[i] & ~(LPL - 1)) | (LPL - 1 - i);
+  }
+  // lane j: the key and the lane of the j-th choice; one more than are chosen, for its margin
+  int my_key = kNoKey, my_lane = 0, after = kNoKey, found = 0, same = 0;
+  for (int j = 0; j <= g.K; ++j) {
+    int best = key[0];
     #pragma unroll
-    for (int i = 0; i < LPL; ++i) {
-      const bool is = c[i] == best;
-      n += __popcll(__ballot(is));
-      round[i] = is ? j : round[i];
-      c[i] = is ? -INFINITY : c[i];
-    }
-    ok = ok && n == 1;
-    prev = best;
+    for (int i = 1; i < LPL; ++i) best = max(best, key[i]);
+    const int mine = best;
+    best = __builtin_amdgcn_readfirstlane(wave_max(best));
+    after = best;
+    if (best == kNoKey || j == g.K) break;
+    const uint64_t who = __ballot(mine == best);
+    same |= (who & (who - 1)) != 0;
+    my_key = at.lane == j ? best : my_key;
+    my_lane = at.lane == j ? __builtin_ctzll(who) : my_lane;
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) key[i] = key[i] == best ? kNoKey : key[i];
     found = j + 1;
   }
-  if (!ok) return false;
-  if (g.renorm) {
-    float sum = 0.0f;
-    if (!g.sigmoid) {           // relative to the largest chosen, which may be far below m
-      float top = -INFINITY;
-      #pragma unroll
-      for (int i = 0; i < LPL; ++i) top = fmaxf(top, round[i] >= 0 ? l[i] : -INFINITY);
-      top = fmaxf(wave_max(top), -3.40282347e38f);
-      if (top != m) {
-        #pragma unroll
-        for (int i = 0; i < LPL; ++i) s[i] = exp_diff(l[i], fmaxf(top, l[i]));
-      }
-    }
-    #pragma unroll
-    for (int i = 0; i < LPL; ++i) sum += round[i] >= 0 ? s[i] : 0.0f;
-    total = wave_allreduce(sum, [](float a, float b) { return a + b; });
-    if (g.sigmoid && total < 0x1p-100f) return false;    // their ratios need 64 bits
+  const bool here = at.lane < found;
+  if (!whole_ids) {
+    int next = __shfl_down(my_key, 1, kWave);
+    if (at.lane + 1 >= found) next = after;
+    const bool sure_of = next == kNoKey || apart(of_key(my_key & ~(LPL - 1)),
+                                                 of_key(next & ~(LPL - 1)), sure,
+                                                 SCORES ? 2 * LPL + 4 : 2 * LPL);
+    if (same || !ok || __ballot(here && !sure_of)) return false;
   }
-  const bool divide = g.renorm || !g.sigmoid;
+  const int grp = my_lane >> g.lg, sub = my_lane & ((1 << g.lg) - 1);
+  const int e0 = grp * g.gs + sub;
+  int item, id;
+  if (whole_ids) {
+    id = 0xffff - (my_key & 0xffff);
+    item = (id - e0) >> g.lg;
+  } else {
+    item = LPL - 1 - (my_key & (LPL - 1));
+    id = e0 + (item << g.lg);
+  }
+  float lj = -INFINITY;
   #pragma unroll
   for (int i = 0; i < LPL; ++i) {
-    if (round[i] < 0) continue;
-    const float w = divide ? (total > 0.0f ? s[i] / total : 0.0f) : s[i];
-    g.ids[at.t * g.K + round[i]] = at.e0 + (i << g.lg);
-    g.w[at.t * g.K + round[i]] = w * g.scale;
+    const float v = __shfl(l[i], my_lane, kWave);
+    if (i == item) lj = v;
   }
-  if (at.lane >= found && at.lane < g.K) {
-    g.ids[at.t * g.K + at.lane] = -1;
-    g.w[at.t * g.K + at.lane] = 0.0f;
+  if (!here) lj = -INFINITY;
+  if (!g.sigmoid && g.renorm) m = fmaxf(wave_max(lj), -3.40282347e38f);
+  float s = g.sigmoid ? __builtin_amdgcn_rcpf(1.0f + expf(-lj)) : exp_diff(lj, m);
+  if (g.renorm) {
+    const float sum = wave_allreduce(s, [](float a, float b) { return a + b; });
+    if (g.sigmoid && sum < 0x1p-100f) return false;      // their ratios need 64 bits
+    inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+  }
+  if (at.lane < g.K) {
+    g.ids[at.t * g.K + at.lane] = here ? id : -1;
+    g.w[at.t * g.K + at.lane] = here ? s * inv * g.scale : 0.0f;
   }
   return true;
 }
@@ -353,14 +405,32 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(Args g) {
   if (t >= g.T) return;
   const int grp = lane >> g.lg, sub = lane & ((1 << g.lg) - 1);
   const Token at{t, lane, grp, sub, grp * g.gs + sub};
-  float l[LPL];
+  // all loads first, from places that are there; lanes without the item drop it
+  float l[LPL], bias[LPL];
+  int e[LPL];
   #pragma unroll
   for (int i = 0; i < LPL; ++i) {
     const int in = sub + (i << g.lg);
-    l[i] = grp < g.groups && in < g.gs
-               ? load_logit(g.logits, t * g.E + at.e0 + (i << g.lg), g.bf16) : -INFINITY;
+    e[i] = grp < g.groups && in < g.gs ? at.e0 + (i << g.lg) : 0;
   }
-  if (!route_fast<LPL, SCORES>(g, at, l)) route_exact<LPL, SCORES>(g, at, l);
+  if (g.bf16) {
+    uint16_t raw[LPL];
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) raw[i] = ((const uint16_t*)g.logits)[t * g.E + e[i]];
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) l[i] = bf16_bits_to_f32(raw[i]);
+  } else {
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) l[i] = ((const float*)g.logits)[t * g.E + e[i]];
+  }
+  #pragma unroll
+  for (int i = 0; i < LPL; ++i) bias[i] = SCORES && g.bias ? g.bias[e[i]] : 0.0f;
+  #pragma unroll
+  for (int i = 0; i < LPL; ++i) {
+    const int in = sub + (i << g.lg);
+    l[i] = grp < g.groups && in < g.gs ? clean(l[i]) : -INFINITY;
+  }
+  if (!route_fast<LPL, SCORES>(g, at, l, bias)) route_exact<LPL, SCORES>(g, at, l);
 }
 
 struct BwdArgs {
