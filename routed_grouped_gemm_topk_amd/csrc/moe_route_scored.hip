@@ -61,13 +61,26 @@ __device__ __forceinline__ float wave_max(float v) {
   return wave_allreduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// exp(l - m) in fp32 for l <= m: what the subtraction rounds off is put back (relative error 3 u,
-// u = 2^-24, whatever l - m is).
+// exp(x) for |x| <= 100 from the base-2 exponential of gfx950 (2 u off, u = 2^-24): what the product
+// with log2 e rounds off, and that constant itself, is put back.  3 u off; 0 for results below 2^-126.
+__device__ __forceinline__ float exp_of(float x) {
+  const float t = x * 1.44269502f;
+  const float rest = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, 1.44269502f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, rest * 0.693147181f, e);
+}
+
+// 1 / (1 + exp(-l)): 6 u off (3 u, 1 u for the addition, 2 u for the reciprocal), and 0 below 2^-126.
+__device__ __forceinline__ float sigmoid_of(float l) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_of(__builtin_amdgcn_fmed3f(-l, -88.0f, 88.0f)));
+}
+
+// exp(l - m) for l <= m: what the subtraction rounds off is put back too.  4 u off.
 __device__ __forceinline__ float exp_diff(float l, float m) {
   const float d = l - m, back = d - l;
   const float rest = (l - (d - back)) - (m + back);
-  const float e = expf(d);
-  return d > -104.0f ? __builtin_fmaf(e, rest, e) : 0.0f;      // below it e is 0, and rest may be NaN
+  const float e = exp_of(fmaxf(d, -100.0f));
+  return d > -100.0f ? __builtin_fmaf(e, rest, e) : 0.0f;      // below it rest may be NaN
 }
 
 struct Token {
@@ -82,8 +95,20 @@ __device__ __forceinline__ int ordered(int b) { return b ^ ((b >> 31) & 0x7fffff
 __device__ __forceinline__ int key_of(float f) { return ordered(__builtin_bit_cast(int, f)); }
 __device__ __forceinline__ float of_key(int k) { return __builtin_bit_cast(float, ordered(k)); }
 
-__device__ __forceinline__ int wave_max(int v) {
-  return wave_allreduce(v, [](int a, int b) { return max(a, b); });
+// The largest of a wave's values, as a scalar: within rows of 16 lanes, then row 0 to 1 and 2 to 3, then
+// rows 0-1 to 2-3, whose last lane has it.  Each step's exchange is an operand of its maximum.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int max_step(int v) {
+  return max(v, __builtin_amdgcn_update_dpp(kNoKey, v, CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ int wave_top(int v) {
+  v = max_step<0xB1>(v);          // quad_perm 1,0,3,2
+  v = max_step<0x4E>(v);          // quad_perm 2,3,0,1
+  v = max_step<0x141>(v);         // row_half_mirror
+  v = max_step<0x140>(v);         // row_mirror
+  v = max_step<0x142, 0xa>(v);    // row_bcast 15 into rows 1 and 3
+  v = max_step<0x143, 0xc>(v);    // row_bcast 31 into rows 2 and 3
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
 // A lane exchange after which groups of 2d lanes agree, if groups of d lanes did before.
@@ -104,9 +129,9 @@ __device__ __forceinline__ void exchange(int lg, F step) {
 // place in the lane, so that a lane's keys differ and the largest one names its item.  A bf16 logit
 // leaves 16 bits, which hold the whole id, the lowest largest: its order, ties included, is exact.
 //
-// Errors otherwise (u = 2^-24): a sigmoid score is at most 1 and 5 u of itself off (2 u exponential,
-// 1 u addition, 2 u reciprocal); a softmax score p is 3 u of itself off for its exponential, 3 u and
-// an addition's u for each of LPL + 6 for the sum, 3 u for the quotient, and at most 1 / total; a choice
+// Errors otherwise (u = 2^-24): a sigmoid score is at most 1 and 6 u of itself off; a softmax score p is
+// 4 u of itself off for its exponential, 4 u and an addition's u for each of LPL + 6 for the sum, 3 u
+// for the product with its reciprocal, and at most 1 / total (2^-126 where it is smaller); a choice
 // score c another u |c| for the addition of the bias and 2 LPL u |c| for the bits given up; a sum of
 // two the errors of both and its own.  Two that differ by more than both errors are in the right
 // order.
@@ -135,11 +160,11 @@ __device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const
       }
       sum = wave_allreduce(sum, [](float a, float b) { return a + b; });
       inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
-      sure = 2 * (LPL + 15) * U * inv;
+      sure = 2 * (LPL + 18) * U * inv;
     } else {
       #pragma unroll
-      for (int i = 0; i < LPL; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + expf(-l[i]));
-      sure = 2 * 5 * U;
+      for (int i = 0; i < LPL; ++i) s[i] = sigmoid_of(l[i]);
+      sure = 2 * 6 * U;
     }
     if constexpr (SCORES) {
       #pragma unroll
@@ -206,7 +231,7 @@ __device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const
     #pragma unroll
     for (int i = 1; i < LPL; ++i) best = max(best, key[i]);
     const int mine = best;
-    best = __builtin_amdgcn_readfirstlane(wave_max(best));
+    best = wave_top(best);
     after = best;
     if (best == kNoKey || j == g.K) break;
     const uint64_t who = __ballot(mine == best);
@@ -244,7 +269,7 @@ __device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const
   }
   if (!here) lj = -INFINITY;
   if (!g.sigmoid && g.renorm) m = fmaxf(wave_max(lj), -3.40282347e38f);
-  float s = g.sigmoid ? __builtin_amdgcn_rcpf(1.0f + expf(-lj)) : exp_diff(lj, m);
+  float s = !here ? 0.0f : g.sigmoid ? sigmoid_of(lj) : exp_diff(lj, m);
   if (g.renorm) {
     const float sum = wave_allreduce(s, [](float a, float b) { return a + b; });
     if (g.sigmoid && sum < 0x1p-100f) return false;      // their ratios need 64 bits
@@ -423,8 +448,13 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(Args g) {
     #pragma unroll
     for (int i = 0; i < LPL; ++i) l[i] = ((const float*)g.logits)[t * g.E + e[i]];
   }
-  #pragma unroll
-  for (int i = 0; i < LPL; ++i) bias[i] = SCORES && g.bias ? g.bias[e[i]] : 0.0f;
+  if (SCORES && g.bias) {
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) bias[i] = g.bias[e[i]];
+  } else {
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) bias[i] = 0.0f;
+  }
   #pragma unroll
   for (int i = 0; i < LPL; ++i) {
     const int in = sub + (i << g.lg);
