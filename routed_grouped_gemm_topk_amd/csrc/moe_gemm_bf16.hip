@@ -30,11 +30,17 @@ __device__ __forceinline__ float gelu_tanh_arg(float z) {       // 2 sqrt(2/pi) 
   return 1.59576912f * z * __builtin_fmaf(0.044715f * z, z, 1.0f);
 }
 
+// 1 / (1 + exp(-z)): 6 u off (u = 2^-24); exactly 0 below -88, where z may be anything.
+__device__ __forceinline__ float sigmoid_of(float z) {
+  const float s = __builtin_amdgcn_rcpf(1.0f + exp_of(__builtin_amdgcn_fmed3f(-z, -88.0f, 88.0f)));
+  return z < -88.0f ? 0.0f : s;
+}
+
 __device__ __forceinline__ float activate(float z, int act) {
-  if (act == MOE_ACT_SILU) return z / (1.0f + expf(-z));
+  if (act == MOE_ACT_SILU) return z * sigmoid_of(z);
   if (act == MOE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.707106781f));
   // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
-  if (act == MOE_ACT_GELU_TANH) return z / (1.0f + expf(-gelu_tanh_arg(z)));
+  if (act == MOE_ACT_GELU_TANH) return z * sigmoid_of(gelu_tanh_arg(z));
   return z;
 }
 
@@ -700,14 +706,14 @@ struct Run {
 __device__ __forceinline__ float slope(float z, int act) {
   if (z == z) z = fminf(fmaxf(z, -200.0f), 200.0f);
   if (act == MOE_ACT_SILU) {
-    const float s = 1.0f / (1.0f + expf(-z));
+    const float s = sigmoid_of(z);
     return s * (1.0f + z * (1.0f - s));
   }
   if (act == MOE_ACT_GELU)
-    return 0.5f * (1.0f + erff(z * 0.707106781f)) + z * 0.398942280f * expf(-0.5f * z * z);
+    return 0.5f * (1.0f + erff(z * 0.707106781f)) + z * 0.398942280f * exp_of(fmaxf(-0.5f * z * z, -88.0f));
   if (act == MOE_ACT_GELU_TANH) {
     // with s = (1 + tanh u) / 2: s + z s (1 - s) 2 u'
-    const float s = 1.0f / (1.0f + expf(-gelu_tanh_arg(z)));
+    const float s = sigmoid_of(gelu_tanh_arg(z));
     const float du = 1.59576912f * __builtin_fmaf(3.0f * 0.044715f * z, z, 1.0f);
     return s + z * s * (1.0f - s) * du;
   }
@@ -721,39 +727,82 @@ struct ActArgs {
   int M, N, act;
 };
 
-// A workgroup takes 256 columns and every gridDim.y-th set of 4 rows, a wave of them each, 4
-// neighbouring columns a lane.
-constexpr int kActThreads = 256;
+// A workgroup takes kActCols columns, 8 a lane, and every gridDim.y-th set of rows, one of its waves
+// each, two sets at a time.  VEC: rows are whole 16-byte blocks and a lane's columns neighbours;
+// elsewhere a lane has every 64th column.
+constexpr int kActThreads = 256, kActWaves = kActThreads / kWave;
 
+template <bool VEC>
 __global__ __launch_bounds__(kActThreads) void act_bwd_kernel(ActArgs g) {
-  __shared__ float part[kActThreads / kWave][kActCols];
+  static_assert(kActCols == 8 * kWave, "8 columns a lane");
+  __shared__ float part[kActWaves][kActCols];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int64_t n0 = (int64_t)blockIdx.x * kActCols + lane * 4;
-  const int left = (int)min((int64_t)4, g.N - n0);
-  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t m = (int64_t)blockIdx.y * 4 + wave; m < g.M; m += (int64_t)gridDim.y * 4) {
-    const int64_t at = m * g.N + n0;
+  const int c0 = blockIdx.x * kActCols;
+  auto col = [&](int i) { return VEC ? lane * 8 + i : lane + i * kWave; };
+  struct Eight {
+    uint32_t w[4];
+    __device__ __forceinline__ float get(int i) const {
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+  };
+  auto load = [&](const uint16_t* p, int64_t m) {
+    Eight e = {};
+    if (m >= g.M) return e;
+    p += m * g.N + c0;
+    if constexpr (VEC) {
+      if (c0 + lane * 8 >= g.N) return e;
+      const i32x4 v = *(const i32x4*)(p + lane * 8);
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) e.w[i] = (uint32_t)v[i];
+    } else {
+      #pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + col(i) < g.N) e.w[i / 2] |= (uint32_t)p[col(i)] << (16 * (i & 1));
+    }
+    return e;
+  };
+  float sum[8] = {};
+  const int64_t stride = (int64_t)gridDim.y * kActWaves;
+  for (int64_t m0 = (int64_t)blockIdx.y * kActWaves + wave; m0 < g.M; m0 += 2 * stride) {
+    Eight d[2], z[2];
     #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i >= left) break;
-      float d = bf16_bits_to_f32(g.d_c[at + i]);
-      if (g.act != MOE_ACT_NONE) {
-        d *= slope(bf16_bits_to_f32(g.pre[at + i]), g.act);
-        g.d_z[at + i] = (uint16_t)f32_to_bf16(d);
+    for (int u = 0; u < 2; ++u) {
+      d[u] = load(g.d_c, m0 + u * stride);
+      if (g.act != MOE_ACT_NONE) z[u] = load(g.pre, m0 + u * stride);
+    }
+    #pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t m = m0 + u * stride;
+      if (m >= g.M) break;
+      float v[8];
+      #pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = d[u].get(i);
+        if (g.act != MOE_ACT_NONE) v[i] *= slope(z[u].get(i), g.act);
+        sum[i] += v[i];
       }
-      sum[i] += d;
+      if (g.act == MOE_ACT_NONE) continue;
+      uint16_t* to = g.d_z + m * g.N + c0;
+      if constexpr (VEC) {
+        if (c0 + lane * 8 < g.N) *(i32x4*)(to + lane * 8) = pack8(v);
+      } else {
+        #pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c0 + col(i) < g.N) to[col(i)] = (uint16_t)f32_to_bf16(v[i]);
+      }
     }
   }
   if (!g.partials) return;
   #pragma unroll
-  for (int i = 0; i < 4; ++i) part[wave][lane * 4 + i] = sum[i];
+  for (int i = 0; i < 8; ++i) part[wave][col(i)] = sum[i];
   __syncthreads();
-  const int64_t n = (int64_t)blockIdx.x * kActCols + threadIdx.x;
-  if (n >= g.N) return;
-  float t = part[0][threadIdx.x];
-  #pragma unroll
-  for (int w = 1; w < kActThreads / kWave; ++w) t += part[w][threadIdx.x];
-  g.partials[(int64_t)blockIdx.y * g.N + n] = t;
+  for (int c = threadIdx.x; c < kActCols; c += kActThreads) {
+    if (c0 + c >= g.N) continue;
+    float t = part[0][c];
+    #pragma unroll
+    for (int w = 1; w < kActWaves; ++w) t += part[w][c];
+    g.partials[(int64_t)blockIdx.y * g.N + c0 + c] = t;
+  }
 }
 
 }  // namespace gb
@@ -774,8 +823,9 @@ hipError_t launch_act_bwd(int M, int N, int act, const void* d_c, const void* pr
   const int cus = std::max(device_cu_count(), 8);
   const int cols = (N + kActCols - 1) / kActCols;
   const int rows = act_partial_rows(M, N, cus);
-  hipLaunchKernelGGL(gb::act_bwd_kernel, dim3((unsigned)cols, (unsigned)rows),
-                     dim3(gb::kActThreads), 0, s, g);
+  const dim3 grid((unsigned)cols, (unsigned)rows), block(gb::kActThreads);
+  if (N % 8 == 0) hipLaunchKernelGGL(gb::act_bwd_kernel<true>, grid, block, 0, s, g);
+  else hipLaunchKernelGGL(gb::act_bwd_kernel<false>, grid, block, 0, s, g);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !d_bias) return e;
   return launch_sum_rows(rows, N, partials, d_bias, s);

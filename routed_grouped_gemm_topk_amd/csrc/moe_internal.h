@@ -50,6 +50,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
 }
 
+// exp(x) for |x| <= 100 from the base-2 exponential of gfx950 (2 u off, u = 2^-24): what the product
+// with log2 e rounds off, and that constant itself, is put back.  3 u off; 0 for results below 2^-126.
+__device__ __forceinline__ float exp_of(float x) {
+  const float t = x * 1.44269502f;
+  const float rest = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, 1.44269502f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, rest * 0.693147181f, e);
+}
+
 // OCP E4M3 ("fn") encode: round to nearest even, saturate to +-448, sign kept.
 // Written from the format: 4 exponent bits (bias 7), 3 mantissa bits, subnormal
 // step 2^-9, largest finite 1.75 * 2^8.
@@ -370,10 +379,10 @@ hipError_t launch_rms_norm_bwd(int T, int H, bool bf16, const void* d_y, const v
 hipError_t launch_sum_rows(int rows, int cols, const float* partials, float* out, hipStream_t s);
 // bf16 products with an epilogue and the epilogue's gradient (moe_gemm_bf16.hip).
 constexpr int kMaxUnits = 1024;     // compute units that a launch counts on, at most
-constexpr int kActCols = 256;       // columns of a workgroup of the epilogue's gradient
-// Its rows of workgroups, and of partial sums: as many as fill the units eight times.
+constexpr int kActCols = 512;       // columns of a workgroup of the epilogue's gradient
+// Its rows of workgroups, and of partial sums: as many as fill the units four times.
 inline int act_partial_rows(int M, int N, int cus) {
-  const int per_unit = (cus < kMaxUnits ? cus : kMaxUnits) * 8 / ((N + kActCols - 1) / kActCols);
+  const int per_unit = (cus < kMaxUnits ? cus : kMaxUnits) * 4 / ((N + kActCols - 1) / kActCols);
   int rows = (M + 3) / 4;
   rows = rows < kPartialRows ? rows : kPartialRows;
   rows = rows < per_unit ? rows : per_unit;

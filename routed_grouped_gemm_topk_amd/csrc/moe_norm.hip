@@ -6,8 +6,9 @@
 //   d_x = r (g - n' mean(g n')) + d_sum,  d_w = sum over rows of d_y n',   n' = s r, g = d_y w
 //
 // HBM bounds both: every row is read once and stays in registers.  TPR threads share a row, each
-// with NV chunks of 8 neighbouring columns: chunk v of thread i begins at column (v TPR + i) 8, so
-// that 16 neighbouring lanes hold one scale group.
+// with NV chunks of 8 columns.  Where rows are whole 16-byte blocks (VEC), chunk v of thread i begins
+// at column (v TPR + i) 8, so that 16 neighbouring lanes hold one scale group; elsewhere its k-th
+// column is (8 v + k) TPR + i, so that a wave's loads still are neighbours.
 #include <algorithm>
 #include <type_traits>
 
@@ -19,6 +20,7 @@ namespace moe {
 namespace nm {
 
 constexpr int kThreads = 256;     // of a workgroup, at least
+constexpr int kMaxGrid = 1 << 21;  // workgroups of a launch; more rows are run by striding
 
 struct Args {
   const void *x, *residual, *weight;
@@ -29,54 +31,56 @@ struct Args {
   float eps;
 };
 
-// Eight neighbouring values of a row as they lie in memory, and as fp32.  VEC: rows are whole
-// 16-byte blocks; n: values of the chunk that the row has.
-template <bool BF16, bool VEC>
+// Eight values of a row as they lie in memory, and as fp32; thread i's chunk v of a row that begins at
+// `row`.
+template <int TPR, bool BF16, bool VEC>
 struct Chunk {
   static constexpr int W = BF16 ? 4 : 8;
   uint32_t w[W];
 
-  __device__ __forceinline__ void load(const void* base, int64_t at, int n) {
+  __device__ static __forceinline__ int first(int v, int i) {
+    return VEC ? (v * TPR + i) * 8 : v * 8 * TPR + i;
+  }
+  // column of value k, if the row has it
+  template <class F>
+  __device__ static __forceinline__ void each(int H, int v, int i, F f) {
+    const int c = first(v, i);
     #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = 0;
+    for (int k = 0; k < 8; ++k)
+      if (c + (VEC ? k : k * TPR) < H) f(k, c + (VEC ? k : k * TPR));
+  }
+
+  __device__ __forceinline__ void load(const void* base, int64_t row, int H, int v, int i) {
+    #pragma unroll
+    for (int q = 0; q < W; ++q) w[q] = 0;
     if constexpr (VEC) {
-      if (n <= 0) return;
-      const i32x4* p = (const i32x4*)((const char*)base + at * (BF16 ? 2 : 4));
+      if (first(v, i) >= H) return;
+      const i32x4* p = (const i32x4*)((const char*)base + (row + first(v, i)) * (BF16 ? 2 : 4));
       #pragma unroll
       for (int q = 0; q < W / 4; ++q) {
-        const i32x4 v = p[q];
+        const i32x4 x = p[q];
         #pragma unroll
-        for (int i = 0; i < 4; ++i) w[4 * q + i] = (uint32_t)v[i];
+        for (int k = 0; k < 4; ++k) w[4 * q + k] = (uint32_t)x[k];
       }
-    } else if constexpr (BF16) {
-      const uint16_t* p = (const uint16_t*)base + at;
-      #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
     } else {
-      const uint32_t* p = (const uint32_t*)base + at;
-      #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) w[i] = p[i];
+      each(H, v, i, [&](int k, int c) {
+        if constexpr (BF16) w[k / 2] |= (uint32_t)((const uint16_t*)base)[row + c] << (16 * (k & 1));
+        else w[k] = ((const uint32_t*)base)[row + c];
+      });
     }
   }
-  __device__ __forceinline__ void store(void* base, int64_t at, int n) const {
+  __device__ __forceinline__ void store(void* base, int64_t row, int H, int v, int i) const {
     if constexpr (VEC) {
-      if (n <= 0) return;
-      i32x4* p = (i32x4*)((char*)base + at * (BF16 ? 2 : 4));
+      if (first(v, i) >= H) return;
+      i32x4* p = (i32x4*)((char*)base + (row + first(v, i)) * (BF16 ? 2 : 4));
       #pragma unroll
       for (int q = 0; q < W / 4; ++q)
         p[q] = i32x4{(int)w[4 * q], (int)w[4 * q + 1], (int)w[4 * q + 2], (int)w[4 * q + 3]};
-    } else if constexpr (BF16) {
-      uint16_t* p = (uint16_t*)base + at;
-      #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
     } else {
-      uint32_t* p = (uint32_t*)base + at;
-      #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = w[i];
+      each(H, v, i, [&](int k, int c) {
+        if constexpr (BF16) ((uint16_t*)base)[row + c] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+        else ((uint32_t*)base)[row + c] = w[k];
+      });
     }
   }
   __device__ __forceinline__ float get(int i) const {
@@ -114,42 +118,35 @@ __device__ __forceinline__ V row_sum(V v, V (*words)[TPR / kWave], int turn) {
 template <int TPR, int NV, bool BF16, bool VEC>
 __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kernel(Args g) {
   constexpr int ROWS = TPR < kThreads ? kThreads / TPR : 1;      // of a workgroup
-  using Row = Chunk<BF16, VEC>;
+  using Part = Chunk<TPR, BF16, VEC>;
   __shared__ double words[2][TPR / kWave];
   const int i = ROWS > 1 ? threadIdx.x % TPR : threadIdx.x;
   const int in_row = ROWS > 1 ? threadIdx.x / TPR : 0;
-  Row w[NV];
-  int n[NV];
+  Part w[NV];
   #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    n[v] = g.H - (v * TPR + i) * 8;
-    if (g.weight) w[v].load(g.weight, (v * TPR + i) * 8, n[v]);
-  }
+  for (int v = 0; v < NV; ++v)
+    if (g.weight) w[v].load(g.weight, 0, g.H, v, i);
   int turn = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < g.T; row0 += (int64_t)gridDim.x * ROWS) {
-    const int64_t row = row0 + in_row;
-    const bool live = row < g.T;                       // the same for a whole wave
-    const int64_t at = row * g.H + i * 8;
-    Row x[NV];
+  for (int64_t set = blockIdx.x; set * ROWS < g.T; set += gridDim.x) {
+    const int64_t t = set * ROWS + in_row, row = t * g.H;
+    const bool live = t < g.T;                         // the same for a whole wave
+    Part x[NV] = {};
     if (live) {
       #pragma unroll
-      for (int v = 0; v < NV; ++v) x[v].load(g.x, at + v * TPR * 8, n[v]);
+      for (int v = 0; v < NV; ++v) x[v].load(g.x, row, g.H, v, i);
       if (g.residual) {
-        Row r[NV];
+        Part r[NV];
         #pragma unroll
-        for (int v = 0; v < NV; ++v) r[v].load(g.residual, at + v * TPR * 8, n[v]);
+        for (int v = 0; v < NV; ++v) r[v].load(g.residual, row, g.H, v, i);
         #pragma unroll
         for (int v = 0; v < NV; ++v) {
           float s[8];
           #pragma unroll
           for (int k = 0; k < 8; ++k) s[k] = x[v].get(k) + r[v].get(k);
           x[v].set(s);
-          x[v].store(g.sum, at + v * TPR * 8, n[v]);
+          x[v].store(g.sum, row, g.H, v, i);
         }
       }
-    } else {
-      #pragma unroll
-      for (int v = 0; v < NV; ++v) x[v] = Row{};
     }
     // squares of fp32 values neither overflow nor vanish in 64 bits
     double sq = 0.0;
@@ -164,7 +161,7 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kern
     turn ^= 1;
     if (!live) continue;
     const float rstd = (float)rsqrt(sq / (double)g.H + (double)g.eps);
-    if (g.rstd && i == 0) g.rstd[row] = rstd;
+    if (g.rstd && i == 0) g.rstd[t] = rstd;
     #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float y[8];
@@ -174,9 +171,9 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kern
         if (g.weight) y[k] *= w[v].get(k);
       }
       if (g.y) {
-        Row o;
+        Part o;
         o.set(y);
-        o.store(g.y, at + v * TPR * 8, n[v]);
+        o.store(g.y, row, g.H, v, i);
       }
       if (VEC && g.codes) {
         float m = 0.0f;
@@ -188,7 +185,8 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kern
         m = fmaxf(m, dpp_xchg<0x141>(m));
         m = fmaxf(m, dpp_xchg<0x140>(m));
         const float s = m == 0.0f ? 1.0f : m / kE4M3Max;
-        if (n[v] > 0) {
+        const int c = Part::first(v, i);
+        if (c < g.H) {
           // quotients are at most 448 up to their rounding, below the 464 from which e4m3 would
           // overflow, so the convert (nearest even, NaN kept) needs no clamp
           uint32_t q[2];
@@ -197,8 +195,8 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kern
             q[h] = __builtin_amdgcn_cvt_pk_fp8_f32(
                 y[4 * h + 2] / s, y[4 * h + 3] / s,
                 __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h] / s, y[4 * h + 1] / s, 0, false), true);
-          *(uint2*)(g.codes + at + v * TPR * 8) = make_uint2(q[0], q[1]);
-          if ((i & 15) == 0) g.scales[row * (g.H / kGroup) + (v * TPR + i) / 16] = s;
+          *(uint2*)(g.codes + row + c) = make_uint2(q[0], q[1]);
+          if ((i & 15) == 0) g.scales[t * (g.H / kGroup) + c / kGroup] = s;
         }
       }
     }
@@ -215,67 +213,117 @@ struct BwdArgs {
 
 // A workgroup takes every gridDim.x-th set of rows and keeps its part of d_w in registers; its rows
 // (one per wave where TPR is a wave) are added through LDS at the end, then one row of partials.
+// Up to 16 values a thread, the rows stay in registers and the next ones are on
+// their way while a row's sum goes round (4096 x 4096: 42.5 -> 34.5 us).  Longer ones are loaded again,
+// from the caches, once the sum is known.
 template <int TPR, int NV, bool BF16, bool VEC>
 __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_bwd_kernel(BwdArgs g) {
   constexpr int ROWS = TPR < kThreads ? kThreads / TPR : 1;
-  using Row = Chunk<BF16, VEC>;
+  using Part = Chunk<TPR, BF16, VEC>;
+  constexpr bool HELD = NV * Part::W <= 16 && TPR < 1024;
   __shared__ float words[2][TPR / kWave];
   __shared__ float part[ROWS > 1 ? ROWS * TPR * 8 : 1];
   const int i = ROWS > 1 ? threadIdx.x % TPR : threadIdx.x;
   const int in_row = ROWS > 1 ? threadIdx.x / TPR : 0;
-  Row w[NV];
-  int n[NV];
   float dw[NV][8];
   #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    n[v] = g.H - (v * TPR + i) * 8;
-    if (g.weight) w[v].load(g.weight, (v * TPR + i) * 8, n[v]);
+  for (int v = 0; v < NV; ++v)
     #pragma unroll
     for (int k = 0; k < 8; ++k) dw[v][k] = 0.0f;
-  }
-  int turn = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < g.T; row0 += (int64_t)gridDim.x * ROWS) {
-    const int64_t row = row0 + in_row;
-    const bool live = row < g.T;
-    const int64_t at = row * g.H + i * 8;
-    Row dy[NV], s[NV], ds[NV];
-    float r = 0.0f;
-    if (live) {
-      r = g.rstd[row];
-      #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        dy[v].load(g.d_y, at + v * TPR * 8, n[v]);
-        s[v].load(g.sum, at + v * TPR * 8, n[v]);
-        if (g.d_sum) ds[v].load(g.d_sum, at + v * TPR * 8, n[v]);
-      }
-    } else {
-      #pragma unroll
-      for (int v = 0; v < NV; ++v) dy[v] = s[v] = Row{};
+  // one chunk's part of the sum of g n, and of d_w
+  auto gather = [&](const Part& dy, const Part& s, const Part& w, float r, float (&d_w)[8],
+                    float& dot) {
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float d = dy.get(k), norm = s.get(k) * r;
+      d_w[k] = __builtin_fmaf(d, norm, d_w[k]);
+      dot = __builtin_fmaf(g.weight ? d * w.get(k) : d, norm, dot);
     }
-    float dot = 0.0f;
+  };
+  auto finish = [&](const Part& dy, const Part& s, const Part& w, const Part& ds, float r, float dot,
+                    int64_t row, int v) {
+    float d[8];
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float gk = g.weight ? dy.get(k) * w.get(k) : dy.get(k);
+      d[k] = r * (gk - s.get(k) * r * dot);
+      if (g.d_sum) d[k] += ds.get(k);
+    }
+    Part o;
+    o.set(d);
+    o.store(g.d_x, row, g.H, v, i);
+  };
+  int turn = 0;
+  if constexpr (HELD) {
+    Part w[NV];
     #pragma unroll
     for (int v = 0; v < NV; ++v)
-      #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float d = dy[v].get(k), norm = s[v].get(k) * r;
-        dw[v][k] = __builtin_fmaf(d, norm, dw[v][k]);
-        dot = __builtin_fmaf(g.weight ? d * w[v].get(k) : d, norm, dot);
+      if (g.weight) w[v].load(g.weight, 0, g.H, v, i);
+    struct Row {
+      Part dy[NV], s[NV], ds[NV];
+      float r;
+    };
+    auto load = [&](Row& o, int64_t set) {
+      const int64_t t = set * ROWS + in_row, row = t * g.H;
+      if (t >= g.T) {
+        o.r = 0.0f;
+        #pragma unroll
+        for (int v = 0; v < NV; ++v) o.dy[v] = o.s[v] = Part{};
+        return;
       }
-    dot = row_sum<TPR>(dot, words, turn) / (float)g.H;
-    turn ^= 1;
-    if (!live) continue;
-    #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float d[8];
+      o.r = g.rstd[t];
       #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float gk = g.weight ? dy[v].get(k) * w[v].get(k) : dy[v].get(k);
-        d[k] = r * (gk - s[v].get(k) * r * dot);
-        if (g.d_sum) d[k] += ds[v].get(k);
+      for (int v = 0; v < NV; ++v) {
+        o.dy[v].load(g.d_y, row, g.H, v, i);
+        o.s[v].load(g.sum, row, g.H, v, i);
       }
-      Row o;
-      o.set(d);
-      o.store(g.d_x, at + v * TPR * 8, n[v]);
+      if (g.d_sum) {
+        #pragma unroll
+        for (int v = 0; v < NV; ++v) o.ds[v].load(g.d_sum, row, g.H, v, i);
+      }
+    };
+    Row cur, nxt;
+    load(cur, blockIdx.x);
+    for (int64_t set = blockIdx.x; set * ROWS < g.T; set += gridDim.x) {
+      load(nxt, set + gridDim.x);
+      float dot = 0.0f;
+      #pragma unroll
+      for (int v = 0; v < NV; ++v) gather(cur.dy[v], cur.s[v], w[v], cur.r, dw[v], dot);
+      dot = row_sum<TPR>(dot, words, turn) / (float)g.H;
+      turn ^= 1;
+      const int64_t t = set * ROWS + in_row;
+      if (t < g.T) {
+        #pragma unroll
+        for (int v = 0; v < NV; ++v)
+          finish(cur.dy[v], cur.s[v], w[v], cur.ds[v], cur.r, dot, t * g.H, v);
+      }
+      cur = nxt;
+    }
+  } else {
+    static_assert(HELD || ROWS == 1, "every thread has a row");
+    for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
+      const int64_t row = t * g.H;
+      const float r = g.rstd[t];
+      float dot = 0.0f;
+      #pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        Part dy, s, w = {};
+        dy.load(g.d_y, row, g.H, v, i);
+        s.load(g.sum, row, g.H, v, i);
+        if (g.weight) w.load(g.weight, 0, g.H, v, i);
+        gather(dy, s, w, r, dw[v], dot);
+      }
+      dot = row_sum<TPR>(dot, words, turn) / (float)g.H;
+      turn ^= 1;
+      #pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        Part dy, s, w = {}, ds = {};
+        dy.load(g.d_y, row, g.H, v, i);
+        s.load(g.sum, row, g.H, v, i);
+        if (g.weight) w.load(g.weight, 0, g.H, v, i);
+        if (g.d_sum) ds.load(g.d_sum, row, g.H, v, i);
+        finish(dy, s, w, ds, r, dot, row, v);
+      }
     }
   }
   if (!g.partials) return;
@@ -287,17 +335,13 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_bwd_
       #pragma unroll
       for (int k = 0; k < 8; ++k) part[(in_row * TPR + i) * 8 + k] = dw[v][k];
       __syncthreads();
-      for (int c = threadIdx.x; c < TPR * 8; c += kThreads) {
-        float t = part[c];
-        #pragma unroll
-        for (int q = 1; q < ROWS; ++q) t += part[q * TPR * 8 + c];
-        if (v * TPR * 8 + c < g.H) out[v * TPR * 8 + c] = t;
-      }
-    } else {
+      if (in_row > 0) continue;
       #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n[v]) out[(v * TPR + i) * 8 + k] = dw[v][k];
+      for (int q = 1; q < ROWS; ++q)
+        #pragma unroll
+        for (int k = 0; k < 8; ++k) dw[v][k] += part[(q * TPR + i) * 8 + k];
     }
+    Part::each(g.H, v, i, [&](int k, int c) { out[c] = dw[v][k]; });
   }
 }
 
@@ -310,9 +354,24 @@ __global__ __launch_bounds__(kSumWaves * kWave) void sum_rows_kernel(
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int64_t c = (int64_t)blockIdx.x * kWave + lane;
   const int per = (rows + kSumWaves - 1) / kSumWaves;
+  const int end = min(rows, (wave + 1) * per);
   float t = 0.0f;
-  if (c < cols)
-    for (int r = wave * per; r < min(rows, (wave + 1) * per); ++r) t += partials[(int64_t)r * cols + c];
+  if (c < cols) {
+    const float* p = partials + c;
+    int r = wave * per;
+    for (; r + 8 <= end; r += 8) {
+      float v[8];
+      #pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = p[(int64_t)(r + k) * cols];
+      #pragma unroll
+      for (int k = 0; k < 8; ++k) t += v[k];
+    }
+    float v[8];
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = r + k < end ? p[(int64_t)(r + k) * cols] : 0.0f;
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) t += v[k];
+  }
   part[wave][lane] = t;
   __syncthreads();
   if (wave > 0 || c >= cols) return;
@@ -323,7 +382,7 @@ __global__ __launch_bounds__(kSumWaves * kWave) void sum_rows_kernel(
 
 // Calls f(TPR, NV, VEC) as compile-time constants for rows of H values.
 template <class F>
-hipError_t by_width(int T, int H, F f) {
+hipError_t by_width(int H, F f) {
   using std::integral_constant;
   const bool vec = H % 8 == 0;
   auto with = [&](auto tpr, auto nv) {
@@ -334,13 +393,14 @@ hipError_t by_width(int T, int H, F f) {
   const integral_constant<int, 4> four{};
   const integral_constant<int, 64> wave{};
   const integral_constant<int, 256> four_waves{};
+  const integral_constant<int, 512> eight_waves{};
   const integral_constant<int, 1024> all{};
   if (H <= 512) return with(wave, one);
   if (H <= 1024) return with(wave, two);
   if (H <= 2048) return with(four_waves, one);
   if (H <= 4096) return with(four_waves, two);
-  if (H <= 8192) return with(all, one);
-  if (H <= 16384) return with(all, two);
+  if (H <= 8192) return with(eight_waves, two);
+  if (H <= 16384) return with(eight_waves, four);
   return with(all, four);
 }
 
@@ -350,13 +410,12 @@ hipError_t launch_rms_norm(int T, int H, bool bf16, const void* x, const void* r
                            const void* weight, float eps, void* sum, void* y, uint8_t* codes,
                            float* scales, float* rstd, hipStream_t s) {
   nm::Args a{x, residual, weight, sum, y, codes, scales, rstd, T, H, eps};
-  const int cus = std::max(device_cu_count(), 8);
-  return nm::by_width(T, H, [&](auto tpr, auto nv, auto vec) {
+  return nm::by_width(H, [&](auto tpr, auto nv, auto vec) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     constexpr bool VEC = decltype(vec)::value;
     constexpr int TH = std::max(TPR, nm::kThreads), ROWS = TH / TPR;
     const int64_t sets = ((int64_t)T + ROWS - 1) / ROWS;
-    const unsigned grid = (unsigned)std::min<int64_t>(sets, (int64_t)cus * (2048 / TH) * 2);
+    const unsigned grid = (unsigned)std::min<int64_t>(sets, nm::kMaxGrid);
     if (bf16)
       hipLaunchKernelGGL((nm::rms_norm_kernel<TPR, NV, true, VEC>), dim3(grid), dim3(TH), 0, s, a);
     else
@@ -377,7 +436,7 @@ hipError_t launch_rms_norm_bwd(int T, int H, bool bf16, const void* d_y, const v
   nm::BwdArgs a{d_y, d_sum, sum, weight, rstd, d_x, d_weight ? partials : nullptr, T, H};
   const int cus = std::max(device_cu_count(), 8);
   unsigned grid = 0;
-  const hipError_t e = nm::by_width(T, H, [&](auto tpr, auto nv, auto vec) {
+  const hipError_t e = nm::by_width(H, [&](auto tpr, auto nv, auto vec) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     constexpr bool VEC = decltype(vec)::value;
     constexpr int TH = std::max(TPR, nm::kThreads), ROWS = TH / TPR;

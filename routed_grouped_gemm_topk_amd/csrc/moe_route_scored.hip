@@ -61,15 +61,6 @@ __device__ __forceinline__ float wave_max(float v) {
   return wave_allreduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// exp(x) for |x| <= 100 from the base-2 exponential of gfx950 (2 u off, u = 2^-24): what the product
-// with log2 e rounds off, and that constant itself, is put back.  3 u off; 0 for results below 2^-126.
-__device__ __forceinline__ float exp_of(float x) {
-  const float t = x * 1.44269502f;
-  const float rest = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, 1.44269502f, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, rest * 0.693147181f, e);
-}
-
 // 1 / (1 + exp(-l)): 6 u off (3 u, 1 u for the addition, 2 u for the reciprocal), and 0 below 2^-126.
 __device__ __forceinline__ float sigmoid_of(float l) {
   return __builtin_amdgcn_rcpf(1.0f + exp_of(__builtin_amdgcn_fmed3f(-l, -88.0f, 88.0f)));
