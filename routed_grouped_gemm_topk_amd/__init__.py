@@ -161,6 +161,13 @@ def _new(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
         return like.new_empty(shape, dtype=dtype)
 
 
+def _vec(like: torch.Tensor, n: int, dtype: torch.dtype, stream) -> torch.Tensor:
+    """The same for n values in a row."""
+    if stream is None:
+        return torch.empty_strided((n,), (1,), dtype=dtype, device=like.device)
+    return _new(like, (1, n), dtype, stream).view(n)
+
+
 def permute(p: Problem, x: torch.Tensor, a: dict, x_scales: Optional[torch.Tensor] = None,
             rows: Optional[torch.Tensor] = None, row_scales: Optional[torch.Tensor] = None,
             stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
@@ -277,22 +284,22 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     """Root-mean-square norm of the rows of x (plus residual) through moe_rms_norm.  `want` names
     the outputs: "y" (rows), "codes" (e4m3 codes, with "scales" per 128 columns) and "rstd" (for
     rms_norm_bwd); with a residual "sum" comes too, in `sum` if given (residual or x, say)."""
-    for name in want:
-        if name not in ("y", "codes", "rstd"):
-            raise ValueError(f"want: {name!r}, expected 'y', 'codes' or 'rstd'")
-    t, h = x.shape
+    shape = t, h = x.shape
     out = {}
     if residual is not None:
-        out["sum"] = sum if sum is not None else _new(x, (t, h), x.dtype, stream)
+        out["sum"] = sum if sum is not None else _new(x, shape, x.dtype, stream)
     elif sum is not None:
         raise ValueError("sum: given without a residual")
-    if "y" in want:
-        out["y"] = _new(x, (t, h), x.dtype, stream)
-    if "codes" in want:
-        out["codes"] = _new(x, (t, h), torch.float8_e4m3fn, stream)
-        out["scales"] = _new(x, (t, h // 128), torch.float32, stream)
-    if "rstd" in want:
-        out["rstd"] = _new(x, (1, t), torch.float32, stream).view(t)
+    for name in want:
+        if name == "y":
+            out["y"] = _new(x, shape, x.dtype, stream)
+        elif name == "codes":
+            out["codes"] = _new(x, shape, torch.float8_e4m3fn, stream)
+            out["scales"] = _new(x, (t, h // 128), torch.float32, stream)
+        elif name == "rstd":
+            out["rstd"] = _vec(x, t, torch.float32, stream)
+        else:
+            raise ValueError(f"want: {name!r}, expected 'y', 'codes' or 'rstd'")
     get = out.get
     moe_rms_norm(x, residual, weight, eps, get("sum"), get("y"), get("codes"), get("scales"),
                  get("rstd"), stream)
@@ -312,9 +319,9 @@ def rms_norm_bwd(d_y: torch.Tensor, s: torch.Tensor, weight: Optional[torch.Tens
         d_x = _new(d_y, (t, h), d_y.dtype, stream)
     dw = None
     if d_weight:
-        dw = _new(d_y, (1, h), torch.float32, stream).view(h)
+        dw = _vec(d_y, h, torch.float32, stream)
         if workspace is None:
-            workspace = _new(d_y, (1, moe_rms_norm_bwd_workspace_bytes(t, h)), torch.uint8, stream)
+            workspace = _vec(d_y, moe_rms_norm_bwd_workspace_bytes(t, h), torch.uint8, stream)
     moe_rms_norm_bwd(d_y, d_sum, s, weight, rstd, d_x, dw, workspace if d_weight else None, stream)
     return d_x, dw
 
@@ -351,8 +358,8 @@ def act_bwd(d_c: torch.Tensor, pre: Optional[torch.Tensor] = None, act: str = "n
         d_z = _new(d_c, (m, n), torch.bfloat16, stream)
     db = None
     if d_bias:
-        db = _new(d_c, (1, n), torch.float32, stream).view(n)
+        db = _vec(d_c, n, torch.float32, stream)
         if workspace is None:
-            workspace = _new(d_c, (1, moe_act_bwd_workspace_bytes(m, n)), torch.uint8, stream)
+            workspace = _vec(d_c, moe_act_bwd_workspace_bytes(m, n), torch.uint8, stream)
     moe_act_bwd(act, d_c, pre, d_z, db, workspace if d_bias else None, stream)
     return (d_c if none else d_z), db

@@ -599,10 +599,12 @@ def moe_route_scored_bwd(p: Problem, r: Router, logits, topk_ids, d_weights, d_l
 
 
 def _rows(x, name: str, where: str):
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+    shape = x.shape if isinstance(x, torch.Tensor) else ()
+    if len(shape) != 2:
         raise ValueError(f"{name}: expected a matrix")
-    _refuse_past_int32(where, *x.shape)
-    return x.shape
+    if (shape[0] | shape[1]) > 0x7FFFFFFF:
+        raise MoeError(MOE_ERR_SHAPE, where)
+    return shape
 
 
 def moe_rms_norm(x, residual, weight, eps: float, sum, y, codes, scales, rstd,
@@ -647,28 +649,33 @@ def moe_rms_norm_bwd(d_y, d_sum, s, weight, rstd, d_x, d_weight, workspace, stre
 
 
 def _named(value, names: dict, what: str) -> int:
-    got = names.get(value, value) if isinstance(value, str) else value
-    if isinstance(got, str):
+    """The number of a name; a number stands for itself."""
+    if isinstance(value, str):
         raise ValueError(f"{what}: {value!r}, expected one of {', '.join(names)}")
-    return int(got)
+    return int(value)
 
 
 def moe_gemm_bf16(layout, a, b, bias, act, residual, pre, c, stream=None) -> None:
-    layout, act = _named(layout, _LAYOUT, "layout"), _named(act, _ACT, "act")
-    if layout not in _LAYOUT.values():
-        raise MoeError(MOE_ERR_SHAPE, "moe_gemm_bf16")
+    lay = _LAYOUT.get(layout)
+    if lay is None:
+        lay = _named(layout, _LAYOUT, "layout")
+        if lay not in _LAYOUT.values():
+            raise MoeError(MOE_ERR_SHAPE, "moe_gemm_bf16")
+    ac = _ACT.get(act)
+    if ac is None:
+        ac = _named(act, _ACT, "act")
     a0, a1 = _rows(a, "a", "moe_gemm_bf16")
     b0, b1 = _rows(b, "b", "moe_gemm_bf16")
-    m, k = (a1, a0) if layout == MOE_TN else (a0, a1)
-    n, kb = (b0, b1) if layout == MOE_NT else (b1, b0)
+    m, k = (a1, a0) if lay == MOE_TN else (a0, a1)
+    n, kb = (b0, b1) if lay == MOE_NT else (b1, b0)
     if k != kb:
         raise ValueError(f"b: shape {tuple(b.shape)}, its k is {kb}, that of a is {k}")
     dev = _device()
     shape = (m, n)
     dt = _row_dtype(c, "c")
     _checked(load().moe_gemm_bf16(
-        m, n, k, layout, _arg(a, "a", _BF16, m * k, dev), _arg(b, "b", _BF16, n * k, dev),
-        _arg(bias, "bias", _F32, n, dev), act, _mat(residual, "residual", (c.dtype,), shape, dev),
+        m, n, k, lay, _arg(a, "a", _BF16, m * k, dev), _arg(b, "b", _BF16, n * k, dev),
+        _arg(bias, "bias", _F32, n, dev), ac, _mat(residual, "residual", (c.dtype,), shape, dev),
         _mat(pre, "pre", _BF16, shape, dev), _mat(c, "c", _OUT, shape, dev), dt,
         _where(stream, dev)), "moe_gemm_bf16")
 
@@ -681,8 +688,11 @@ def moe_act_bwd_workspace_bytes(m: int, n: int) -> int:
 def moe_act_bwd(act, d_c, pre, d_z, d_bias, workspace, stream=None) -> None:
     m, n = shape = _rows(d_c, "d_c", "moe_act_bwd")
     dev = _device()
+    ac = _ACT.get(act)
+    if ac is None:
+        ac = _named(act, _ACT, "act")
     _checked(load().moe_act_bwd(
-        m, n, _named(act, _ACT, "act"), _arg(d_c, "d_c", _BF16, m * n, dev),
+        m, n, ac, _arg(d_c, "d_c", _BF16, m * n, dev),
         _mat(pre, "pre", _BF16, shape, dev), _mat(d_z, "d_z", _BF16, shape, dev),
         _arg(d_bias, "d_bias", _F32, n, dev), *_space(workspace, dev), _where(stream, dev)),
         "moe_act_bwd")
