@@ -315,10 +315,11 @@ struct TileGemm {
     const i32x4 ra = buf_rsrc(g.a + (size_t)t.m0 * K, (uint32_t)t.rows * (uint32_t)K * 2);
     const i32x4 rb = buf_rsrc(g.b + (size_t)t.n0 * K, (uint32_t)t.cols * (uint32_t)K * 2);
     // the descriptor of 64 rows of k of an operand whose rows are k
-    auto rows_of_k = [&](const uint16_t* p, int ld, int64_t first, int kt) {
-      const int left = min(max(K - kt * kSlice, 0), kSlice);
-      return buf_rsrc(p + (size_t)min(kt, KT) * kSlice * ld + first,
-                      left > 0 ? (uint32_t)(left * (int64_t)ld - first) * 2 : 0u);
+    auto rows_of_k = [&](auto ends, const uint16_t* p, int ld, int64_t first, int kt) {
+      constexpr bool ENDS = decltype(ends)::value;
+      const int left = ENDS ? min(max(K - kt * kSlice, 0), kSlice) : kSlice;
+      const uint32_t bytes = (uint32_t)max((int64_t)left * ld - first, (int64_t)0) * 2;
+      return buf_rsrc(p + (size_t)(ENDS ? min(kt, KT) : kt) * kSlice * ld + first, bytes);
     };
     const int kc = ((lane & 7) ^ (lane >> 3)) * 8;           // k of the lane's chunk, even copies
     // where copy q of an operand's slice (8 of its rows, or 8 rows of k of a panel) lies
@@ -348,12 +349,12 @@ struct TileGemm {
     };
     auto copy_a = [&](auto ends, int buf, int step, int i) {
       i32x4 r = ra;
-      if constexpr (!KA) r = rows_of_k(g.a, g.M, t.m0, step * KG + kg);
+      if constexpr (!KA) r = rows_of_k(ends, g.a, g.M, t.m0, step * KG + kg);
       copy(ends, ContA{}, r, va[i], wave * CA + i, step, (uint32_t)((buf * KG + kg) * STAGE_A));
     };
     auto copy_b = [&](auto ends, int buf, int step, int i) {
       i32x4 r = rb;
-      if constexpr (!KB) r = rows_of_k(g.b, g.N, t.n0, step * KG + kg);
+      if constexpr (!KB) r = rows_of_k(ends, g.b, g.N, t.n0, step * KG + kg);
       copy(ends, ContB{}, r, vb[i], wave * CB + i, step,
            (uint32_t)(RING_B + (buf * KG + kg) * STAGE_B));
     };
@@ -399,10 +400,9 @@ struct TileGemm {
         if (u >= BNEXT) read_b(0, u - BNEXT, 2);       // the next slice's
         if (u <= LAST) copy_tail(ends, pa, pb, step - 1 + NSA, step - 1 + NSB, EARLY + u);
         else copy_tail(ends, ba, bb, step + NSA, step + NSB, u - LAST - 1);
-        if (SOON && u > BFREE)
-          #pragma unroll
-          for (int i = 2 * (u - BFREE - 1); i < std::min(CB, 2 * (u - BFREE)); ++i)
-            copy_b(ends, bb, step + NSB, i);
+        #pragma unroll
+        for (int i = 0; i < CB; ++i)
+          if (SOON && u > BFREE && i / 2 == u - BFREE - 1) copy_b(ends, bb, step + NSB, i);
         #pragma unroll
         for (int j = 0; j < FN; ++j)
           acc[u % FM][j] = OpBf16::mma(bf[u / FM][j], af[u % (AHEAD + 1)], acc[u % FM][j]);

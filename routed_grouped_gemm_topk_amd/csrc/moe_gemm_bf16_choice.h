@@ -53,10 +53,10 @@ inline bool fits_blocks(int M, int N, int K, bool ka, bool kb) {
 
 // Time of a product in ns: `fixed`, and for every round of one workgroup per unit `round` and per
 // slice of k `slice`.  Fitted to 1500 shapes of 1 to 9000 rows, 16 to 16000 columns and k of 128 to
-// 9600 (rms 5-17%, the most where the launch is most of it).  On 700 shapes of the same range that
-// they were not fitted to, the kernel chosen takes 0.4% more than the best of each on average, at
-// most 1.9% in 19 of 20, at worst 35% (448 x 424 x 224: 7.3 against 5.4 us).  Without any one of the
-// kernels that is 0.5% to 6.3%.
+// 9600 (rms 7-17%, the most where the launch is most of it).  On 700 shapes of the same range that
+// they were not fitted to, the kernel chosen takes 0.7% more than the best of each on average, at
+// most 4% in 19 of 20, at worst 42% (105 x 64 x 296: 7.5 against 5.3 us).  Without any one of the
+// kernels that is 0.8% to 6.6%.
 struct Price {
   int fixed, round, slice;      // round 0: the kernel does not take the layout
 };
@@ -67,20 +67,20 @@ struct Prices {
 };
 constexpr Prices kPrices[3] = {
     // a b^T
-    {{{0, 0, 0}, {2174, 2290, 43}, {1763, 2715, 63}, {1657, 3004, 112}, {1118, 3567, 141},
-      {2578, 2300, 796}, {-370, 5578, 430}, {-3060, 9918, 640}, {-3608, 11889, 680},
-      {-4812, 14077, 944}, {-6176, 17609, 1147}},
-     {0, 1801, 237}, {0, 9918, 640}},
+    {{{0, 0, 0}, {2310, 2231, 42}, {1888, 2692, 61}, {1701, 3000, 112}, {1155, 3556, 140},
+      {2656, 2315, 790}, {-325, 5585, 429}, {-3099, 9981, 640}, {-3528, 11839, 680},
+      {-5239, 14066, 878}, {-7190, 18056, 1047}},
+     {0, 1802, 235}, {0, 7500, 1000}},
     // a b
-    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1687, 3044, 141}, {1435, 3405, 168}, {2210, 3283, 734},
-      {246, 5363, 451}, {-943, 8479, 690}, {-1679, 10217, 707}, {-2008, 11482, 1054},
-      {-2022, 13749, 1219}},
-     {0, 2397, 285}, {0, 8479, 690}},
+    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1611, 3405, 128}, {1466, 3583, 158}, {2106, 3511, 735},
+      {132, 5949, 420}, {-1141, 9202, 616}, {-1777, 10684, 682}, {-2593, 12172, 833},
+      {-6485, 17865, 1066}},
+     {0, 2921, 255}, {0, 7500, 1000}},
     // a^T b
-    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1426, 3427, 224}, {3314, 2772, 775},
-      {325, 5341, 565}, {-1510, 8693, 816}, {-2780, 11154, 830}, {-2898, 12178, 1164},
-      {-4967, 15735, 1420}},
-     {0, 1315, 341}, {0, 8693, 816}}};
+    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1023, 4165, 180}, {3263, 3131, 748},
+      {-213, 6474, 436}, {-2273, 10140, 658}, {-3576, 12594, 686}, {-4274, 13851, 888},
+      {-6245, 17291, 1147}},
+     {0, 1759, 292}, {0, 7500, 1000}}};
 
 inline Kernel choose(int M, int N, int K, bool ka, bool kb, int cus) {
   if (!fits_blocks(M, N, K, ka, kb)) return kAny;
