@@ -63,74 +63,8 @@ __device__ __forceinline__ void finish(const Args& g, const float* acc, int64_t 
   }
 }
 
-// Any sizes and any alignment of the rows: 64x64 tiles, 32 values of k a step, elements loaded one
-// by one, zeros past the ends.
-constexpr int kAnyThreads = 256;
-constexpr int kAnyTile = 64, kAnyK = 32;
-constexpr int64_t kAnyGrid = 1 << 22;    // workgroups of a launch; more tiles are run by striding
-
-// KA, KB: k is the contiguous dimension of a, of b.
-template <bool KA, bool KB>
-__global__ __launch_bounds__(kAnyThreads) void any_kernel(Args g) {
-  constexpr int PITCH = kAnyK + 8;                     // values
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2][kAnyTile * PITCH];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int wm = wave / 2 * 32, wn = wave % 2 * 32;
-  const int fr = lane & 15, fq = lane >> 4;
-  const int64_t nblk = ((int64_t)g.N + kAnyTile - 1) / kAnyTile;
-  const int64_t tiles = ((int64_t)g.M + kAnyTile - 1) / kAnyTile * nblk;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t m0 = tile / nblk * kAnyTile;
-    const int n0 = (int)(tile % nblk * kAnyTile);
-    f32x4 acc[2][2] = {};
-    for (int k0 = 0; k0 < g.K; k0 += kAnyK) {
-      auto fill = [&](uint16_t* to, const uint16_t* p, bool kc, int64_t r0, int64_t rows) {
-        #pragma unroll
-        for (int i = 0; i < kAnyTile * kAnyK / kAnyThreads; ++i) {
-          const int q = i * kAnyThreads + threadIdx.x;
-          const int k = kc ? q % kAnyK : q / kAnyTile, r = kc ? q / kAnyK : q % kAnyTile;
-          const bool in = r0 + r < rows && k0 + k < g.K;
-          to[r * PITCH + k] =
-              in ? p[kc ? (r0 + r) * g.K + k0 + k : (int64_t)(k0 + k) * rows + r0 + r] : 0;
-        }
-      };
-      fill(lds[0], g.a, KA, m0, g.M);
-      fill(lds[1], g.b, KB, n0, g.N);
-      __syncthreads();
-      #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const bf16x8 a = OpBf16::load((const char*)&lds[0][(wm + i * 16 + fr) * PITCH + fq * 8]);
-          const bf16x8 b = OpBf16::load((const char*)&lds[1][(wn + j * 16 + fr) * PITCH + fq * 8]);
-          acc[i][j] = OpBf16::mma(b, a, acc[i][j]);
-        }
-      __syncthreads();
-    }
-    #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t m = m0 + wm + i * 16 + fr;
-        const int n = n0 + wn + j * 16 + fq * 4;
-        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        if (m < g.M) finish<4>(g, v, m, n, g.N - n);
-      }
-  }
-}
-
-hipError_t run_any(const Args& g, int layout, hipStream_t s) {
-  const int64_t tiles = ((int64_t)g.M + kAnyTile - 1) / kAnyTile *
-                        (((int64_t)g.N + kAnyTile - 1) / kAnyTile);
-  const dim3 grid((unsigned)std::min(tiles, kAnyGrid)), block(kAnyThreads);
-  if (layout == MOE_NT) hipLaunchKernelGGL((any_kernel<true, true>), grid, block, 0, s, g);
-  else if (layout == MOE_NN) hipLaunchKernelGGL((any_kernel<true, false>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((any_kernel<false, false>), grid, block, 0, s, g);
-  return hipGetLastError();
-}
-
 // ---------------------------------------------------------------------------------------------
-// Rows of whole 16-byte blocks
+// Tiles of c through LDS
 // ---------------------------------------------------------------------------------------------
 constexpr int ROWB = 128;       // bytes of a row of LDS
 constexpr int kGroupM = 8;      // m-blocks that sweep the n-blocks together
@@ -450,8 +384,113 @@ struct TileGemm {
     for (; step < whole; ++step) slice(std::false_type{}, step);
     for (; step < steps; ++step) slice(std::true_type{}, step);
     wait_vmcnt<0>();
+    __syncthreads();
+    finish_tile(g, t, lds, acc, kg, wave, lane);
+  }
 
-    __syncthreads();              // the ring is done with
+  // The same tile from rows of any alignment: a thread loads its chunks of 16 bytes into registers, two
+  // steps ahead, values past the operands' ends as zeros, and stores them to the stage of the step
+  // after; two stages of each operand.
+  __device__ static __forceinline__ void run_any(const Args& g, const Tile& t, char* lds) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int kg = all / NW, wave = all % NW;
+    const int wn = wave % WN, wm = wave / WN;
+    const int K = g.K, steps = ((K + kSlice - 1) / kSlice + KG - 1) / KG;
+    constexpr int PA = BM * 8 / (NW * kWave), PB = BN * 8 / (NW * kWave);    // a thread's chunks
+    static_assert(BM * 8 % (NW * kWave) == 0 && BN * 8 % (NW * kWave) == 0, "whole chunks");
+    const int me = wave * kWave + lane;
+    // chunk q of an operand: its place in a stage
+    auto place = [](bool contiguous, int q) {
+      const int c = q & 7;
+      if (contiguous) return (q >> 3) * ROWB + ((c ^ swz(q >> 3)) << 4);
+      const int k = (q >> 3) & 63;
+      const int f = ((k >> 1) & 1) | ((k >> 4) & 1) << 1;
+      return (q >> 9) * 64 * ROWB + k * ROWB + ((c ^ (2 * f)) << 4);
+    };
+    auto load = [&](bool contiguous, const uint16_t* p, int64_t first, int64_t rows, int q, int k0) {
+      i32x4 v = {0, 0, 0, 0};
+      const int c = q & 7;
+      int64_t at;
+      int left;
+      if (contiguous) {
+        const int64_t r = first + (q >> 3);
+        at = r * K + k0 + c * 8;
+        left = r < rows ? K - k0 - c * 8 : 0;
+      } else {
+        const int k = k0 + ((q >> 3) & 63);
+        const int64_t n = first + (q >> 9) * 64 + c * 8;
+        at = (int64_t)k * rows + n;
+        left = k < K ? (int)min(rows - n, (int64_t)8) : 0;
+      }
+      if (left >= 8) {
+        __builtin_memcpy(&v, p + at, 16);              // of 2-byte alignment
+      } else {
+        #pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < left) v[i / 2] |= (int)((uint32_t)p[at + i] << (16 * (i & 1)));
+      }
+      return v;
+    };
+    i32x4 a[PA], b[PB];
+    auto load_step = [&](int step) {
+      const int k0 = min(step * KG + kg, 1 << 24) * kSlice;
+      #pragma unroll
+      for (int i = 0; i < PA; ++i) a[i] = load(KA, g.a, t.m0, g.M, i * NW * kWave + me, k0);
+      #pragma unroll
+      for (int i = 0; i < PB; ++i) b[i] = load(KB, g.b, t.n0, g.N, i * NW * kWave + me, k0);
+    };
+    constexpr int STAGE = STAGE_A + STAGE_B;
+    auto store_step = [&](int buf) {
+      char* st = lds + (buf * KG + kg) * STAGE;
+      #pragma unroll
+      for (int i = 0; i < PA; ++i)
+        *reinterpret_cast<i32x4*>(st + place(KA, i * NW * kWave + me)) = a[i];
+      #pragma unroll
+      for (int i = 0; i < PB; ++i)
+        *reinterpret_cast<i32x4*>(st + STAGE_A + place(KB, i * NW * kWave + me)) = b[i];
+    };
+    Where<KA, WTM, FM> wa;
+    Where<KB, WTN, FN> wb;
+    wa.init(kg * STAGE, wm, lane);
+    wb.init(kg * STAGE + STAGE_A, wn, lane);
+    f32x4 acc[FM][FN];
+    #pragma unroll
+    for (int i = 0; i < FM; ++i)
+      #pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    load_step(0);
+    store_step(0);
+    load_step(1);
+    __syncthreads();
+    for (int step = 0; step < steps; ++step) {
+      store_step((step + 1) & 1);                      // read last in the step before
+      load_step(step + 2);
+      #pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bf16x8 bf[FN];
+        #pragma unroll
+        for (int j = 0; j < FN; ++j) bf[j] = wb.read(lds, j, h);
+        #pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const bf16x8 af = wa.read(lds, i, h);
+          #pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = OpBf16::mma(bf[j], af, acc[i][j]);
+        }
+      }
+      __syncthreads();
+      const uint32_t d = (uint32_t)(step & 1 ? -KG * STAGE : KG * STAGE);
+      wa.step(d);
+      wb.step(d);
+    }
+    finish_tile(g, t, lds, acc, kg, wave, lane);
+  }
+
+  // The sums of the k-groups, the epilogue, and c.  The stages are done with.
+  __device__ static __forceinline__ void finish_tile(const Args& g, const Tile& t, char* lds,
+                                                     f32x4 (&acc)[FM][FN], int kg, int wave,
+                                                     int lane) {
+    const int wn = wave % WN, wm = wave / WN;
     if constexpr (KG > 1) {
       f32x4* sums = reinterpret_cast<f32x4*>(lds);
       auto at = [&](int g_, int i, int j) {
@@ -531,6 +570,26 @@ __global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void tile_kernel(Args g)
   const int logical = xcd_logical(blockIdx.x, mblk * nblk);
   if (logical < 0) return;
   G::run(g, tile_at<BM, BN>(g, logical), lds);
+}
+
+// Rows of any alignment and sizes past the other kernels' offsets.
+constexpr int64_t kAnyGrid = 1 << 21;    // workgroups of a launch; more tiles are run by striding
+
+template <int BM, int BN, int WM, int WN, int KG, bool KA, bool KB>
+__global__ __launch_bounds__(WM * WN * KG * kWave) void any_kernel(Args g) {
+  using G = TileGemm<BM, BN, WM, WN, KG, 2, 2, KA, KB>;
+  __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
+  const int64_t nblk = ((int64_t)g.N + BN - 1) / BN;
+  const int64_t tiles = ((int64_t)g.M + BM - 1) / BM * nblk;
+  for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+    Tile t;
+    t.m0 = i / nblk * BM;
+    t.n0 = (int)(i % nblk * BN);
+    t.rows = (int)min((int64_t)BM, (int64_t)g.M - t.m0);
+    t.cols = min(BN, g.N - t.n0);
+    __syncthreads();
+    G::run_any(g, t, lds);
+  }
 }
 
 // 256x256 tiles in rounds of one workgroup per compute unit, the first `whole` of them whole, the others
@@ -667,6 +726,14 @@ struct Run {
                        dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(WM * WN * KG * kWave), 0, s, a);
     return hipGetLastError();
   }
+  template <int BM, int BN, int WM, int WN, int KG>
+  static hipError_t any(const Args& a, hipStream_t s) {
+    const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
+    hipLaunchKernelGGL((any_kernel<BM, BN, WM, WN, KG, KA, KB>),
+                       dim3((unsigned)std::min(tiles, kAnyGrid)), dim3(WM * WN * KG * kWave), 0, s,
+                       a);
+    return hipGetLastError();
+  }
   static hipError_t large(const Args& a, int cus, hipStream_t s) {
     const int64_t tiles = tiles_of(kTile256x256, a.M, a.N), whole = whole_tiles(tiles, cus);
     const int64_t whole_grid = (whole + 7) / 8 * 8, halves = ((tiles - whole) * 2 + 7) / 8 * 8;
@@ -674,9 +741,10 @@ struct Run {
                        s, a, (int)whole, (int)whole_grid);
     return hipGetLastError();
   }
-  static hipError_t dense(const Args& a, int layout, int cus, hipStream_t s) {
+  static hipError_t dense(const Args& a, int cus, hipStream_t s) {
     switch (choose(a.M, a.N, a.K, KA, KB, cus)) {
-      case kAny: return run_any(a, layout, s);
+      case kAny64x64: return any<64, 64, 2, 2, 4>(a, s);
+      case kAny128x128: return any<128, 128, 2, 4, 1>(a, s);
       case kStream16x16:
         if constexpr (KA && KB) return run_stream<1, 1, 8, 4>(a, s);
         break;
@@ -811,9 +879,9 @@ hipError_t launch_gemm_bf16(const GemmBf16& p, hipStream_t s) {
   gb::Args g{(const uint16_t*)p.a, (const uint16_t*)p.b, p.bias, p.residual, (uint16_t*)p.pre, p.c,
              p.M, p.N, p.K, p.act, p.c_f32};
   const int cus = std::max(device_cu_count(), 8);
-  if (p.layout == MOE_NT) return gb::Run<true, true>::dense(g, p.layout, cus, s);
-  if (p.layout == MOE_NN) return gb::Run<true, false>::dense(g, p.layout, cus, s);
-  return gb::Run<false, false>::dense(g, p.layout, cus, s);
+  if (p.layout == MOE_NT) return gb::Run<true, true>::dense(g, cus, s);
+  if (p.layout == MOE_NN) return gb::Run<true, false>::dense(g, cus, s);
+  return gb::Run<false, false>::dense(g, cus, s);
 }
 
 hipError_t launch_act_bwd(int M, int N, int act, const void* d_c, const void* pre, void* d_z,

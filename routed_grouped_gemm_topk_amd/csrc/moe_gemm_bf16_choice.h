@@ -10,7 +10,7 @@ namespace moe {
 namespace gb {
 
 enum Kernel {
-  kAny, kStream16x16, kStream16x32, kTile32x64, kTile64x64, kTile64x128, kTile128x128,
+  kAny64x64, kAny128x128, kStream16x16, kStream16x32, kTile32x64, kTile64x64, kTile64x128, kTile128x128,
   kTile128x256, kTile192x192, kTile192x256, kTile256x256, kKernels
 };
 
@@ -18,8 +18,8 @@ struct TileSize {
   int bm, bn, threads;          // a tile's rows and columns of c, threads of its workgroup
 };
 constexpr TileSize kTileSize[kKernels] = {
-    {64, 64, 256},   {16, 16, 512},   {16, 32, 512},   {32, 64, 512},   {64, 64, 512},  {64, 128, 512},
-    {128, 128, 512}, {128, 256, 512}, {192, 192, 512}, {192, 256, 512}, {256, 256, 512}};
+    {64, 64, 1024},  {128, 128, 512}, {16, 16, 512},   {16, 32, 512},   {32, 64, 512},
+    {64, 64, 512},   {64, 128, 512},  {128, 128, 512}, {128, 256, 512}, {192, 192, 512}, {192, 256, 512}, {256, 256, 512}};
 
 constexpr int kSlice = 64;      // values of k per slice
 
@@ -67,28 +67,29 @@ struct Prices {
 };
 constexpr Prices kPrices[3] = {
     // a b^T
-    {{{0, 0, 0}, {2310, 2231, 42}, {1888, 2692, 61}, {1701, 3000, 112}, {1155, 3556, 140},
+    {{{0, 0, 0}, {0, 0, 0}, {2310, 2231, 42}, {1888, 2692, 61}, {1701, 3000, 112}, {1155, 3556, 140},
       {2656, 2315, 790}, {-325, 5585, 429}, {-3099, 9981, 640}, {-3528, 11839, 680},
       {-5239, 14066, 878}, {-7190, 18056, 1047}},
      {0, 1802, 235}, {0, 7500, 1000}},
     // a b
-    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1611, 3405, 128}, {1466, 3583, 158}, {2106, 3511, 735},
+    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1611, 3405, 128}, {1466, 3583, 158}, {2106, 3511, 735},
       {132, 5949, 420}, {-1141, 9202, 616}, {-1777, 10684, 682}, {-2593, 12172, 833},
       {-6485, 17865, 1066}},
      {0, 2921, 255}, {0, 7500, 1000}},
     // a^T b
-    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1023, 4165, 180}, {3263, 3131, 748},
+    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1023, 4165, 180}, {3263, 3131, 748},
       {-213, 6474, 436}, {-2273, 10140, 658}, {-3576, 12594, 686}, {-4274, 13851, 888},
       {-6245, 17291, 1147}},
      {0, 1759, 292}, {0, 7500, 1000}}};
 
 inline Kernel choose(int M, int N, int K, bool ka, bool kb, int cus) {
-  if (!fits_blocks(M, N, K, ka, kb)) return kAny;
+  if (!fits_blocks(M, N, K, ka, kb))
+    return tiles_of(kAny128x128, M, N) * 2 >= cus ? kAny128x128 : kAny64x64;
   const Prices& prices = kPrices[ka ? kb ? 0 : 1 : 2];
   const int64_t slices = ((int64_t)K + kSlice - 1) / kSlice;
-  Kernel best = kAny;
+  Kernel best = kAny128x128;
   int64_t least = INT64_MAX;
-  for (int i = kAny + 1; i < kKernels; ++i) {
+  for (int i = kStream16x16; i < kKernels; ++i) {
     const Kernel kernel = (Kernel)i;
     const Price& p = prices.of[i];
     if (!p.round || !launchable(kernel, M, N)) continue;

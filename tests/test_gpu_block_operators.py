@@ -435,7 +435,8 @@ GEMMS = [(1, 1, 1), (1, 256, 7168), (1, 8, 8), (3, 5, 7), (2, 64, 64), (16, 16, 
          (15, 40, 200), (64, 64, 64), (65, 72, 136), (8, 1000, 72), (33, 7, 130), (100, 130, 257),
          (128, 128, 128), (129, 136, 1000), (200, 328, 520), (256, 256, 256), (257, 264, 64),
          (300, 600, 1096), (513, 520, 264), (1000, 8, 512), (8, 1000, 2048), (777, 1544, 392),
-         (1030, 1032, 72), (2100, 768, 128), (31, 2056, 4096), (1, 4104, 1032), (640, 3200, 200)]
+         (1030, 1032, 72), (2100, 768, 128), (31, 2056, 4096), (1, 4104, 1032), (640, 3200, 200),
+         (1, 5, 14001), (1501, 1503, 77), (1502, 1600, 129), (200, 331, 3001)]
 LAYOUTS = ["nt", "nn", "tn"]
 ACTS = {"none": lambda z: z, "silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu,
         "gelu_tanh": lambda z: torch.nn.functional.gelu(z, approximate="tanh")}
