@@ -289,7 +289,8 @@ int moe_route_scored_bwd(const moe_problem* p, const moe_router* router, const v
  *   rstd[i]      = 1 / sqrt(mean over h of s[i, h]^2 + eps)
  *   n[i, h]      = s[i, h] * rstd[i] * weight[h]          (weight NULL: 1)
  *   y[i, :]      = round(n[i, :])
- *   scales[i, g] = amax |n[i, g-group]| / 448 over 128 columns (1 if they are all zero)
+ *   scales[i, g] = amax |n[i, g-group]| / 448 over 128 columns, at least 2^-126 (1 if they are all
+ *                  zero)
  *   codes[i, h]  = e4m3(n[i, h] / scales[i, h/128]), nearest even
  * The norm is taken of the rounded sum, so that it is that of the rows which go on as the residual
  * stream; n is held in fp32 and rounded once for either output; the mean is held in 64 bits.
@@ -606,7 +607,8 @@ typedef enum moe_layout {
  *   d_x   MOE_NN  a = d_z,  b = w        moe_gemm_bf16(m, k, n)
  *   d_w   MOE_TN  a = d_z,  b = x        moe_gemm_bf16(n, k, m)
  * Needs m, n, k >= 1 and at most 2^24, ceil(m/16) * ceil(n/16) <= 2^29, and a layout and an act of
- * those above (MOE_ERR_SHAPE otherwise).  Rows of a and b that are no multiple of 16 bytes (8 values) run on a slower kernel.
+ * those above (MOE_ERR_SHAPE otherwise).  Rows of a and b that are no multiple of 16 bytes (8
+ * values) run on slower kernels.
  * In:  a, b bf16; bias fp32 [n] or NULL; residual c_dtype [m, n] or NULL
  * Out: c c_dtype (MOE_F32 or MOE_BF16) [m, n], may be residual's own memory; pre bf16 [m, n] or NULL
  * Deterministic on one device: the order of the additions depends on the sizes, the layout and

@@ -350,10 +350,12 @@ def act_bwd(d_c: torch.Tensor, pre: Optional[torch.Tensor] = None, act: str = "n
     without an activation; the bias' gradient fp32 [n], None if not asked for)."""
     m, n = d_c.shape
     none = act in ("none", MOE_ACT_NONE)
+    if none and d_z is not None:
+        raise ValueError("d_z: given without an activation, where it is d_c itself")
     if none and not d_bias:
         return d_c, None
     if none:                    # nothing to multiply with: d_z is d_c
-        pre = d_z = None
+        pre = None
     elif d_z is None:
         d_z = _new(d_c, (m, n), torch.bfloat16, stream)
     db = None

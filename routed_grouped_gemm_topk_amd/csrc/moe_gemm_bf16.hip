@@ -161,7 +161,7 @@ struct TileGemm {
   static constexpr int RING = RING_B + NSB * KG * STAGE_B;
   static constexpr int SUMS = (KG - 1) * NW * FM * FN * kWave * 16;
   static constexpr int PITCH = WTN * 4 + 16;
-  static constexpr int OUTF = FM <= 4 ? FM : FM % 4 ? 3 : 4;              // fragments turned around at a time
+  static constexpr int OUTF = FM <= 4 ? FM : FM % 4 ? 3 : 4;   // fragments turned around at a time
   static constexpr int OUT_OFF = KG > 1 ? SUMS : 0;
   static constexpr int OUT = OUT_OFF + NW * OUTF * 16 * PITCH;
   static constexpr int LDS = RING > OUT ? RING : OUT;
@@ -176,8 +176,8 @@ struct TileGemm {
   // so that two stages of b reach as far ahead as three of a.
   static constexpr bool SOON = NSA != NSB;
   static constexpr int BFREE = BSTEPS + 1;
-  // Copies go out one a step, b's (SOON) two a step from step BFREE + 1 on, the others from step LAST + 1 on into
-  // the next slice's first steps.
+  // Copies go out one a step, b's (SOON) two a step from step BFREE + 1 on, the others from step
+  // LAST + 1 on into the next slice's first steps.
   static constexpr int TAIL = SOON ? CA : CA + CB;
   static constexpr int EARLY = AHEAD < TAIL ? AHEAD : TAIL;   // of them before the next slice begins
   // copies that may still be on their way when the next slice has to have landed: those that went out

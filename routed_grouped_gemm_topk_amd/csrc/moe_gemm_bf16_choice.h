@@ -18,8 +18,8 @@ struct TileSize {
   int bm, bn, threads;          // a tile's rows and columns of c, threads of its workgroup
 };
 constexpr TileSize kTileSize[kKernels] = {
-    {64, 64, 1024},  {128, 128, 512}, {16, 16, 512},   {16, 32, 512},   {32, 64, 512},
-    {64, 64, 512},   {64, 128, 512},  {128, 128, 512}, {128, 256, 512}, {192, 192, 512}, {192, 256, 512}, {256, 256, 512}};
+    {64, 64, 1024},  {128, 128, 512}, {16, 16, 512},   {16, 32, 512},   {32, 64, 512},   {64, 64, 512},
+    {64, 128, 512},  {128, 128, 512}, {128, 256, 512}, {192, 192, 512}, {192, 256, 512}, {256, 256, 512}};
 
 constexpr int kSlice = 64;      // values of k per slice
 
@@ -82,6 +82,9 @@ constexpr Prices kPrices[3] = {
       {-6245, 17291, 1147}},
      {0, 1759, 292}, {0, 7500, 1000}}};
 
+// Rows of any alignment: 128x128 tiles from half of one per unit on, below that 64x64 with four groups of
+// waves along k.  The second and the first, in us: 700 x 1001 x 1001 16.3 and 25.3, 1400 x 1501 x 1001
+// 42.2 and 25.2 (a b^T); 1000 x 1501 x 1001 29.5 and 38.2, 2047 x 2047 x 1001 81.8 and 50.7 (a^T b).
 inline Kernel choose(int M, int N, int K, bool ka, bool kb, int cus) {
   if (!fits_blocks(M, N, K, ka, kb))
     return tiles_of(kAny128x128, M, N) * 2 >= cus ? kAny128x128 : kAny64x64;

@@ -2,7 +2,7 @@
 // codes as its outputs, and its gradient.
 //
 //   s = round(x + residual),  r = 1 / sqrt(mean s^2 + eps),  n = s r w
-//   y = round(n);  codes = e4m3(n / scale), scale = amax |n| / 448 over 128 columns
+//   y = round(n);  codes = e4m3(n / scale), scale = amax |n| / 448 over 128 columns, at least 2^-126
 //   d_x = r (g - n' mean(g n')) + d_sum,  d_w = sum over rows of d_y n',   n' = s r, g = d_y w
 //
 // HBM bounds both: every row is read once and stays in registers.  TPR threads share a row, each
@@ -184,7 +184,8 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kern
         m = fmaxf(m, dpp_xchg<0x4E>(m));
         m = fmaxf(m, dpp_xchg<0x141>(m));
         m = fmaxf(m, dpp_xchg<0x140>(m));
-        const float s = m == 0.0f ? 1.0f : m / kE4M3Max;
+        // below 2^-126 the scale would lose bits, and its quotients pass 448
+        const float s = m == 0.0f ? 1.0f : fmaxf(m, kE4M3Max * 0x1p-126f) / kE4M3Max;
         const int c = Part::first(v, i);
         if (c < g.H) {
           // quotients are at most 448 up to their rounding, below the 464 from which e4m3 would

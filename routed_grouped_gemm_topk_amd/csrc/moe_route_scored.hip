@@ -31,9 +31,10 @@ struct Args {
   float scale;
 };
 
-// -inf and NaN take the expert out, +inf counts as the largest finite logit.
+// -inf and NaN take the expert out, +inf counts as the largest finite logit, -0 is 0 (their bits are
+// compared).
 __device__ __forceinline__ float clean(float l) {
-  return l > -INFINITY ? fminf(l, 3.40282347e38f) : -INFINITY;
+  return l > -INFINITY ? fminf(l, 3.40282347e38f) + 0.0f : -INFINITY;
 }
 
 __device__ __forceinline__ float load_logit(const void* p, int64_t at, bool bf16) {
@@ -114,7 +115,8 @@ __device__ __forceinline__ void exchange(int lg, F step) {
 }
 
 // The choice and the weights in fp32; returns false, having stored nothing, where fp32 does not tell
-// two experts or groups apart that the choice depends on.  Every lane of the wave must be active.
+// two experts or groups apart that the choice depends on, or has no normal number for a weight.  Every
+// lane of the wave must be active.
 //
 // An expert's key is its choice score's (its logit's) ordered integer, whose last bits hold the item's
 // place in the lane, so that a lane's keys differ and the largest one names its item.  A bf16 logit
@@ -261,9 +263,9 @@ __device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const
   if (!here) lj = -INFINITY;
   if (!g.sigmoid && g.renorm) m = fmaxf(wave_max(lj), -3.40282347e38f);
   float s = !here ? 0.0f : g.sigmoid ? sigmoid_of(lj) : exp_diff(lj, m);
+  if (__ballot(here && s < 0x1p-100f)) return false;     // what fp32 rounds away may count yet
   if (g.renorm) {
     const float sum = wave_allreduce(s, [](float a, float b) { return a + b; });
-    if (g.sigmoid && sum < 0x1p-100f) return false;      // their ratios need 64 bits
     inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
   }
   if (at.lane < g.K) {
