@@ -160,15 +160,21 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kern
     sq = row_sum<TPR>(sq, words, turn);
     turn ^= 1;
     if (!live) continue;
-    const float rstd = (float)rsqrt(sq / (double)g.H + (double)g.eps);
+    const double r64 = rsqrt(sq / (double)g.H + (double)g.eps);
+    const float rstd = (float)r64;
     if (g.rstd && i == 0) g.rstd[t] = rstd;
+    // n = (s p) w r with rstd = p r, p a power of two: s p is exact, and so is its product with w in
+    // bf16, which leaves r's rounding and one more (s r w by itself rounds three times)
+    const float p = fmaxf(__uint_as_float(__float_as_uint(rstd) & 0x7F800000u), 0x1p-126f);
+    const double r_p = r64 / (double)p;
     #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float y[8];
+      float n[8], y[8];
       #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        y[k] = x[v].get(k) * rstd;
-        if (g.weight) y[k] *= w[v].get(k);
+        n[k] = x[v].get(k) * p;
+        if (g.weight) n[k] *= w[v].get(k);
+        y[k] = n[k] * (float)r_p;
       }
       if (g.y) {
         Part o;
@@ -178,14 +184,18 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kern
       if (VEC && g.codes) {
         float m = 0.0f;
         #pragma unroll
-        for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(y[k]));
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(n[k]));
         // 16 lanes hold a group
         m = fmaxf(m, dpp_xchg<0xB1>(m));
         m = fmaxf(m, dpp_xchg<0x4E>(m));
         m = fmaxf(m, dpp_xchg<0x141>(m));
         m = fmaxf(m, dpp_xchg<0x140>(m));
-        // below 2^-126 the scale would lose bits, and its quotients pass 448
-        const float s = m == 0.0f ? 1.0f : fmaxf(m, kE4M3Max * 0x1p-126f) / kE4M3Max;
+        // A scale below 2^-126 would lose bits, and its quotients pass 448.  A quotient is n times
+        // r / scale: that factor's rounding and its own.
+        const float amax = (float)(m * r_p);
+        const float s = amax > 0.0f ? fmaxf(amax, kE4M3Max * 0x1p-126f) / kE4M3Max : 1.0f;
+        const double inv = __builtin_amdgcn_rcpf(s);
+        const float f = (float)(r_p * (inv * (2.0 - (double)s * inv)));
         const int c = Part::first(v, i);
         if (c < g.H) {
           // quotients are at most 448 up to their rounding, below the 464 from which e4m3 would
@@ -194,8 +204,8 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kern
           #pragma unroll
           for (int h = 0; h < 2; ++h)
             q[h] = __builtin_amdgcn_cvt_pk_fp8_f32(
-                y[4 * h + 2] / s, y[4 * h + 3] / s,
-                __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h] / s, y[4 * h + 1] / s, 0, false), true);
+                n[4 * h + 2] * f, n[4 * h + 3] * f,
+                __builtin_amdgcn_cvt_pk_fp8_f32(n[4 * h] * f, n[4 * h + 1] * f, 0, false), true);
           *(uint2*)(g.codes + row + c) = make_uint2(q[0], q[1]);
           if ((i & 15) == 0) g.scales[t * (g.H / kGroup) + c / kGroup] = s;
         }
