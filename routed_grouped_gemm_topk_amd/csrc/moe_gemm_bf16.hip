@@ -6,6 +6,14 @@
 //
 // Accumulated in fp32 by the bf16 matrix instructions.  The operand order puts b on a result's rows
 // and a on its columns, so a lane holds 4 neighbouring columns of ONE row of c.
+//
+// Measured, kernels alone, operands from memory (a large library product reaches 1390 TFLOP/s here):
+//   4096 x 14336 x 4096 367 us, 8192^3 753 us (1460 TFLOP/s); 4096 x 4096 x 14336 with residual 341 us
+//   (1410): matrix cores busy 70% at 1.87 GHz
+//   4096^3 a b^T, a b, a^T b 108, 112, 114 us (1210-1270 TFLOP/s)
+//   64 x 256 x 7168 8.2 us, 1 x 256 x 7168 6.7 us: the chain of slices of one tile; 1 x 4096 x 7168
+//   11.9 us, 4.9 TB/s of the weights
+//   rows of any alignment, 2047^3: 48, 51, 53 us (2048^3: 21, 22, 23)
 #include <algorithm>
 #include <type_traits>
 
@@ -388,9 +396,13 @@ struct TileGemm {
     finish_tile(g, t, lds, acc, kg, wave, lane);
   }
 
-  // The same tile from rows of any alignment: a thread loads its chunks of 16 bytes into registers, two
-  // steps ahead, values past the operands' ends as zeros, and stores them to the stage of the step
-  // after; two stages of each operand.
+  // The same tile from rows of any alignment: a thread loads its chunks of 16 bytes into registers a step
+  // before it stores them to one of two stages of LDS.  A chunk that reaches past its row's end is
+  // loaded whole, at the operand's end from where it still lies in it, and the values that are not its
+  // row's are dropped on the way to LDS: with loads of single values there, which hold up every step of
+  // the last column of tiles, 2047^3 takes 96 us for a b, 49 so.  Loads two steps ahead gain nothing
+  // (their registers cost a workgroup per unit or are spilled).  TINY: operands of less than a chunk.
+  template <bool TINY>
   __device__ static __forceinline__ void run_any(const Args& g, const Tile& t, char* lds) {
     const int lane = threadIdx.x & (kWave - 1);
     const int all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -408,31 +420,62 @@ struct TileGemm {
       const int f = ((k >> 1) & 1) | ((k >> 4) & 1) << 1;
       return (q >> 9) * 64 * ROWB + k * ROWB + ((c ^ (2 * f)) << 4);
     };
+    struct Piece {
+      i32x4 v;                  // not loaded where fix is 0
+      int fix;                  // values that exist, from value fix / 16 of v on
+    };
+    // chunk q of the slice that begins at k0 of an operand of `rows` rows (columns, if k is not its
+    // contiguous dimension), whose part in the tile begins at `first`
     auto load = [&](bool contiguous, const uint16_t* p, int64_t first, int64_t rows, int q, int k0) {
-      i32x4 v = {0, 0, 0, 0};
+      Piece o;
       const int c = q & 7;
       int64_t at;
       int left;
       if (contiguous) {
         const int64_t r = first + (q >> 3);
-        at = r * K + k0 + c * 8;
+        at = r * K + c * 8 + k0;
         left = r < rows ? K - k0 - c * 8 : 0;
       } else {
-        const int k = k0 + ((q >> 3) & 63);
+        const int k = (q >> 3) & 63;
         const int64_t n = first + (q >> 9) * 64 + c * 8;
-        at = (int64_t)k * rows + n;
-        left = k < K ? (int)min(rows - n, (int64_t)8) : 0;
+        at = k * rows + n + k0 * rows;
+        left = k0 + k < K ? (int)min(rows - n, (int64_t)8) : 0;
       }
-      if (left >= 8) {
-        __builtin_memcpy(&v, p + at, 16);              // of 2-byte alignment
-      } else {
+      left = min(max(left, 0), 8);
+      if constexpr (TINY) {
+        o.v = i32x4{0, 0, 0, 0};
         #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i < left) v[i / 2] |= (int)((uint32_t)p[at + i] << (16 * (i & 1)));
+          if (i < left) o.v[i / 2] |= (int)((uint32_t)p[at + i] << (16 * (i & 1)));
+        o.fix = 8;
+      } else {
+        o.fix = 0;
+        if (left > 0) {
+          const int64_t start = min(at, rows * K - kChunk);
+          __builtin_memcpy(&o.v, p + start, 16);       // of 2-byte alignment
+          o.fix = left | (int)(at - start) << 4;
+        }
       }
-      return v;
+      return o;
     };
-    i32x4 a[PA], b[PB];
+    auto store = [&](char* to, const Piece& o) {
+      i32x4 v = o.v;
+      if (o.fix != 8) {
+        const int left = o.fix & 15, off = o.fix >> 4;
+        if (off & 4) v = i32x4{v[2], v[3], 0, 0};
+        if (off & 2) v = i32x4{v[1], v[2], v[3], 0};
+        if (off & 1) {
+          #pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = (int)((uint32_t)v[i] >> 16 | (uint32_t)(i < 3 ? v[i + 1] : 0) << 16);
+        }
+        #pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = left >= 2 * i + 2 ? v[i] : left == 2 * i + 1 ? v[i] & 0xffff : 0;
+      }
+      *reinterpret_cast<i32x4*>(to) = v;
+    };
+    Piece a[PA], b[PB];
     auto load_step = [&](int step) {
       const int k0 = min(step * KG + kg, 1 << 24) * kSlice;
       #pragma unroll
@@ -444,11 +487,9 @@ struct TileGemm {
     auto store_step = [&](int buf) {
       char* st = lds + (buf * KG + kg) * STAGE;
       #pragma unroll
-      for (int i = 0; i < PA; ++i)
-        *reinterpret_cast<i32x4*>(st + place(KA, i * NW * kWave + me)) = a[i];
+      for (int i = 0; i < PA; ++i) store(st + place(KA, i * NW * kWave + me), a[i]);
       #pragma unroll
-      for (int i = 0; i < PB; ++i)
-        *reinterpret_cast<i32x4*>(st + STAGE_A + place(KB, i * NW * kWave + me)) = b[i];
+      for (int i = 0; i < PB; ++i) store(st + STAGE_A + place(KB, i * NW * kWave + me), b[i]);
     };
     Where<KA, WTM, FM> wa;
     Where<KB, WTN, FN> wb;
@@ -575,8 +616,8 @@ __global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void tile_kernel(Args g)
 // Rows of any alignment and sizes past the other kernels' offsets.
 constexpr int64_t kAnyGrid = 1 << 21;    // workgroups of a launch; more tiles are run by striding
 
-template <int BM, int BN, int WM, int WN, int KG, bool KA, bool KB>
-__global__ __launch_bounds__(WM * WN * KG * kWave) void any_kernel(Args g) {
+template <int BM, int BN, int WM, int WN, int KG, bool TINY, bool KA, bool KB>
+__global__ __launch_bounds__(WM * WN * KG * kWave, 4) void any_kernel(Args g) {
   using G = TileGemm<BM, BN, WM, WN, KG, 2, 2, KA, KB>;
   __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
   const int64_t nblk = ((int64_t)g.N + BN - 1) / BN;
@@ -588,7 +629,7 @@ __global__ __launch_bounds__(WM * WN * KG * kWave) void any_kernel(Args g) {
     t.rows = (int)min((int64_t)BM, (int64_t)g.M - t.m0);
     t.cols = min(BN, g.N - t.n0);
     __syncthreads();
-    G::run_any(g, t, lds);
+    G::template run_any<TINY>(g, t, lds);
   }
 }
 
@@ -726,10 +767,10 @@ struct Run {
                        dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(WM * WN * KG * kWave), 0, s, a);
     return hipGetLastError();
   }
-  template <int BM, int BN, int WM, int WN, int KG>
+  template <int BM, int BN, int WM, int WN, int KG, bool TINY = false>
   static hipError_t any(const Args& a, hipStream_t s) {
     const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
-    hipLaunchKernelGGL((any_kernel<BM, BN, WM, WN, KG, KA, KB>),
+    hipLaunchKernelGGL((any_kernel<BM, BN, WM, WN, KG, TINY, KA, KB>),
                        dim3((unsigned)std::min(tiles, kAnyGrid)), dim3(WM * WN * KG * kWave), 0, s,
                        a);
     return hipGetLastError();
@@ -743,7 +784,9 @@ struct Run {
   }
   static hipError_t dense(const Args& a, int cus, hipStream_t s) {
     switch (choose(a.M, a.N, a.K, KA, KB, cus)) {
-      case kAny64x64: return any<64, 64, 2, 2, 4>(a, s);
+      case kAny64x64:
+        if (tiny(a.M, a.N, a.K)) return any<64, 64, 2, 2, 4, true>(a, s);
+        return any<64, 64, 2, 2, 4>(a, s);
       case kAny128x128: return any<128, 128, 2, 4, 1>(a, s);
       case kStream16x16:
         if constexpr (KA && KB) return run_stream<1, 1, 8, 4>(a, s);
@@ -795,8 +838,8 @@ struct ActArgs {
   int M, N, act;
 };
 
-// A workgroup takes kActCols columns, 8 a lane, and every gridDim.y-th set of rows, one of its waves
-// each, two sets at a time.  VEC: rows are whole 16-byte blocks and a lane's columns neighbours;
+// HBM bounds it: 4096 x 14336, tanh form, with the bias 74 us, 4.8 TB/s.  A workgroup takes kActCols
+// columns, 8 a lane, and every gridDim.y-th set of rows, one of its waves each, two sets at a time.  VEC: rows are whole 16-byte blocks and a lane's columns neighbours;
 // elsewhere a lane has every 64th column.
 constexpr int kActThreads = 256, kActWaves = kActThreads / kWave;
 

@@ -22,6 +22,7 @@ constexpr TileSize kTileSize[kKernels] = {
     {64, 128, 512},  {128, 128, 512}, {128, 256, 512}, {192, 192, 512}, {192, 256, 512}, {256, 256, 512}};
 
 constexpr int kSlice = 64;      // values of k per slice
+constexpr int kChunk = 8;       // values of a load
 
 inline int64_t tiles_of(Kernel kernel, int M, int N) {
   const TileSize& s = kTileSize[kernel];
@@ -50,6 +51,9 @@ inline bool fits_blocks(int M, int N, int K, bool ka, bool kb) {
   const bool b = kb ? K % 8 == 0 && K <= kMaxK : N % 8 == 0 && N <= kMaxLd;
   return a && b;
 }
+
+// An operand of less than one chunk: 64x64 tiles, in a form of their own.
+inline bool tiny(int M, int N, int K) { return (int64_t)std::min(M, N) * K < kChunk; }
 
 // Time of a product in ns: `fixed`, and for every round of one workgroup per unit `round` and per
 // slice of k `slice`.  Fitted to 1500 shapes of 1 to 9000 rows, 16 to 16000 columns and k of 128 to
@@ -83,11 +87,12 @@ constexpr Prices kPrices[3] = {
      {0, 1759, 292}, {0, 7500, 1000}}};
 
 // Rows of any alignment: 128x128 tiles from half of one per unit on, below that 64x64 with four groups of
-// waves along k.  The second and the first, in us: 700 x 1001 x 1001 16.3 and 25.3, 1400 x 1501 x 1001
-// 42.2 and 25.2 (a b^T); 1000 x 1501 x 1001 29.5 and 38.2, 2047 x 2047 x 1001 81.8 and 50.7 (a^T b).
+// waves along k.  The second and the first, in us: 700 x 1001 x 1001 15.7 and 26.6, 300 x 3001 x 2001
+// 23.4 and 44.9, 1400 x 1501 x 1001 40.1 and 25.7, 2047 x 2047 x 1001 54.1 and 27.9 (a b^T; the other
+// layouts are within 10% of that).
 inline Kernel choose(int M, int N, int K, bool ka, bool kb, int cus) {
   if (!fits_blocks(M, N, K, ka, kb))
-    return tiles_of(kAny128x128, M, N) * 2 >= cus ? kAny128x128 : kAny64x64;
+    return tiles_of(kAny128x128, M, N) * 2 >= cus && !tiny(M, N, K) ? kAny128x128 : kAny64x64;
   const Prices& prices = kPrices[ka ? kb ? 0 : 1 : 2];
   const int64_t slices = ((int64_t)K + kSlice - 1) / kSlice;
   Kernel best = kAny128x128;

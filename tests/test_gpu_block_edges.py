@@ -98,3 +98,31 @@ def test_gemm_of_subnormal_operands(device, layout):
         z = (a64.t() if layout == "tn" else a64) @ (b64.t() if layout == "nt" else b64)
         out = moe.gemm_bf16(a, b, layout, out_dtype=torch.float32)
         assert torch.equal(out.double(), z)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["nt", "nn", "tn"])
+def test_gemm_rows_of_any_alignment_between_nan(device, layout):
+    """Operands right between NaN, down to less than one load of 8 values, rows that end inside one:
+    nothing beside an operand, and nothing of a row's neighbour, reaches a result."""
+    for m, n, k in [(1, 1, 1), (1, 3, 5), (2, 3, 3), (7, 1, 1), (1, 7, 1), (8, 1, 1), (1, 8, 1), (1, 9, 7),
+                    (3, 3, 3), (1, 20001, 3), (20001, 1, 5), (9, 9, 9), (63, 65, 66), (70, 131, 67),
+                    (129, 270, 515), (1030, 1031, 65), (2049, 1027, 131), (1027, 2050, 200)]:
+        say("any alignment", m, n, k, layout)
+        g = gen(device, 134)
+        held = []
+        for shape in (((k, m) if layout == "tn" else (m, k)), ((n, k) if layout == "nt" else (k, n))):
+            size = shape[0] * shape[1]
+            buf = torch.full((size + 128,), float("nan"), dtype=torch.bfloat16, device=device)
+            held.append(buf[64:64 + size].view(shape))
+            held[-1].copy_(torch.randint(-2, 3, shape, generator=g, device=device))
+        a, b = held
+        out = moe.gemm_bf16(a, b, layout, out_dtype=torch.float32)
+        a64, b64 = a.to(F64), b.to(F64)
+        z = (a64.t() if layout == "tn" else a64) @ (b64.t() if layout == "nt" else b64)
+        assert torch.equal(out.double(), z)
+        # NaN in one row (column) of an operand stays in its row (column) of the result
+        (a.t() if layout == "tn" else a)[m // 2] = float("nan")
+        out = moe.gemm_bf16(a, b, layout, out_dtype=torch.float32)
+        rows = torch.arange(m, device=device) != m // 2
+        assert torch.equal(out[rows].double(), z[rows]) and torch.isnan(out[m // 2]).all()
