@@ -13,7 +13,7 @@
 //   4096^3 a b^T, a b, a^T b 108, 112, 114 us (1210-1270 TFLOP/s)
 //   64 x 256 x 7168 8.2 us, 1 x 256 x 7168 6.7 us: the chain of slices of one tile; 1 x 4096 x 7168
 //   11.9 us, 4.9 TB/s of the weights
-//   rows of any alignment, 2047^3: 48, 51, 53 us (2048^3: 21, 22, 23)
+//   rows of any alignment, 2047^3: 48, 49, 52 us (2048^3: 21, 22, 23); 3 x 5 x 14001 a b^T 14.5 us
 #include <algorithm>
 #include <type_traits>
 
@@ -146,6 +146,46 @@ __device__ __forceinline__ void finish8(const Args& g, const f32x4& z0, const f3
     *(i32x4*)((uint16_t*)g.c + at) = pack8(z);
   }
 }
+
+// Eight values from place `at` of an operand of `total`, of any alignment, of which the first `left` are
+// wanted; `get` leaves zeros for the others.  They are loaded whole where they reach past the wanted
+// ones, and at the operand's end from where they still lie in it.
+struct Piece {
+  i32x4 v;                      // not loaded where fix is 0
+  int fix;                      // wanted values, from value fix / 16 of v on
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t at, int64_t total, int left) {
+    fix = 0;
+    if (left <= 0) return;
+    if (total >= kChunk) {
+      const int64_t start = min(at, total - kChunk);
+      __builtin_memcpy(&v, p + start, 16);             // of 2-byte alignment
+      fix = min(left, kChunk) | (int)(at - start) << 4;
+    } else {
+      v = i32x4{0, 0, 0, 0};
+      fix = kChunk;
+      #pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (i < left) v[i / 2] |= (int)((uint32_t)p[at + i] << (16 * (i & 1)));
+    }
+  }
+  __device__ __forceinline__ i32x4 get() const {
+    i32x4 o = v;
+    if (fix != kChunk) {
+      const int left = fix & 15, off = fix >> 4;
+      if (off & 4) o = i32x4{o[2], o[3], 0, 0};
+      if (off & 2) o = i32x4{o[1], o[2], o[3], 0};
+      if (off & 1) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = (int)((uint32_t)o[i] >> 16 | (uint32_t)(i < 3 ? o[i + 1] : 0) << 16);
+      }
+      #pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = left >= 2 * i + 2 ? o[i] : left == 2 * i + 1 ? o[i] & 0xffff : 0;
+    }
+    return o;
+  }
+};
 
 // BM x BN tile by WM x WN waves; slices of 64 values of k of both operands in rings of LDS stages,
 // NSA of a and NSB of b, copied by direct-to-LDS loads.  KG groups of WM x WN waves take every KG-th
@@ -397,12 +437,10 @@ struct TileGemm {
   }
 
   // The same tile from rows of any alignment: a thread loads its chunks of 16 bytes into registers a step
-  // before it stores them to one of two stages of LDS.  A chunk that reaches past its row's end is
-  // loaded whole, at the operand's end from where it still lies in it, and the values that are not its
-  // row's are dropped on the way to LDS: with loads of single values there, which hold up every step of
-  // the last column of tiles, 2047^3 takes 96 us for a b, 49 so.  Loads two steps ahead gain nothing
-  // (their registers cost a workgroup per unit or are spilled).  TINY: operands of less than a chunk.
-  template <bool TINY>
+  // before it stores them to one of two stages of LDS.  With loads of single values at the rows' ends,
+  // which hold up every step of the last column of tiles, 2047^3 a b takes 96 us, so 50.  Loads two steps
+  // ahead gain nothing (their registers cost a workgroup per unit or are spilled), nor do those of whole
+  // words that any_stream_kernel makes (a b^T 57 us against 47).
   __device__ static __forceinline__ void run_any(const Args& g, const Tile& t, char* lds) {
     const int lane = threadIdx.x & (kWave - 1);
     const int all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -419,10 +457,6 @@ struct TileGemm {
       const int k = (q >> 3) & 63;
       const int f = ((k >> 1) & 1) | ((k >> 4) & 1) << 1;
       return (q >> 9) * 64 * ROWB + k * ROWB + ((c ^ (2 * f)) << 4);
-    };
-    struct Piece {
-      i32x4 v;                  // not loaded where fix is 0
-      int fix;                  // values that exist, from value fix / 16 of v on
     };
     // chunk q of the slice that begins at k0 of an operand of `rows` rows (columns, if k is not its
     // contiguous dimension), whose part in the tile begins at `first`
@@ -441,39 +475,8 @@ struct TileGemm {
         at = k * rows + n + k0 * rows;
         left = k0 + k < K ? (int)min(rows - n, (int64_t)8) : 0;
       }
-      left = min(max(left, 0), 8);
-      if constexpr (TINY) {
-        o.v = i32x4{0, 0, 0, 0};
-        #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < left) o.v[i / 2] |= (int)((uint32_t)p[at + i] << (16 * (i & 1)));
-        o.fix = 8;
-      } else {
-        o.fix = 0;
-        if (left > 0) {
-          const int64_t start = min(at, rows * K - kChunk);
-          __builtin_memcpy(&o.v, p + start, 16);       // of 2-byte alignment
-          o.fix = left | (int)(at - start) << 4;
-        }
-      }
+      o.load(p, at, rows * K, left);
       return o;
-    };
-    auto store = [&](char* to, const Piece& o) {
-      i32x4 v = o.v;
-      if (o.fix != 8) {
-        const int left = o.fix & 15, off = o.fix >> 4;
-        if (off & 4) v = i32x4{v[2], v[3], 0, 0};
-        if (off & 2) v = i32x4{v[1], v[2], v[3], 0};
-        if (off & 1) {
-          #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = (int)((uint32_t)v[i] >> 16 | (uint32_t)(i < 3 ? v[i + 1] : 0) << 16);
-        }
-        #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = left >= 2 * i + 2 ? v[i] : left == 2 * i + 1 ? v[i] & 0xffff : 0;
-      }
-      *reinterpret_cast<i32x4*>(to) = v;
     };
     Piece a[PA], b[PB];
     auto load_step = [&](int step) {
@@ -487,9 +490,11 @@ struct TileGemm {
     auto store_step = [&](int buf) {
       char* st = lds + (buf * KG + kg) * STAGE;
       #pragma unroll
-      for (int i = 0; i < PA; ++i) store(st + place(KA, i * NW * kWave + me), a[i]);
+      for (int i = 0; i < PA; ++i)
+        *reinterpret_cast<i32x4*>(st + place(KA, i * NW * kWave + me)) = a[i].get();
       #pragma unroll
-      for (int i = 0; i < PB; ++i) store(st + STAGE_A + place(KB, i * NW * kWave + me), b[i]);
+      for (int i = 0; i < PB; ++i)
+        *reinterpret_cast<i32x4*>(st + STAGE_A + place(KB, i * NW * kWave + me)) = b[i].get();
     };
     Where<KA, WTM, FM> wa;
     Where<KB, WTN, FN> wb;
@@ -616,7 +621,7 @@ __global__ __launch_bounds__(WM * WN * KG * kWave, WPS) void tile_kernel(Args g)
 // Rows of any alignment and sizes past the other kernels' offsets.
 constexpr int64_t kAnyGrid = 1 << 21;    // workgroups of a launch; more tiles are run by striding
 
-template <int BM, int BN, int WM, int WN, int KG, bool TINY, bool KA, bool KB>
+template <int BM, int BN, int WM, int WN, int KG, bool KA, bool KB>
 __global__ __launch_bounds__(WM * WN * KG * kWave, 4) void any_kernel(Args g) {
   using G = TileGemm<BM, BN, WM, WN, KG, 2, 2, KA, KB>;
   __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
@@ -629,7 +634,7 @@ __global__ __launch_bounds__(WM * WN * KG * kWave, 4) void any_kernel(Args g) {
     t.rows = (int)min((int64_t)BM, (int64_t)g.M - t.m0);
     t.cols = min(BN, g.N - t.n0);
     __syncthreads();
-    G::template run_any<TINY>(g, t, lds);
+    G::run_any(g, t, lds);
   }
 }
 
@@ -739,6 +744,82 @@ __global__ __launch_bounds__(NW * kWave) void stream_kernel(Args g) {
   }
 }
 
+// The same few rows where they are no whole 16-byte blocks: every wave loads its fragments straight into
+// registers, AT_ONCE slices at a time, in aligned words, one more where a row begins in the middle of
+// one (loads of 16 bytes that begin there take several times as long: 64 x 255 x 7167 46 us, 20 so).
+// Lanes of rows that a or b has not take its last row, whose products are not stored.  k past the last
+// whole slice is one wave's.
+template <int NW>
+__global__ __launch_bounds__(NW * kWave) void any_stream_kernel(Args g) {
+  constexpr int AT_ONCE = 4;
+  __shared__ f32x4 sums[NW * kWave];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int K = g.K, whole = K / kSlice;
+  const int fr = lane & 15, fq = lane >> 4;
+  const int nblk = (g.N + 15) / 16;
+  const int m0 = (int)blockIdx.x / nblk * 16, n0 = (int)blockIdx.x % nblk * 16;
+  const int64_t at_a = (int64_t)min(m0 + fr, g.M - 1) * K + fq * 16;
+  const int64_t at_b = (int64_t)min(n0 + fr, g.N - 1) * K + fq * 16;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  // a row's 16 values of a whole slice; they begin in the middle of a word only where rows are of an odd
+  // length, and then one more follows them
+  struct Sixteen {
+    i32x4 v[2];
+    int more, odd;
+    __device__ __forceinline__ void load(const uint16_t* p, int64_t at) {
+      odd = (int)(at & 1);
+      const int* w = (const int*)p + (at >> 1);
+      __builtin_memcpy(v, w, 32);                      // of 4-byte alignment
+      more = w[7 + odd];
+    }
+    __device__ __forceinline__ i32x4 get(int h) const {
+      const int next = h == 0 ? v[1][0] : more;
+      i32x4 o;
+      #pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = __builtin_amdgcn_alignbit(i < 3 ? v[h][i + 1] : next, v[h][i], odd * 16);
+      return o;
+    }
+  };
+  auto mul = [&](const i32x4& a, const i32x4& b) {
+    acc = OpBf16::mma(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), acc);
+  };
+  for (int kt = wave; kt < whole; kt += AT_ONCE * NW) {
+    Sixteen a[AT_ONCE], b[AT_ONCE];
+    #pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const int64_t k = (int64_t)min(kt + u * NW, whole - 1) * kSlice;
+      a[u].load(g.a, at_a + k);
+      b[u].load(g.b, at_b + k);
+    }
+    #pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      if (kt + u * NW >= whole) break;
+      #pragma unroll
+      for (int h = 0; h < 2; ++h) mul(a[u].get(h), b[u].get(h));
+    }
+  }
+  if (K % kSlice != 0 && wave == whole % NW) {
+    #pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = whole * kSlice + h * kChunk, left = K - k - fq * 16;
+      Piece a, b;
+      a.load(g.a, at_a + k, (int64_t)g.M * K, left);
+      b.load(g.b, at_b + k, (int64_t)g.N * K, left);
+      mul(a.get(), b.get());
+    }
+  }
+  sums[wave * kWave + lane] = acc;
+  __syncthreads();
+  if (wave > 0) return;
+  #pragma unroll
+  for (int w = 1; w < NW; ++w) acc += sums[w * kWave + lane];
+  const int m = m0 + fr, n = n0 + fq * 4;
+  const float z[4] = {acc[0], acc[1], acc[2], acc[3]};
+  if (m < g.M && n < g.N) finish<4>(g, z, m, n, g.N - n);
+}
+
 // The kernels of these tiles, as moe_gemm_bf16_choice.h knows them.
 template <int BM, int BN, int THREADS>
 constexpr bool listed() {
@@ -767,10 +848,10 @@ struct Run {
                        dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(WM * WN * KG * kWave), 0, s, a);
     return hipGetLastError();
   }
-  template <int BM, int BN, int WM, int WN, int KG, bool TINY = false>
+  template <int BM, int BN, int WM, int WN, int KG>
   static hipError_t any(const Args& a, hipStream_t s) {
     const int64_t tiles = (((int64_t)a.M + BM - 1) / BM) * (((int64_t)a.N + BN - 1) / BN);
-    hipLaunchKernelGGL((any_kernel<BM, BN, WM, WN, KG, TINY, KA, KB>),
+    hipLaunchKernelGGL((any_kernel<BM, BN, WM, WN, KG, KA, KB>),
                        dim3((unsigned)std::min(tiles, kAnyGrid)), dim3(WM * WN * KG * kWave), 0, s,
                        a);
     return hipGetLastError();
@@ -784,10 +865,16 @@ struct Run {
   }
   static hipError_t dense(const Args& a, int cus, hipStream_t s) {
     switch (choose(a.M, a.N, a.K, KA, KB, cus)) {
-      case kAny64x64:
-        if (tiny(a.M, a.N, a.K)) return any<64, 64, 2, 2, 4, true>(a, s);
-        return any<64, 64, 2, 2, 4>(a, s);
+      case kAny64x64: return any<64, 64, 2, 2, 4>(a, s);
       case kAny128x128: return any<128, 128, 2, 4, 1>(a, s);
+      case kAnyStream16x16:
+        if constexpr (KA && KB) {
+          static_assert(listed<16, 16, 16 * kWave>(), "the choice counts these tiles and threads");
+          const int64_t tiles = tiles_of(kAnyStream16x16, a.M, a.N);
+          hipLaunchKernelGGL(any_stream_kernel<16>, dim3((unsigned)tiles), dim3(16 * kWave), 0, s, a);
+          return hipGetLastError();
+        }
+        break;
       case kStream16x16:
         if constexpr (KA && KB) return run_stream<1, 1, 8, 4>(a, s);
         break;

@@ -10,19 +10,20 @@ namespace moe {
 namespace gb {
 
 enum Kernel {
-  kAny64x64, kAny128x128, kStream16x16, kStream16x32, kTile32x64, kTile64x64, kTile64x128, kTile128x128,
-  kTile128x256, kTile192x192, kTile192x256, kTile256x256, kKernels
+  kAny64x64, kAny128x128, kAnyStream16x16, kStream16x16, kStream16x32, kTile32x64, kTile64x64, kTile64x128,
+  kTile128x128, kTile128x256, kTile192x192, kTile192x256, kTile256x256, kKernels
 };
 
 struct TileSize {
   int bm, bn, threads;          // a tile's rows and columns of c, threads of its workgroup
 };
 constexpr TileSize kTileSize[kKernels] = {
-    {64, 64, 1024},  {128, 128, 512}, {16, 16, 512},   {16, 32, 512},   {32, 64, 512},   {64, 64, 512},
-    {64, 128, 512},  {128, 128, 512}, {128, 256, 512}, {192, 192, 512}, {192, 256, 512}, {256, 256, 512}};
+    {64, 64, 1024},  {128, 128, 512}, {16, 16, 1024},  {16, 16, 512},   {16, 32, 512},
+    {32, 64, 512},   {64, 64, 512},   {64, 128, 512},  {128, 128, 512}, {128, 256, 512},
+    {192, 192, 512}, {192, 256, 512}, {256, 256, 512}};
 
 constexpr int kSlice = 64;      // values of k per slice
-constexpr int kChunk = 8;       // values of a load
+constexpr int kChunk = 8;       // values of a load, of rows of any alignment
 
 inline int64_t tiles_of(Kernel kernel, int M, int N) {
   const TileSize& s = kTileSize[kernel];
@@ -52,9 +53,6 @@ inline bool fits_blocks(int M, int N, int K, bool ka, bool kb) {
   return a && b;
 }
 
-// An operand of less than one chunk: 64x64 tiles, in a form of their own.
-inline bool tiny(int M, int N, int K) { return (int64_t)std::min(M, N) * K < kChunk; }
-
 // Time of a product in ns: `fixed`, and for every round of one workgroup per unit `round` and per
 // slice of k `slice`.  Fitted to 1500 shapes of 1 to 9000 rows, 16 to 16000 columns and k of 128 to
 // 9600 (rms 7-17%, the most where the launch is most of it).  On 700 shapes of the same range that
@@ -71,28 +69,33 @@ struct Prices {
 };
 constexpr Prices kPrices[3] = {
     // a b^T
-    {{{0, 0, 0}, {0, 0, 0}, {2310, 2231, 42}, {1888, 2692, 61}, {1701, 3000, 112}, {1155, 3556, 140},
+    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {2310, 2231, 42}, {1888, 2692, 61}, {1701, 3000, 112}, {1155, 3556, 140},
       {2656, 2315, 790}, {-325, 5585, 429}, {-3099, 9981, 640}, {-3528, 11839, 680},
       {-5239, 14066, 878}, {-7190, 18056, 1047}},
      {0, 1802, 235}, {0, 7500, 1000}},
     // a b
-    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1611, 3405, 128}, {1466, 3583, 158}, {2106, 3511, 735},
+    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1611, 3405, 128}, {1466, 3583, 158}, {2106, 3511, 735},
       {132, 5949, 420}, {-1141, 9202, 616}, {-1777, 10684, 682}, {-2593, 12172, 833},
       {-6485, 17865, 1066}},
      {0, 2921, 255}, {0, 7500, 1000}},
     // a^T b
-    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1023, 4165, 180}, {3263, 3131, 748},
+    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1023, 4165, 180}, {3263, 3131, 748},
       {-213, 6474, 436}, {-2273, 10140, 658}, {-3576, 12594, 686}, {-4274, 13851, 888},
       {-6245, 17291, 1147}},
      {0, 1759, 292}, {0, 7500, 1000}}};
 
-// Rows of any alignment: 128x128 tiles from half of one per unit on, below that 64x64 with four groups of
-// waves along k.  The second and the first, in us: 700 x 1001 x 1001 15.7 and 26.6, 300 x 3001 x 2001
-// 23.4 and 44.9, 1400 x 1501 x 1001 40.1 and 25.7, 2047 x 2047 x 1001 54.1 and 27.9 (a b^T; the other
-// layouts are within 10% of that).
+// Rows of any alignment, in us:
+//   a b^T in up to two 16x16 tiles a unit, a stream, against 64x64: 3 x 5 x 14001 14.5 and 94, 33 x 501 x
+//   1003 5.5 and 13.0, 16 x 8001 x 4097 (501 tiles) 23 and 32; beyond, 16 x 11001 x 4097 40 and 32,
+//   500 x 1001 x 2001 37 and 20
+//   128x128 from half a tile per unit on, against 64x64 with four groups of waves along k: 1400 x 1501 x
+//   1001 25.7 and 40.1, 2047 x 2047 x 1001 27.9 and 54.1; below, 700 x 1001 x 1001 26.6 and 15.7, 300
+//   x 3001 x 2001 44.9 and 23.4 (a b^T; the other layouts are within 10% of that)
 inline Kernel choose(int M, int N, int K, bool ka, bool kb, int cus) {
-  if (!fits_blocks(M, N, K, ka, kb))
-    return tiles_of(kAny128x128, M, N) * 2 >= cus && !tiny(M, N, K) ? kAny128x128 : kAny64x64;
+  if (!fits_blocks(M, N, K, ka, kb)) {
+    if (ka && kb && tiles_of(kAnyStream16x16, M, N) <= 2LL * cus) return kAnyStream16x16;
+    return tiles_of(kAny128x128, M, N) * 2 >= cus ? kAny128x128 : kAny64x64;
+  }
   const Prices& prices = kPrices[ka ? kb ? 0 : 1 : 2];
   const int64_t slices = ((int64_t)K + kSlice - 1) / kSlice;
   Kernel best = kAny128x128;

@@ -8,7 +8,7 @@ import pytest
 import routed_grouped_gemm_topk_amd as moe
 
 CSRC = os.path.join(os.path.dirname(moe.__file__), "csrc")
-KERNELS = ["any 64x64", "any 128x128", "stream 16x16", "stream 16x32", "32x64", "64x64", "64x128",
+KERNELS = ["any 64x64", "any 128x128", "any stream 16x16", "stream 16x16", "stream 16x32", "32x64", "64x64", "64x128",
            "128x128", "128x256", "192x192", "192x256", "256x256"]
 LAYOUTS = {"nt": (True, True), "nn": (True, False), "tn": (False, False)}
 SHIM = """
@@ -76,6 +76,8 @@ def test_launches_count_their_threads_in_32_bits(choice, m, n, k):
             groups = -(-tiles // 8) * 8
             if kernel < 2:
                 groups = min(tiles, 2 ** 21)               # the others are run by striding
+            elif kernel == 2:
+                groups = tiles
             elif KERNELS[kernel] == "256x256":             # whole tiles and halves
                 w = choice.whole(tiles, cus)
                 assert tiles < 2 ** 30
@@ -94,7 +96,7 @@ def test_offsets_of_one_tile_stay_within_31_bits(choice):
             bm, bn, _ = size_of(choice, kernel)
             a = bm * k if ka else 64 * m
             b = bn * k if kb else 64 * n
-            assert kernel < 2 or (max(a, b) * 2 < 2 ** 31), (m, n, k, name, KERNELS[kernel])
+            assert kernel < 3 or (max(a, b) * 2 < 2 ** 31), (m, n, k, name, KERNELS[kernel])
 
 
 def test_just_past_the_largest_is_refused():
@@ -107,7 +109,7 @@ def test_rows_that_are_no_whole_blocks_take_the_kernels_of_any_alignment(choice)
     for m, n, k in [(7, 8, 8), (8, 7, 8), (8, 8, 7), (2047, 2047, 2047), (1000, 1001, 1000)]:
         for ka, kb in LAYOUTS.values():
             whole = (k if ka else m) % 8 == 0 and (k if kb else n) % 8 == 0
-            assert (choice.choose_(m, n, k, ka, kb, 256) >= 2) == whole
+            assert (choice.choose_(m, n, k, ka, kb, 256) >= 3) == whole
 
 
 def test_every_kernel_is_run_by_the_gpu_tests(choice):
@@ -116,9 +118,9 @@ def test_every_kernel_is_run_by_the_gpu_tests(choice):
     allows it), with ragged tiles, a number of slices that is no multiple of the groups of waves
     along k, and more steps than stages, so that every stage is filled again."""
     from test_gpu_gemm_bf16_tiles import TILES, UNITS
-    groups = [4, 1, 8, 8, 2, 2, 1, 1, 1, 1, 1, 1]          # of waves that cut k
-    stages = [2, 2, 4, 3, 4, 3, 3, 3, 3, 3, 4, 3]
-    none = {"nt": set(), "nn": {2, 3}, "tn": {2, 3, 4}}    # kernels that the layout has not
+    groups = [4, 1, 16, 8, 8, 2, 2, 1, 1, 1, 1, 1, 1]          # of waves that cut k
+    stages = [2, 2, 4, 4, 3, 4, 3, 3, 3, 3, 3, 4, 3]
+    none = {"nt": set(), "nn": {2, 3, 4}, "tn": {2, 3, 4, 5}}    # kernels that the layout has not
     hit = set()
     for m, n, k, name in TILES:
         q = choice.choose_(m, n, k, *LAYOUTS[name], UNITS)
@@ -131,7 +133,7 @@ def test_every_kernel_is_run_by_the_gpu_tests(choice):
         for name, (ka, kb) in LAYOUTS.items():
             if q in none[name]:
                 continue
-            for rows in ("odd", "16 bytes", "even") if kb or q < 2 else ("16 bytes",):
+            for rows in ("odd", "16 bytes", "even") if kb or q < 3 else ("16 bytes",):
                 assert (q, name, rows) in hit, (kernel, name, rows)
 
 

@@ -34,7 +34,9 @@ TILES = [(3, 2, 773, "nn"), (3, 3, 773, "nn"), (3, 8, 771, "nn"), (3, 2, 796, "n
          12365, 344, "nt"), (782, 9912, 344, "nt"), (584, 13416, 328, "tn"), (779, 13440, 264,
          "nn"), (774, 13930, 288, "nt"), (1005, 10907, 264, "nt"), (1173, 9344, 272, "nt"), (6960,
          1560, 268, "tn"), (17, 9, 2640, "nt"), (17, 8, 2648, "nt"), (17, 10, 2640, "nt"), (17,
-         2085, 2672, "nt"), (17, 2056, 2672, "nt"), (17, 2068, 2640, "nt")]
+         2085, 2672, "nt"), (17, 2056, 2672, "nt"), (17, 2068, 2640, "nt"),
+         (700, 1001, 1100, "nt"), (700, 1002, 1100, "nt"), (700, 1000, 1100, "nt"),
+         (3, 3, 5301, "nt"), (19, 10, 5300, "nt"), (17, 24, 5303, "nt")]
 # 256x256 tiles whose last round runs as halves of 128 rows, the last of them with rows and without
 HALVES = [(1554, 11080, 272, "nn"), (1443, 12368, 264, "nn"), (1384, 12483, 264, "nt"), (1166,
           14501, 264, "nt"), (1544, 11208, 263, "tn"), (1224, 14216, 264, "tn")]
