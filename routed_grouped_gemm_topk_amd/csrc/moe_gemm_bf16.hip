@@ -908,7 +908,8 @@ __device__ __forceinline__ float slope(float z, int act) {
     return s * (1.0f + z * (1.0f - s));
   }
   if (act == MOE_ACT_GELU)
-    return 0.5f * (1.0f + erff(z * 0.707106781f)) + z * 0.398942280f * exp_of(fmaxf(-0.5f * z * z, -88.0f));
+    return 0.5f * (1.0f + erff(z * 0.707106781f)) +
+           z * 0.398942280f * exp_of(fmaxf(-0.5f * z * z, -88.0f));
   if (act == MOE_ACT_GELU_TANH) {
     // with s = (1 + tanh u) / 2: s + z s (1 - s) 2 u'
     const float s = sigmoid_of(gelu_tanh_arg(z));
@@ -926,8 +927,9 @@ struct ActArgs {
 };
 
 // HBM bounds it: 4096 x 14336, tanh form, with the bias 74 us, 4.8 TB/s.  A workgroup takes kActCols
-// columns, 8 a lane, and every gridDim.y-th set of rows, one of its waves each, two sets at a time.  VEC: rows are whole 16-byte blocks and a lane's columns neighbours;
-// elsewhere a lane has every 64th column.
+// columns, 8 a lane, and every gridDim.y-th set of rows, one of its waves each, two sets at a time.
+// VEC: rows are whole 16-byte blocks and a lane's columns neighbours; elsewhere a lane has every 64th
+// column.
 constexpr int kActThreads = 256, kActWaves = kActThreads / kWave;
 
 template <bool VEC>

@@ -10,8 +10,8 @@ namespace moe {
 namespace gb {
 
 enum Kernel {
-  kAny64x64, kAny128x128, kAnyStream16x16, kStream16x16, kStream16x32, kTile32x64, kTile64x64, kTile64x128,
-  kTile128x128, kTile128x256, kTile192x192, kTile192x256, kTile256x256, kKernels
+  kAny64x64, kAny128x128, kAnyStream16x16, kStream16x16, kStream16x32, kTile32x64, kTile64x64,
+  kTile64x128, kTile128x128, kTile128x256, kTile192x192, kTile192x256, kTile256x256, kKernels
 };
 
 struct TileSize {
@@ -69,17 +69,20 @@ struct Prices {
 };
 constexpr Prices kPrices[3] = {
     // a b^T
-    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {2310, 2231, 42}, {1888, 2692, 61}, {1701, 3000, 112}, {1155, 3556, 140},
+    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {2310, 2231, 42}, {1888, 2692, 61},
+      {1701, 3000, 112}, {1155, 3556, 140},
       {2656, 2315, 790}, {-325, 5585, 429}, {-3099, 9981, 640}, {-3528, 11839, 680},
       {-5239, 14066, 878}, {-7190, 18056, 1047}},
      {0, 1802, 235}, {0, 7500, 1000}},
     // a b
-    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1611, 3405, 128}, {1466, 3583, 158}, {2106, 3511, 735},
+    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1611, 3405, 128},
+      {1466, 3583, 158}, {2106, 3511, 735},
       {132, 5949, 420}, {-1141, 9202, 616}, {-1777, 10684, 682}, {-2593, 12172, 833},
       {-6485, 17865, 1066}},
      {0, 2921, 255}, {0, 7500, 1000}},
     // a^T b
-    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {1023, 4165, 180}, {3263, 3131, 748},
+    {{{0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0}, {0, 0, 0},
+      {1023, 4165, 180}, {3263, 3131, 748},
       {-213, 6474, 436}, {-2273, 10140, 658}, {-3576, 12594, 686}, {-4274, 13851, 888},
       {-6245, 17291, 1147}},
      {0, 1759, 292}, {0, 7500, 1000}}};

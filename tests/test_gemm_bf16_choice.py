@@ -1,4 +1,5 @@
-"""The choice of a bf16 product's kernel (csrc/moe_gemm_bf16_choice.h), compiled by itself for the host."""
+"""The choice of a bf16 product's kernel (csrc/moe_gemm_bf16_choice.h), compiled by itself for the
+host."""
 import ctypes
 import os
 import subprocess
@@ -8,8 +9,8 @@ import pytest
 import routed_grouped_gemm_topk_amd as moe
 
 CSRC = os.path.join(os.path.dirname(moe.__file__), "csrc")
-KERNELS = ["any 64x64", "any 128x128", "any stream 16x16", "stream 16x16", "stream 16x32", "32x64", "64x64", "64x128",
-           "128x128", "128x256", "192x192", "192x256", "256x256"]
+KERNELS = ["any 64x64", "any 128x128", "any stream 16x16", "stream 16x16", "stream 16x32", "32x64",
+           "64x64", "64x128", "128x128", "128x256", "192x192", "192x256", "256x256"]
 LAYOUTS = {"nt": (True, True), "nn": (True, False), "tn": (False, False)}
 SHIM = """
 #include "moe_gemm_bf16_choice.h"
