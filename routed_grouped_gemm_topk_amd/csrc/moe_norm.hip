@@ -170,8 +170,9 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_kern
     if (g.rstd && i == 0) g.rstd[t] = rstd;
     // n = (s p) w r with rstd = p r, p a power of two: s p is exact, and so is its product with w in
     // bf16, which leaves r's rounding and one more (s r w by itself rounds three times)
-    const float p = fmaxf(__uint_as_float(__float_as_uint(rstd) & 0x7F800000u), 0x1p-126f);
-    const double r_p = r64 / (double)p;
+    const int exponent = min(max((int)(__float_as_uint(rstd) >> 23), 1), 254);
+    const float p = __uint_as_float((uint32_t)exponent << 23);
+    const double r_p = ldexp(r64, 127 - exponent);
     #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float n[8], y[8];
