@@ -251,7 +251,7 @@ int moe_router_validate(const moe_problem* p, const moe_router* r);
  * closer than about 2^-50.  (It is made in 32 bits first, and again in 64 for a token where two
  * values that it depends on are closer than the error of that.)  Where no bias and no sum of scores
  * counts (bias NULL, and n_groups == topk_groups or group_top 1) the logits are compared, which the
- * scores keep in order.  The weights are fp32.
+ * scores keep in order.  The weights are computed in 64 bits and rounded once.
  * A logit of -inf or NaN takes its expert out: its score is 0 and it is never chosen; a bias of
  * -inf or NaN keeps it from being chosen.  A group value counts the experts that can be chosen,
  * and a group without any is not kept.  Where fewer than top_k experts can be chosen, the ids left

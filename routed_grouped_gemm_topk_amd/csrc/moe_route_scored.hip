@@ -58,9 +58,23 @@ __device__ __forceinline__ double bcast(double v, int lane) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+// A lane exchange after which groups of 2d lanes agree, if groups of d lanes did before.
+template <class F>
+__device__ __forceinline__ void exchange(int lg, F step) {
+  if (lg > 0) step([](int v) { return dpp_xchg<0xB1>(v); });      // quad_perm 1,0,3,2
+  if (lg > 1) step([](int v) { return dpp_xchg<0x4E>(v); });      // quad_perm 2,3,0,1
+  if (lg > 2) step([](int v) { return dpp_xchg<0x141>(v); });     // row_half_mirror
+  if (lg > 3) step([](int v) { return dpp_xchg<0x140>(v); });     // row_mirror
+  if (lg > 4) step([](int v) { return __shfl_xor(v, 16, kWave); });
+  if (lg > 5) step([](int v) { return __shfl_xor(v, 32, kWave); });
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
-  #pragma unroll
-  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d, kWave);
+  exchange(6, [&](auto from) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = from((int)(uint32_t)u), hi = from((int)(uint32_t)(u >> 32));
+    v += __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+  });
   return v;
 }
 
@@ -109,20 +123,39 @@ __device__ __forceinline__ int wave_top(int v) {
   return __builtin_amdgcn_readlane(v, 63);
 }
 
-// A lane exchange after which groups of 2d lanes agree, if groups of d lanes did before.
-template <class F>
-__device__ __forceinline__ void exchange(int lg, F step) {
-  if (lg > 0) step([](int v) { return dpp_xchg<0xB1>(v); });      // quad_perm 1,0,3,2
-  if (lg > 1) step([](int v) { return dpp_xchg<0x4E>(v); });      // quad_perm 2,3,0,1
-  if (lg > 2) step([](int v) { return dpp_xchg<0x141>(v); });     // row_half_mirror
-  if (lg > 3) step([](int v) { return dpp_xchg<0x140>(v); });     // row_mirror
-  if (lg > 4) step([](int v) { return __shfl_xor(v, 16, kWave); });
-  if (lg > 5) step([](int v) { return __shfl_xor(v, 32, kWave); });
+// Stores slot j of lane j < K: its id (-1: none) and its weight, from the id's logit lj.  In 64 bits, so
+// that the weight is rounded once: one evaluation a lane, but for softmax's sum over all experts.
+template <int LPL>
+__device__ __forceinline__ void store_slots(const Args& g, const Token& at, const float (&l)[LPL],
+                                            int id, float lj) {
+  double s, total = 1.0;
+  if (g.sigmoid) {
+    s = 1.0 / (1.0 + exp(-(double)lj));
+  } else {
+    float m = lj;               // the largest chosen; without renormalising the largest of all
+    if (!g.renorm) {
+      #pragma unroll
+      for (int i = 0; i < LPL; ++i) m = fmaxf(m, l[i]);
+    }
+    m = fmaxf(wave_max(m), -3.40282347e38f);
+    s = exp((double)lj - (double)m);
+    if (!g.renorm) {
+      total = 0.0;
+      #pragma unroll
+      for (int i = 0; i < LPL; ++i) total += exp((double)l[i] - (double)m);
+      total = wave_sum(total);
+    }
+  }
+  if (id < 0) s = 0.0;
+  if (g.renorm) total = wave_sum(s);
+  if (at.lane < g.K) {
+    g.ids[at.t * g.K + at.lane] = id;
+    g.w[at.t * g.K + at.lane] = total > 0.0 ? (float)(s / total * (double)g.scale) : 0.0f;
+  }
 }
 
-// The choice and the weights in fp32; returns false, having stored nothing, where fp32 does not tell
-// two experts or groups apart that the choice depends on, or has no normal number for a weight.  Every
-// lane of the wave must be active.
+// The choice in fp32; returns false, having stored nothing, where fp32 does not tell two experts or
+// groups apart that the choice depends on.  Every lane of the wave must be active.
 //
 // An expert's key is its choice score's (its logit's) ordered integer, whose last bits hold the item's
 // place in the lane, so that a lane's keys differ and the largest one names its item.  A bf16 logit
@@ -141,19 +174,16 @@ __device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const
                                            const float (&bias)[LPL]) {
   constexpr float U = 0x1p-24f;
   const bool whole_ids = !SCORES && g.bf16;
-  float m = 0.0f, inv = 1.0f, sure = 0.0f;     // sure: error of the scores of two experts
-  if (!g.sigmoid && (SCORES || !g.renorm)) {
-    m = -INFINITY;
-    #pragma unroll
-    for (int i = 0; i < LPL; ++i) m = fmaxf(m, l[i]);
-    m = wave_max(m);
-    if (m == -INFINITY) m = 0.0f;
-  }
+  float sure = 0.0f;            // error of the scores of two experts
   int key[LPL], group1 = kNoKey, group2 = kNoKey;      // the group's two largest
-  if (SCORES || (!g.sigmoid && !g.renorm)) {
-    float s[LPL];
+  if constexpr (SCORES) {
+    float s[LPL], inv = 1.0f;
     if (!g.sigmoid) {
-      float sum = 0.0f;
+      float m = -INFINITY, sum = 0.0f;
+      #pragma unroll
+      for (int i = 0; i < LPL; ++i) m = fmaxf(m, l[i]);
+      m = wave_max(m);
+      if (m == -INFINITY) m = 0.0f;
       #pragma unroll
       for (int i = 0; i < LPL; ++i) {
         s[i] = exp_diff(l[i], m);
@@ -167,15 +197,12 @@ __device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const
       for (int i = 0; i < LPL; ++i) s[i] = sigmoid_of(l[i]);
       sure = 2 * 6 * U;
     }
-    if constexpr (SCORES) {
-      #pragma unroll
-      for (int i = 0; i < LPL; ++i) {
-        const float c = s[i] * inv + bias[i];
-        key[i] = l[i] > -INFINITY && bias[i] > -INFINITY ? key_of(c) : kNoKey;
-      }
+    #pragma unroll
+    for (int i = 0; i < LPL; ++i) {
+      const float c = s[i] * inv + bias[i];
+      key[i] = l[i] > -INFINITY && bias[i] > -INFINITY ? key_of(c) : kNoKey;
     }
-  }
-  if constexpr (!SCORES) {
+  } else {
     #pragma unroll
     for (int i = 0; i < LPL; ++i) {
       const int k = key_of(l[i]);
@@ -268,39 +295,27 @@ __device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const
     const float v = __shfl(l[i], my_lane, kWave);
     if (i == item) lj = v;
   }
-  if (!here) lj = -INFINITY;
-  if (!g.sigmoid && g.renorm) m = fmaxf(wave_max(lj), -3.40282347e38f);
-  float s = !here ? 0.0f : g.sigmoid ? sigmoid_of(lj) : exp_diff(lj, m);
-  if (__ballot(here && s < 0x1p-100f)) return false;     // what fp32 rounds away may count yet
-  if (g.renorm) {
-    const float sum = wave_allreduce(s, [](float a, float b) { return a + b; });
-    inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
-  }
-  if (at.lane < g.K) {
-    g.ids[at.t * g.K + at.lane] = here ? id : -1;
-    g.w[at.t * g.K + at.lane] = here ? s * inv * g.scale : 0.0f;
-  }
+  store_slots(g, at, l, here ? id : -1, here ? lj : -INFINITY);
   return true;
 }
 
-// The same with scores, group values and weights in 64 bits (SCORES) and ties to the lowest ids.
+// The same with scores and group values in 64 bits (SCORES) and ties to the lowest ids.
 template <int LPL, bool SCORES>
 __device__ __forceinline__ void route_exact(const Args& g, const Token& at_, const float (&l)[LPL]) {
   using C = typename std::conditional<SCORES, double, float>::type;
   constexpr C NONE = -INFINITY;
   const int lane = at_.lane, grp = at_.grp, e0 = at_.e0;
-  const int64_t t = at_.t;
-  float m = 0.0f;               // softmax: the largest logit, 0 without any
-  double total = 0.0;           // softmax: the sum of exp(l - m)
-  if (!g.sigmoid && (SCORES || !g.renorm)) {
-    m = -INFINITY;
-    #pragma unroll
-    for (int i = 0; i < LPL; ++i) m = fmaxf(m, l[i]);
-    m = wave_max(m);
-    if (m == -INFINITY) m = 0.0f;
-  }
   C c[LPL];                     // choice scores
   if constexpr (SCORES) {
+    float m = 0.0f;             // softmax: the largest logit, 0 without any
+    double total = 0.0;         // softmax: the sum of exp(l - m)
+    if (!g.sigmoid) {
+      m = -INFINITY;
+      #pragma unroll
+      for (int i = 0; i < LPL; ++i) m = fmaxf(m, l[i]);
+      m = wave_max(m);
+      if (m == -INFINITY) m = 0.0f;
+    }
     #pragma unroll
     for (int i = 0; i < LPL; ++i) {
       c[i] = g.sigmoid ? 1.0 / (1.0 + exp(-(double)l[i])) : exp((double)l[i] - (double)m);
@@ -323,12 +338,6 @@ __device__ __forceinline__ void route_exact(const Args& g, const Token& at_, con
   } else {
     #pragma unroll
     for (int i = 0; i < LPL; ++i) c[i] = l[i];
-    if (!g.sigmoid && !g.renorm) {
-      float sum = 0.0f;
-      #pragma unroll
-      for (int i = 0; i < LPL; ++i) sum += expf(l[i] - m);      // 0 for a lane without the item
-      total = wave_allreduce(sum, [](float a, float b) { return a + b; });
-    }
   }
 
   if (g.kept < g.groups) {
@@ -400,27 +409,13 @@ __device__ __forceinline__ void route_exact(const Args& g, const Token& at_, con
     }
   }
 
-  // lane j: the weight of slot j, in 64 bits
-  float lj = -INFINITY;
+  float lj = -INFINITY;         // lane j: the logit of slot j
   #pragma unroll
   for (int i = 0; i < LPL; ++i) {
     const float v = __shfl(l[i], my_lane, kWave);
     if (my_id >= 0 && i == my_item) lj = v;
   }
-  double s;
-  if (g.sigmoid) {
-    s = 1.0 / (1.0 + exp(-(double)lj));
-  } else {
-    if (g.renorm) m = fmaxf(wave_max(lj), -3.40282347e38f);     // the largest chosen
-    s = exp((double)lj - (double)m);
-  }
-  if (my_id < 0) s = 0.0;
-  if (g.renorm) total = wave_sum(s);
-  if (g.renorm || !g.sigmoid) s = total > 0.0 ? s / total : 0.0;
-  if (lane < g.K) {
-    g.ids[t * g.K + lane] = my_id;
-    g.w[t * g.K + lane] = (float)(s * (double)g.scale);
-  }
+  store_slots(g, at_, l, my_id, lj);
 }
 
 // LPL: items per lane.  SCORES: scores and their sums are compared, not the logits.

@@ -1,10 +1,17 @@
 """What the operators before the layer and beside it promise of 64 bits, where 32 would not do: groups whose
-large scores cancel."""
+large scores cancel, weights of the router rounded once.
+
+Tolerances (u = 2^-24, half a step of fp32, relative; 2^-150 absolute below fp32's normal numbers):
+  * the router's weights: sums of at most 1024 terms in 64 bits, each off by a few 2^-53, stay within
+    2^-40 of the terms' magnitudes; then one rounding to fp32.
+"""
+import math
+
 import pytest
 import torch
 
 import routed_grouped_gemm_topk_amd as moe
-from test_gpu_block_operators import U32, close, ref_route
+from test_gpu_block_operators import ROUTERS, U32, WAYS, close, make_logits, ref_route, scores, weights_of
 from test_gpu_operators import gen, say
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +57,27 @@ def test_route_scored_forced_and_masked_experts(device, score, size):
             r = moe.make_router(score, True, G, kept, top)
             p = moe.make_problem(T, 64, 64, E, k, "bf16")
             same_choice(p, r, x, bias, k, (forced, k, kept, top))
+
+
+# ---------------------------------------------------------------------------------------------
+# weights of the router
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("way", WAYS, ids=str)
+@pytest.mark.parametrize("c", ROUTERS, ids=str)
+def test_route_scored_weights_rounded_once(device, c, way):
+    T, E, k, G, kept, top = c
+    p = moe.make_problem(T, 64, 64, E, k, "bf16")
+    for kind in ("plain", "ties", "holes", "far"):
+        for dtype in ("f32", "bf16"):
+            x = make_logits(c, dtype, device, kind, 1)
+            for bias in (None, 0.1 * torch.randn(E, generator=gen(device, 2), device=device)):
+                say("weights", c, way, kind, dtype, bias is None)
+                r = moe.make_router(*way, G, kept, top, 2.5)
+                ids, w = moe.route_scored(p, r, x, bias)
+                v, s = scores(x.cpu(), way[0] == "sigmoid")
+                i = ids.cpu().long()
+                if way == ("softmax", True):             # ratios of the chosen, however small
+                    m = torch.where(i >= 0, torch.gather(v, 1, i.clamp(min=0)), -math.inf).amax(1, True)
+                    s = torch.exp(v - torch.where(torch.isinf(m), 0.0, m))
+                ref = weights_of(s, i, r)
+                close(w.cpu(), ref, (U32 + 2.0 ** -40) * ref.abs() + 2.0 ** -149, "weights")
