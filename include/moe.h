@@ -276,7 +276,7 @@ int moe_route_scored(const moe_problem* p, const moe_router* router, const void*
  * used; nor are experts that a logit of -inf or NaN took out.
  * In:  logits logit_dtype [T,E]; topk_ids int32 [T,top_k]; d_weights fp32 [T,top_k]
  * Out: d_logits logit_dtype [T,E], every element written.
- * Sums in 32 bits or more, rounded once.  Deterministic.
+ * In 64 bits, rounded to fp32 (and from there to bf16) at the end.  Deterministic.
  */
 int moe_route_scored_bwd(const moe_problem* p, const moe_router* router, const void* logits,
                          int32_t logit_dtype, const int32_t* topk_ids, const float* d_weights,

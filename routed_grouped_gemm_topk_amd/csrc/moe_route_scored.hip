@@ -469,9 +469,10 @@ struct BwdArgs {
   float scale;
 };
 
-// One wavefront per token.  Lane l holds experts l, l+64, ...; lane j < K slot j, whose terms are
-// computed in 64 bits and reach the lane that holds the expert by a lane broadcast, slots in
-// ascending j, so the result does not depend on timing.
+// One wavefront per token.  Lane l holds experts l, l+64, ...; lane j < K slot j, whose terms reach the
+// lane that holds the expert by a lane broadcast, slots in ascending j, so the result does not depend on
+// timing.  All in 64 bits until the end: an expert's share and a slot's term may cancel, and an expert
+// may be named twice.
 template <int LPL>
 __global__ __launch_bounds__(kThreads) void route_scored_bwd_kernel(BwdArgs g) {
   const int lane = threadIdx.x & (kWave - 1);
@@ -486,27 +487,29 @@ __global__ __launch_bounds__(kThreads) void route_scored_bwd_kernel(BwdArgs g) {
     if ((uint32_t)id < (uint32_t)g.E) lj = load_logit(g.logits, row + id, g.bf16);
   }
   const bool chosen = lj > -INFINITY;   // an id outside [0,E) names no logit
-  float d[LPL];
+  double d[LPL];
   #pragma unroll
-  for (int i = 0; i < LPL; ++i) d[i] = 0.0f;
-  float m = 0.0f, total = 1.0f;
+  for (int i = 0; i < LPL; ++i) d[i] = 0.0;
+  float m = 0.0f;
+  double total = 1.0;
   if (!g.sigmoid && !g.renorm) {        // every expert has a share
     m = -INFINITY;
+    float l[LPL];
     #pragma unroll
     for (int i = 0; i < LPL; ++i) {
       const int e = lane + kWave * i;
-      d[i] = e < g.E ? load_logit(g.logits, row + e, g.bf16) : -INFINITY;
-      m = fmaxf(m, d[i]);
+      l[i] = e < g.E ? load_logit(g.logits, row + e, g.bf16) : -INFINITY;
+      m = fmaxf(m, l[i]);
     }
     m = wave_max(m);
     if (m == -INFINITY) m = 0.0f;
-    total = 0.0f;
+    total = 0.0;
     #pragma unroll
     for (int i = 0; i < LPL; ++i) {
-      d[i] = expf(d[i] - m);
+      d[i] = exp((double)l[i] - (double)m);
       total += d[i];
     }
-    total = wave_allreduce(total, [](float a, float b) { return a + b; });
+    total = wave_sum(total);
   } else if (!g.sigmoid) {
     m = fmaxf(wave_max(lj), -3.40282347e38f);
   }
@@ -516,7 +519,7 @@ __global__ __launch_bounds__(kThreads) void route_scored_bwd_kernel(BwdArgs g) {
     s = lj >= 0.0f ? v : u * v;
     rest = lj >= 0.0f ? u * v : v;
   } else {
-    s = exp((double)lj - (double)m) / (double)total;
+    s = exp((double)lj - (double)m) / total;
   }
   if (!chosen) s = 0.0;
   double mean = 0.0;                    // sum of the weights times their gradients
@@ -528,14 +531,14 @@ __global__ __launch_bounds__(kThreads) void route_scored_bwd_kernel(BwdArgs g) {
     term -= mean;
   } else if (!g.sigmoid) {
     mean = wave_sum(chosen ? s * (double)dw : 0.0);
-    const float share = -(float)(mean * (double)g.scale) / (total > 0.0f ? total : 1.0f);
+    const double share = total > 0.0 ? -mean * (double)g.scale / total : 0.0;
     #pragma unroll
     for (int i = 0; i < LPL; ++i) d[i] *= share;
   }
-  const float mine = chosen ? (float)(s * (double)g.scale * rest * term) : 0.0f;
+  const double mine = chosen ? s * (double)g.scale * rest * term : 0.0;
   for (int j = 0; j < g.K; ++j) {
     const int e = __builtin_amdgcn_readlane(chosen ? id : -1, j);
-    const float v = bcast(mine, j);
+    const double v = bcast(mine, j);
     #pragma unroll
     for (int i = 0; i < LPL; ++i)
       if (lane + kWave * i == e) d[i] += v;
@@ -545,9 +548,9 @@ __global__ __launch_bounds__(kThreads) void route_scored_bwd_kernel(BwdArgs g) {
     const int e = lane + kWave * i;
     if (e >= g.E) continue;
     if (g.bf16)
-      ((uint16_t*)g.d_logits)[row + e] = (uint16_t)f32_to_bf16(d[i]);
+      ((uint16_t*)g.d_logits)[row + e] = (uint16_t)f32_to_bf16((float)d[i]);
     else
-      ((float*)g.d_logits)[row + e] = d[i];
+      ((float*)g.d_logits)[row + e] = (float)d[i];
   }
 }
 

@@ -1,9 +1,10 @@
 """What the operators before the layer and beside it promise of 64 bits, where 32 would not do: groups whose
-large scores cancel, weights of the router rounded once.
+large scores cancel, weights and gradients of the router rounded once.
 
 Tolerances (u = 2^-24, half a step of fp32, relative; 2^-150 absolute below fp32's normal numbers):
-  * the router's weights: sums of at most 1024 terms in 64 bits, each off by a few 2^-53, stay within
-    2^-40 of the terms' magnitudes; then one rounding to fp32.
+  * the router's weights and the gradient of its logits: sums of at most 1024 terms in 64 bits, each off
+    by a few 2^-53, stay within 2^-40 of the terms' magnitudes; then one rounding to fp32, and for bf16
+    one more from there.
 """
 import math
 
@@ -11,7 +12,8 @@ import pytest
 import torch
 
 import routed_grouped_gemm_topk_amd as moe
-from test_gpu_block_operators import ROUTERS, U32, WAYS, close, make_logits, ref_route, scores, weights_of
+from test_gpu_block_operators import (F64, ROUTERS, U32, UBF, WAYS, close, make_logits, ref_route, scores,
+                                      weights_of)
 from test_gpu_operators import gen, say
 
 pytestmark = pytest.mark.gpu
@@ -60,7 +62,7 @@ def test_route_scored_forced_and_masked_experts(device, score, size):
 
 
 # ---------------------------------------------------------------------------------------------
-# weights of the router
+# weights and gradient of the router
 # ---------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("way", WAYS, ids=str)
 @pytest.mark.parametrize("c", ROUTERS, ids=str)
@@ -81,3 +83,65 @@ def test_route_scored_weights_rounded_once(device, c, way):
                     s = torch.exp(v - torch.where(torch.isinf(m), 0.0, m))
                 ref = weights_of(s, i, r)
                 close(w.cpu(), ref, (U32 + 2.0 ** -40) * ref.abs() + 2.0 ** -149, "weights")
+
+
+def formula_bwd(x, ids, dw, r):
+    """Gradient of the logits in 64 bits as moe.h writes it, and the magnitudes of its terms."""
+    v, s = scores(x, r.score == moe.MOE_SCORE_SIGMOID)
+    T, E = v.shape
+    ok = (ids >= 0) & (ids < E)
+    i = torch.where(ok, ids, 0).long()
+    ok = ok & (torch.gather(v, 1, i) > -math.inf)
+    dw = torch.where(ok, dw.to(F64), 0.0)
+    p = torch.where(ok, torch.gather(s, 1, i), 0.0)
+    if r.renormalize:
+        if r.score == moe.MOE_SCORE_SOFTMAX:
+            m = torch.where(ok, torch.gather(v, 1, i), -math.inf).amax(1, keepdim=True)
+            p = torch.where(ok, torch.exp(torch.gather(v, 1, i) - torch.where(torch.isinf(m), 0.0, m)), 0.0)
+        total = p.sum(1, keepdim=True)
+        p = p / torch.where(total > 0, total, 1.0)
+    mean, size = (p * dw).sum(1, keepdim=True), (p * dw).abs().sum(1, keepdim=True)
+    rest = torch.sigmoid(-torch.gather(v, 1, i)) if r.score == moe.MOE_SCORE_SIGMOID else 1.0
+    term, mag = p * rest * dw, p * rest * dw.abs()
+    if r.renormalize:
+        term, mag = term - p * rest * mean, mag + p * rest * size
+    zero = torch.zeros((T, E), dtype=F64)
+    d, m = zero.scatter_add(1, i, torch.where(ok, term, 0.0)), zero.scatter_add(1, i, mag)
+    if r.score == moe.MOE_SCORE_SOFTMAX and not r.renormalize:
+        d, m = d - s * mean, m + s * size
+    return r.scale * d, r.scale * m
+
+
+@pytest.mark.parametrize("way", WAYS, ids=str)
+@pytest.mark.parametrize("c", ROUTERS, ids=str)
+def test_route_scored_bwd_rounded_once(device, c, way):
+    T, E, k, G, kept, top = c
+    p = moe.make_problem(T, 64, 64, E, k, "bf16")
+    for kind in ("plain", "holes", "far", "twice"):
+        for dtype in ("f32", "bf16"):
+            say("route_scored_bwd", c, way, kind, dtype)
+            x = make_logits(c, dtype, device, kind, 3)
+            r = moe.make_router(*way, G, kept, top, 2.5)
+            ids = moe.route_scored(p, r, x)[0]
+            if kind == "twice":
+                ids = ids[:, :1].expand(T, k).contiguous()
+            dw = torch.randn((T, k), generator=gen(device, 4), device=device)
+            d = moe.route_scored_bwd(p, r, x, ids, dw)
+            ref, size = formula_bwd(x.cpu(), ids.cpu(), dw.cpu(), r)
+            u = U32 if dtype == "f32" else UBF + 2 * U32
+            close(d.cpu(), ref, u * ref.abs() + 2.0 ** -40 * size + 2.0 ** -133, "d_logits")
+
+
+def test_route_scored_bwd_of_tiny_scores(device):
+    """Shares down to exp(-100), which fp32 holds with few bits or none, times a scale of 2^60."""
+    T, E, k = 40, 96, 4
+    p = moe.make_problem(T, 64, 64, E, k, "bf16")
+    x = -80.0 - 20.0 * torch.rand((T, E), generator=gen(device, 142), device=device)
+    x[:, 5] = 0.0
+    r = moe.make_router("softmax", False, scale=2.0 ** 60)
+    ids = moe.route_scored(p, r, x)[0]
+    dw = torch.randn((T, k), generator=gen(device, 143), device=device)
+    d = moe.route_scored_bwd(p, r, x, ids, dw)
+    ref, size = formula_bwd(x.cpu(), ids.cpu(), dw.cpu(), r)
+    assert float(ref[:, 6:].abs().min()) > 2.0 ** -126
+    close(d.cpu(), ref, U32 * ref.abs() + 2.0 ** -40 * size, "d_logits")
