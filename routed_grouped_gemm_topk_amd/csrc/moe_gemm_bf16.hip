@@ -44,9 +44,30 @@ __device__ __forceinline__ float sigmoid_of(float z) {
   return z < -88.0f ? 0.0f : s;
 }
 
+// The part of a normal distribution below -a is exp(-a^2 / 2) times this, 10 u off for 0 <= a <= 14, so
+// that GELU does not cancel below 0 as 1 + erf does (z = -5: one digit left).  (a + 4.75) times it is a
+// polynomial in (a - 4.75) / (a + 4.75), the variable of Shepherd and Laframboise (1981), fitted to the
+// least relative error (0.24 u); beyond 14 the exponential is 0.
+__device__ __forceinline__ float tail_ratio(float a) {
+  const float w = __builtin_amdgcn_rcpf(a + 4.75f), q = __builtin_fmaf(w, -9.5f, 1.0f);
+  float p = -1.304180477745831e-3f;
+  p = __builtin_fmaf(p, q, 2.3066371795721352e-4f);
+  p = __builtin_fmaf(p, q, 1.1544439941644669e-2f);
+  p = __builtin_fmaf(p, q, -5.0630372017621994e-2f);
+  p = __builtin_fmaf(p, q, 0.13810624182224274f);
+  p = __builtin_fmaf(p, q, -0.28418365120887756f);
+  p = __builtin_fmaf(p, q, 0.4720644950866699f);
+  p = __builtin_fmaf(p, q, -0.6535893678665161f);
+  return w * __builtin_fmaf(p, q, 0.7664163112640381f);
+}
+__device__ __forceinline__ float bell(float z) { return exp_of(fmaxf(-0.5f * z * z, -88.0f)); }
+
 __device__ __forceinline__ float activate(float z, int act) {
   if (act == MOE_ACT_SILU) return z * sigmoid_of(z);
-  if (act == MOE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.707106781f));
+  if (act == MOE_ACT_GELU) {
+    const float a = fminf(fabsf(z), 14.0f), tail = bell(z) * tail_ratio(a);
+    return z < 0.0f ? z * tail : z - a * tail;
+  }
   // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
   if (act == MOE_ACT_GELU_TANH) return z * sigmoid_of(gelu_tanh_arg(z));
   return z;
@@ -908,9 +929,10 @@ __device__ __forceinline__ float slope(float z, int act) {
     const float s = sigmoid_of(z);
     return s * (1.0f + z * (1.0f - s));
   }
-  if (act == MOE_ACT_GELU)
-    return 0.5f * (1.0f + erff(z * 0.707106781f)) +
-           z * 0.398942280f * exp_of(fmaxf(-0.5f * z * z, -88.0f));
+  if (act == MOE_ACT_GELU) {            // cdf + z phi
+    const float a = fabsf(z), below = bell(z) * __builtin_fmaf(a, -0.398942280f, tail_ratio(a));
+    return z < 0.0f ? below : 1.0f - below;
+  }
   if (act == MOE_ACT_GELU_TANH) {
     // with s = (1 + tanh u) / 2: s + z s (1 - s) 2 u'
     const float s = sigmoid_of(gelu_tanh_arg(z));

@@ -1,10 +1,14 @@
 """What the operators before the layer and beside it promise of 64 bits, where 32 would not do: groups whose
-large scores cancel, weights and gradients of the router rounded once.
+large scores cancel, weights and gradients of the router rounded once; and GELU far below 0.
 
 Tolerances (u = 2^-24, half a step of fp32, relative; 2^-150 absolute below fp32's normal numbers):
   * the router's weights and the gradient of its logits: sums of at most 1024 terms in 64 bits, each off
     by a few 2^-53, stay within 2^-40 of the terms' magnitudes; then one rounding to fp32, and for bf16
     one more from there.
+  * GELU and its slope: the part of a normal distribution below -|z| is a ratio of at most 10 u times an
+    exponential, 3 u and, where z is no bf16 value, z^2 / 2 u for the rounding of its argument; two
+    products more, and above 0 a difference from at least twice as much: (z^2 / 2 + 16) u.  A slope's other
+    part, z phi(z): 8 u.  Exponentials below 2^-126 count as 0: at most 14 of them.
 """
 import math
 
@@ -12,7 +16,7 @@ import pytest
 import torch
 
 import routed_grouped_gemm_topk_amd as moe
-from test_gpu_block_operators import (F64, ROUTERS, U32, UBF, WAYS, close, make_logits, ref_route, scores,
+from test_gpu_block_operators import (F64, ROUTERS, TD, U32, UBF, WAYS, close, make_logits, ref_route, scores,
                                       weights_of)
 from test_gpu_operators import gen, say
 
@@ -145,3 +149,45 @@ def test_route_scored_bwd_of_tiny_scores(device):
     ref, size = formula_bwd(x.cpu(), ids.cpu(), dw.cpu(), r)
     assert float(ref[:, 6:].abs().min()) > 2.0 ** -126
     close(d.cpu(), ref, U32 * ref.abs() + 2.0 ** -40 * size, "d_logits")
+
+
+# ---------------------------------------------------------------------------------------------
+# GELU below 0
+# ---------------------------------------------------------------------------------------------
+TINY = 2.0 ** -126
+
+
+@pytest.mark.parametrize("m,n", [(1, 4096), (1, 4095), (70, 1000), (300, 8192)])
+def test_gelu_keeps_its_digits_below_zero(device, m, n):
+    z = torch.linspace(-13, 13, n, device=device)
+    z[n // 2] = 0
+    a, b = (torch.zeros(s, device=device).bfloat16() for s in ((m, 8), (n, 8)))
+    z64 = z.to(F64)
+    ref = 0.5 * z64 * torch.erfc(-z64 * math.sqrt(0.5))
+    tol = (z64 * z64 / 2 + 16) * U32 * ref.abs() + TINY
+    for dtype in ("f32", "bf16"):
+        say("gelu", m, n, dtype)
+        c = moe.gemm_bf16(a, b, bias=z, act="gelu", out_dtype=TD[dtype])
+        close(c, ref.expand(m, n), (tol + (UBF * ref.abs() if dtype == "bf16" else 0)).expand(m, n), "gelu")
+
+
+def test_gelu_of_far_and_special_values(device):
+    z = torch.tensor([-1e38, -1e19, -1e4, -200.0, -30.0, -14.5, 0.0, 14.5, 1e4, 1e19, 1e38, math.inf, math.nan],
+                     device=device)
+    a, b = (torch.zeros(s, device=device).bfloat16() for s in ((2, 8), (z.numel(), 8)))
+    c = moe.gemm_bf16(a, b, bias=z, act="gelu", out_dtype=torch.float32)
+    ref = torch.where(z < 0, 0.0, z).to(F64)
+    close(c, ref.expand(2, -1), TINY, "gelu")
+
+
+def test_gelu_slope_keeps_its_digits_below_zero(device):
+    """A row of d_c of ones: d_bias is the slope itself, in fp32."""
+    z = torch.linspace(-13, 13, 8191, device=device).bfloat16()
+    z64 = z.to(F64)
+    cdf = 0.5 * torch.erfc(-z64 * math.sqrt(0.5))
+    tail = z64 * torch.exp(-0.5 * z64 * z64) / math.sqrt(2 * math.pi)
+    ref = cdf + tail
+    tol = (16 * cdf + 8 * tail.abs() + ref.abs()) * U32 + 16 * TINY
+    dz, db = moe.act_bwd(torch.ones_like(z)[None], z[None], "gelu", d_bias=True)
+    close(db, ref, tol, "slope")
+    close(dz[0], ref, tol + UBF * ref.abs(), "d_z")
