@@ -248,17 +248,20 @@ int moe_router_validate(const moe_problem* p, const moe_router* r);
  *   topk_weights[t, j] = scale * s_e of that expert (without the bias), divided by the sum of s
  *   over the chosen ones when renormalize != 0 (0 where that sum is 0)
  * The choice is that of scores, group values and sums in 64 bits: of exact arithmetic but for values
- * closer than about 2^-50.  (It is made in 32 bits first, and again in 64 for a token where two
- * values that it depends on are closer than the error of that.)  Where no bias and no sum of scores
- * counts (bias NULL, and n_groups == topk_groups or group_top 1) the logits are compared, which the
- * scores keep in order.  The weights are computed in 64 bits and rounded once.
+ * closer than about 2^-50 of the largest score or bias in them.  (It is made in 32 bits first, and
+ * again in 64 for a token where two values that it depends on are closer than the error of that.)
+ * Where no bias and no sum of scores counts (bias NULL, and n_groups == topk_groups or group_top 1)
+ * the logits are compared, which the scores keep in order.  The weights are computed in 64 bits and
+ * rounded once.
  * A logit of -inf or NaN takes its expert out: its score is 0 and it is never chosen; a bias of
  * -inf or NaN keeps it from being chosen.  A group value counts the experts that can be chosen,
  * and a group without any is not kept.  Where fewer than top_k experts can be chosen, the ids left
  * over are -1 (excluded by moe_align) with weight 0.  +inf counts as the largest finite logit.
  * In:  logits       logit_dtype (MOE_F32 or MOE_BF16) [T, E];  bias fp32 [E] or NULL
  * Out: topk_ids     int32 [T, top_k];  topk_weights fp32 [T, top_k].
- * Of the problem T, E and top_k count.  Deterministic.
+ * Of the problem only T, E and top_k are used, but all of it has to be valid as moe_validate has it: H
+ * and I multiples of 64, T * H < 2^31 (so T < 2^25), its weights' and grids' limits; a router that
+ * stands alone gives H = I = 64 and block_m 16.  Deterministic.
  */
 int moe_route_scored(const moe_problem* p, const moe_router* router, const void* logits,
                      int32_t logit_dtype, const float* bias, int32_t* topk_ids,

@@ -375,7 +375,8 @@ hipError_t launch_rms_norm(int T, int H, bool bf16, const void* x, const void* r
 hipError_t launch_rms_norm_bwd(int T, int H, bool bf16, const void* d_y, const void* d_sum,
                                const void* sum, const void* weight, const float* rstd, void* d_x,
                                float* d_weight, float* partials, hipStream_t s);
-// out[c] = sum over r < rows, ascending, of partials[r, c].
+// out[c] = sum over r < rows of partials[r, c]: 16 neighbouring stretches of ceil(rows / 16) rows, each in
+// ascending order (eight at a time are loaded, and added one after the other), then the stretches in theirs.
 hipError_t launch_sum_rows(int rows, int cols, const float* partials, float* out, hipStream_t s);
 // bf16 products with an epilogue and the epilogue's gradient (moe_gemm_bf16.hip).
 constexpr int kMaxUnits = 1024;     // compute units that a launch counts on, at most

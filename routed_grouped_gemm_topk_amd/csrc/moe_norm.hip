@@ -13,7 +13,8 @@
 // Measured, operands from memory: forward, residual to rows and codes, bf16, 2048 x 7168 29.6 us (4.5
 // TB/s) and 16384 x 7168 190 us (5.6 TB/s, more than a copy's 5.0, since reads outweigh writes); 2001
 // x 2880 fp32 20.9 us (4.4 TB/s); one row of 7168 4.3 us, a launch's own time and one round trip to
-// memory.  Backward with the weight's gradient 4096 x 4096 bf16 34.4 us (3.9 TB/s), 1000 x 12288 43 us.
+// memory.  Backward with the weight's gradient, bf16, 4096 x 4096 34.4 us (3.9 TB/s); 1000 x 12288 43 us
+// (2.3 TB/s; the bytes at a copy's rate: 19.5), whose registers leave two waves a SIMD.
 #include <algorithm>
 #include <type_traits>
 
@@ -230,7 +231,7 @@ struct BwdArgs {
 
 // A workgroup takes every gridDim.x-th set of rows and keeps its part of d_w in registers; its rows
 // (one per wave where TPR is a wave) are added through LDS at the end, then one row of partials.
-// Up to 16 values a thread, the rows stay in registers and the next ones are on
+// Up to 16 words of a row a thread (32 values of bf16), rows stay in registers and the next ones are on
 // their way while a row's sum goes round (4096 x 4096: 42.5 -> 34.5 us).  Longer ones are loaded again,
 // from the caches, once the sum is known.
 template <int TPR, int NV, bool BF16, bool VEC>

@@ -10,10 +10,10 @@
 // groups item i of lane l is expert l + 64 i.
 //
 // Instructions bound it, not memory: one round of the choice after another, each a maximum over the wave
-// and what takes its expert out (sigmoid, bias, 8 of 256 out of 4 of 8 groups: some 540 vector
-// instructions a token; with everything in 64 bits, as route_exact has it, three times as many).  8192
-// such tokens take 13.5 us, 64 of them 5.4 us, one launch's time and one wave's chain; 8192 tokens of
-// softmax, 6 of 64, bf16 6.4 us.  Backward: 4001 x 256 4.2 us (the bytes: 1.6 us).
+// and what takes its expert out (sigmoid, bias, 8 of 256 out of 4 of 8 groups: some 620 vector
+// instructions a token, 85 more than with weights in fp32).  8192 such tokens take 14.5 us, 69 us
+// where all of them need the choice in 64 bits too; 64 of them 5.7 us, one launch's time and one wave's
+// chain; 8192 tokens of softmax, 6 of 64, bf16 7.1 us.  Backward: 4001 x 256 5.5 us (the bytes: 1.6 us).
 #include <type_traits>
 
 #include "moe_route.h"
