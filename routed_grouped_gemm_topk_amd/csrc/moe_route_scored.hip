@@ -167,8 +167,8 @@ __device__ __forceinline__ void store_slots(const Args& g, const Token& at, cons
 // score c another u |c| for the addition of the bias and 2 LPL u |c| for the bits given up; a sum of
 // two the errors of both and its own.  Two that differ by more than both errors are in the right
 // order.  An expert's error grows with its own value alone, so neighbours in the order speak for all
-// below them; a sum's does not (large scores may cancel), so the last group kept and the first one that is
-// not are held to the largest error of any group.
+// below them; a sum's does not (large scores may cancel), so every group is held to its own error, away
+// from the middle between the last one kept and the first one that is not.
 template <int LPL, bool SCORES>
 __device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const float (&l)[LPL],
                                            const float (&bias)[LPL]) {
@@ -238,10 +238,13 @@ __device__ __forceinline__ bool route_fast(const Args& g, const Token& at, const
     const uint64_t out = __ballot(first && before == g.kept);
     if (__popcll(in) != 1 || __popcll(out) != 1) return false;
     const int a = __builtin_ctzll(in), b = __builtin_ctzll(out);
-    const float size = SCORES && g.top == 2 ? wave_max(two ? fabsf(v1) + fabsf(v2) : 0.0f) : 0.0f;
     const int va = __builtin_amdgcn_readlane(value, a), vb = __builtin_amdgcn_readlane(value, b);
-    if (!whole_ids && vb != kNoKey)
-      ok = apart(of_key(va), of_key(vb), 2 * sure + 8 * U * size, 2);
+    if (SCORES && vb != kNoKey) {
+      const float border = 0.5f * of_key(va) + 0.5f * of_key(vb), v = of_key(value);
+      const float err = sure + 4 * U * (fabsf(v1) + (two ? fabsf(v2) : 0.0f));
+      const bool clear = value == kNoKey || (before < g.kept ? v - err > border : v + err < border);
+      ok = __ballot(first && !clear) == 0;
+    }
     if (before >= g.kept) {
       #pragma unroll
       for (int i = 0; i < LPL; ++i) key[i] = kNoKey;
