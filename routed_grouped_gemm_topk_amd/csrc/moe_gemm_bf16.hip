@@ -949,10 +949,10 @@ struct ActArgs {
   int M, N, act;
 };
 
-// HBM bounds it: 4096 x 14336, tanh form, with the bias 74 us, 4.8 TB/s (GELU 75 to 84).  A workgroup takes kActCols
-// columns, 8 a lane, and every gridDim.y-th set of rows, one of its waves each, two sets at a time.
-// VEC: rows are whole 16-byte blocks and a lane's columns neighbours; elsewhere a lane has every 64th
-// column.
+// HBM bounds it: 4096 x 14336, tanh form, with the bias 74 us, 4.8 TB/s (GELU 75 to 84).  A workgroup
+// takes kActCols columns, 8 a lane, and every gridDim.y-th set of rows, one of its waves each, two sets at
+// a time.  VEC: rows are whole 16-byte blocks and a lane's columns neighbours; elsewhere a lane has every
+// 64th column.
 constexpr int kActThreads = 256, kActWaves = kActThreads / kWave;
 
 template <bool VEC>

@@ -232,8 +232,8 @@ struct BwdArgs {
 // A workgroup takes every gridDim.x-th set of rows and keeps its part of d_w in registers; its rows
 // (one per wave where TPR is a wave) are added through LDS at the end, then one row of partials.
 // Up to 16 words of a row a thread (32 values of bf16), rows stay in registers and the next ones are on
-// their way while a row's sum goes round (4096 x 4096: 42.5 -> 34.5 us).  Longer ones are loaded again,
-// from the caches, once the sum is known.
+// their way while a row's sum goes round (4096 x 4096: 42.5 -> 34.5 us).  Longer ones, and those of 1024
+// threads, are loaded again, from the caches, once the sum is known.
 template <int TPR, int NV, bool BF16, bool VEC>
 __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void rms_norm_bwd_kernel(BwdArgs g) {
   constexpr int ROWS = TPR < kThreads ? kThreads / TPR : 1;
